@@ -88,10 +88,12 @@ typedef enum {
   TB_ERR_LAUNCH = 6,      /* the HIP runtime refused the launch                 */
   TB_ERR_UNSUPPORTED = 7, /* valid request this build does not implement        */
   TB_ERR_ALIAS = 8,       /* input and output overlap where that is not allowed */
-  TB_ERR_WORKSPACE = 9    /* workspace missing or smaller than the call needs   */
+  TB_ERR_WORKSPACE = 9,   /* workspace missing or smaller than the call needs   */
+  TB_ERR_VALUE = 10       /* a scalar argument (scale, eps) outside its range   */
 } tb_status;
 
-typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_ACT8 = 2 } tb_dtype;
+/* TB_FP8 (OCP e4m3) is a dtype of the paged cache only. */
+typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_ACT8 = 2, TB_FP8 = 3 } tb_dtype;
 /* Quantiser rules and storage formats.  TB_FMT_DENSE_MINERR stores the dense
  * format; only the threshold and scale rule differ (tb_quantize_pack).
  * TB_FMT_DENSE_RESID stores two dense planes with their 128-groups
@@ -508,6 +510,231 @@ TB_API tb_status tb_ternary_gemm_splitk(const uint16_t* x, int64_t M, const uint
 TB_API tb_status tb_ternary_gemm_rotated(const uint16_t* x, int64_t M, const uint32_t* codes, const uint16_t* scales,
                                   int64_t N, int64_t K, void* y, int y_dtype, float* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Serving operators around the products: the boundary between two blocks of
+ * a decoder layer, the paged key/value cache, the attention of a chunk of
+ * new tokens over it, and the verification of drafted tokens.  The five
+ * pages cited above stop at the products; these operators are written from
+ * the formulas given with each.
+ * ------------------------------------------------------------------------ */
+
+/* Longest row tb_block_norm takes (a workgroup holds a row in registers). */
+#define TB_NORM_MAX_C 32768
+
+/*
+ * Arguments of tb_block_norm.  For each row r of C channels:
+ *   u = sum_p y[p][r]                        (parts in order, fp32)
+ *   u = R u                  if rotate_in    (R: the 128-blocks' orthonormal
+ *                                             Walsh-Hadamard transform)
+ *   u = u / sqrt(mean(u^2) + eps) * w_post   if w_post
+ *   h = resid[r] + alpha * gate[r / rows_per_gate] * u     (no gate: 1; no resid: 0)
+ *   z = h / sqrt(mean(h^2) + eps) * w_pre,  z = R z if rotate_out
+ * All of it in fp32; h and z are rounded once, z is computed from the
+ * unrounded h.
+ *   y       [parts][rows][C] in y_dtype (TB_F32 or TB_BF16; parts > 1 only
+ *           with TB_F32, at most TB_MAX_PARTS; 0 is read as 1), as the products
+ *           write it (rotate_in takes their rotated basis back).  NULL: the
+ *           boundary has no block before it (h = resid, which must then be
+ *           given; w_post, gate and rotate_in are not used)
+ *   resid   [rows][C] in h_dtype, or NULL
+ *   h       [rows][C] in h_dtype, or NULL (not wanted); h == resid is
+ *           allowed (in place)
+ *   w_post, w_pre   [C] in w_dtype; w_pre may be NULL only when z is
+ *   gate    [ceil(rows / rows_per_gate)][C] in gate_dtype, or NULL;
+ *           rows_per_gate >= 1 (1: a gate for each row; rows: one for all)
+ *   z       [rows][C] in z_dtype, or NULL: TB_F32, TB_BF16 or TB_ACT8 (the
+ *           rounded bf16 result as the operand of tb_ternary_gemv)
+ *   C a positive multiple of 128, at most TB_NORM_MAX_C; rows >= 0; alpha
+ *   finite, eps finite and > 0 (else TB_ERR_VALUE).
+ * Every output overlaps no other argument, h == resid excepted.
+ */
+typedef struct {
+  const void* y;
+  const void* resid;
+  const void* w_post;
+  const void* w_pre;
+  const void* gate;
+  void* h;
+  void* z;
+  int64_t rows;
+  int64_t C;
+  int64_t rows_per_gate;
+  int parts;
+  int y_dtype;
+  int h_dtype;
+  int w_dtype;
+  int gate_dtype;
+  int z_dtype;
+  int rotate_in;
+  int rotate_out;
+  float alpha;
+  float eps;
+} tb_block_norm_args;
+
+/* The norms after one block and before the next, with the gate, residual
+ * scale, residual and rotations between them, in one launch. */
+TB_API tb_status tb_block_norm(const tb_block_norm_args* args, void* stream);
+
+/*
+ * The paged key/value cache.  A pool of n_pages pages of `page` positions
+ * (a power of two, 16 to 1024) for heads_kv heads of head_dim (64 or 128):
+ *   k_cache  [n_pages][heads_kv][page][head_dim]
+ *   v_cache  [n_pages][heads_kv][head_dim][page]  (positions along the fast
+ *            axis: the operand order of the product with the weights)
+ * in cache_dtype: TB_BF16, or TB_FP8 (OCP e4m3) standing for code *
+ * k_scale[head] (v_scale[head]; fp32 [heads_kv], NULL: 1).
+ * Sequence b of B holds kv_len[b] positions, its new tokens among them; the
+ * page of position x is block_table[b * table_stride + x / page], of
+ * table_width entries.  Its new tokens are rows cu_q[b] .. cu_q[b + 1] - 1 of
+ * the token arrays (cu_q [B + 1]), at the last positions: with n of them, token
+ * j is at position kv_len[b] - n + j.
+ * cu_q, kv_len and block_table are read on the device, so a wrong entry is
+ * not refused but kept from harm there: cu_q is clamped to [0, total_q] and to
+ * rise, a position outside the table or on a page id outside [0, n_pages)
+ * does not exist (nothing is written to it, no key is read from it), a token
+ * at a negative position has none.
+ */
+#define TB_MAX_PAGE 1024
+#define TB_MAX_TOKENS ((int64_t)1 << 27)               /* total_q and max_q              */
+#define TB_MAX_ROWS ((int64_t)1 << 27)                 /* max_q * heads_q of an attention */
+
+typedef struct {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int64_t n_pages;
+  int64_t table_stride;
+  int64_t table_width;
+  int64_t B;
+  int64_t total_q;  /* rows of the token arrays                                  */
+  int64_t max_q;    /* at least every sequence's new tokens: those past it are
+                       not computed (attention) or written (append)              */
+  int cache_dtype;
+  int page;
+  int heads_kv;
+  int head_dim;
+} tb_paged_cache;
+
+/*
+ * Write the new tokens' keys and values into the cache: bf16 k, v
+ * [total_q][heads_kv][head_dim], k_stride and v_stride elements between
+ * tokens (a slice of a fused projection's output; multiples of 8, at least
+ * heads_kv * head_dim).  TB_FP8: the nearest e4m3 value (ties to even) of
+ * x / scale, at most 448 in magnitude; NaN stays NaN.  One launch; positions
+ * other than the new tokens' are left as they are.
+ */
+TB_API tb_status tb_paged_append(const tb_paged_cache* cache, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over its cached positions (their
+ * own among them: tb_paged_append first).  For token j at position x = kv_len
+ * - n + j and query head i (key/value head i / (heads_q / heads_kv)):
+ *   s_y = scale * q . k_y            for y <= x, and y > x - window if window > 0
+ *   out = sum_y exp(s_y) v_y / sum_y exp(s_y),   lse = ln sum_y exp(s_y)
+ * A token that sees no position gets out 0 and lse -inf.  What lies at
+ * positions that a token does not see, NaN and infinities included, does not
+ * reach it; pages that no token of the sequence sees are not read, so they
+ * may be given away (their table entries may hold anything).
+ *   q       bf16 [total_q][heads_q][head_dim], q_stride elements between
+ *           tokens (a multiple of 8, at least heads_q * head_dim)
+ *   out     [total_q][heads_q][head_dim], contiguous, out_dtype TB_BF16 or
+ *           TB_F32; rows of no sequence are left as they are
+ *   lse     fp32 [total_q][heads_q], or NULL
+ *   heads_q a multiple of heads_kv, max_q * heads_q at most TB_MAX_ROWS; window >= 0; scale finite (TB_ERR_VALUE)
+ *   max_kv  the most positions a sequence is likely to hold: it only decides
+ *           how far the positions are split over workgroups
+ *   workspace, workspace_bytes  device memory, 16-byte aligned, for the parts
+ *           of split sequences (tb_paged_attention_workspace bytes); with less
+ *           or NULL the positions are not split.  Calls sharing a workspace
+ *           must be ordered on one stream.
+ * Products of bf16 (e4m3 widened exactly) accumulate in fp32; softmax
+ * statistics are fp32.  Results do not change between equal calls.
+ */
+typedef struct {
+  tb_paged_cache cache;
+  const void* q;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t q_stride;
+  int64_t max_kv;
+  int64_t window;
+  int heads_q;
+  int out_dtype;
+  float scale;
+  int reserved;  /* must be 0 */
+} tb_paged_attention_args;
+
+/* Workspace bytes of tb_paged_attention for these arguments (pointers, and
+ * the workspace itself, are not looked at).  Host-only; 0 when none is used or
+ * the arguments are invalid. */
+TB_API size_t tb_paged_attention_workspace(const tb_paged_attention_args* args);
+
+TB_API tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream);
+
+/*
+ * Verification of drafted tokens (speculative decoding) from given random
+ * numbers.  Sequence b has T = cu_draft[b + 1] - cu_draft[b] drafted tokens d_j
+ * (T = 0: plain sampling), the drafter's probabilities q_j they were drawn from
+ * and the target's p_0 .. p_T:
+ *   token j is kept while u_j * q_j(d_j) < p_j(d_j), for j = 0, 1, ...
+ *   accepted = the number kept, m.  One more token is drawn from the weights
+ *   w = max(p_m - q_m, 0) (p_m if m = T, or if that leaves nothing): the lowest
+ *   v with w_0 + .. + w_v > u_next * sum(w).
+ * Weights that are not positive and finite count as 0.  Products, differences
+ * and sums are in 64 bits.
+ *   p       [total + B][vocab] in p_dtype (TB_F32 or TB_BF16), p_stride >= vocab
+ *           elements between rows; sequence b's rows start at cu_draft[b] + b
+ *   q       [total][vocab] in q_dtype, q_stride; NULL: the drafter is certain
+ *           (q_j is 1 at d_j and 0 elsewhere)
+ *   drafts  int32 [total]; an id outside [0, vocab) is not kept
+ *   u       fp32 [total] in [0, 1); u_next fp32 [B] in [0, 1)
+ *   cu_draft  int32 [B + 1]; read on the device, clamped to [0, total] and to
+ *           rise
+ *   max_draft  at least every T (later drafts are not looked at), 0 to
+ *           TB_MAX_DRAFT
+ *   accepted  int32 [B]
+ *   tokens  int32 [B][max_draft + 1]: the kept tokens, the drawn one, then -1
+ *           (the drawn one is -1 too if no weight of p_m is positive and finite)
+ *   workspace  tb_verify_draft_workspace(B, vocab) bytes of device memory,
+ *           16-byte aligned
+ * p, q, u, drafts need only their elements' alignment.
+ */
+#define TB_MAX_DRAFT 64
+
+typedef struct {
+  const void* p;
+  const void* q;
+  const int32_t* drafts;
+  const float* u;
+  const float* u_next;
+  const int32_t* cu_draft;
+  int32_t* accepted;
+  int32_t* tokens;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t B;
+  int64_t total;
+  int64_t vocab;
+  int64_t p_stride;
+  int64_t q_stride;
+  int max_draft;
+  int p_dtype;
+  int q_dtype;
+  int reserved;  /* must be 0 */
+} tb_verify_draft_args;
+
+/* Workspace bytes of tb_verify_draft.  Host-only; 0 for invalid sizes. */
+TB_API size_t tb_verify_draft_workspace(int64_t B, int64_t vocab);
+
+TB_API tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream);
 
 #ifdef __cplusplus
 }

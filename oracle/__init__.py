@@ -27,10 +27,11 @@ Modules
 ``matvec``    the ternary GEMV / GEMM / 2:4 GEMV / two-plane GEMV definitions
               (dequantise, then a float64 matmul) and brute-force loop versions.
 ``bits``      bits-per-weight ledger and packed buffer sizes.
+``serving``   block boundary, paged cache and attention, draft verification.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, library routines or brute force; none is "parity
 unpinned".
 """
 
-from . import bits, hadamard, matvec, numerics, quant  # noqa: F401
+from . import bits, hadamard, matvec, numerics, quant, serving  # noqa: F401

@@ -1,0 +1,132 @@
+// What the attention kernels share: operand conversions, the softmax
+// statistics' helpers, and the product with values that may not be finite.
+#pragma once
+
+#include "paged.h"
+#include "tb_common.h"
+
+namespace tb {
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x in the lane's row of 16 lanes, combined with the other rows': v[lane ^ 16] and v[lane ^ 32]
+__device__ __forceinline__ float max_over_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ __forceinline__ float sum_over_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// 8 e4m3 bytes widened to bf16 / fp16: both hold every e4m3 value exactly
+__device__ __forceinline__ bf16x8 fp8_to_bf16(const u32x2& w) {
+  bf16x8 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true);
+    r[4 * i] = a[0];
+    r[4 * i + 1] = a[1];
+    r[4 * i + 2] = b[0];
+    r[4 * i + 3] = b[1];
+  }
+  return r;
+}
+
+__device__ __forceinline__ f16x8 fp8_to_f16(const u32x2& w) {
+  f16x8 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, true);
+    r[4 * i] = a[0];
+    r[4 * i + 1] = a[1];
+    r[4 * i + 2] = b[0];
+    r[4 * i + 3] = b[1];
+  }
+  return r;
+}
+
+// Values that are not finite must reach only the tokens that see their
+// position, and a matrix instruction multiplies every value with every token's
+// weight, 0 where the token does not see it.  In the rare tile where both
+// occur the values go in with these elements replaced by 0, and whether a
+// token sees a +inf (or NaN), a -inf (or NaN) is counted by two more products
+// with 1 in those places.
+template <typename V8>
+struct SplitValues {
+  V8 finite, up, down;
+};
+
+__device__ __forceinline__ SplitValues<bf16x8> split_values(const bf16x8& v) {
+  SplitValues<bf16x8> r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = (float)v[e];
+    const bool fin = fabsf(f) < __builtin_inff();
+    r.finite[e] = fin ? v[e] : (__bf16)0.f;
+    r.up[e] = (__bf16)(!fin && !(f < 0.f) ? 1.f : 0.f);
+    r.down[e] = (__bf16)(!fin && !(f > 0.f) ? 1.f : 0.f);
+  }
+  return r;
+}
+
+__device__ __forceinline__ SplitValues<f16x8> split_values(const f16x8& v) {
+  SplitValues<f16x8> r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = (float)v[e];
+    const bool fin = fabsf(f) < __builtin_inff();
+    r.finite[e] = fin ? v[e] : (_Float16)0.f;
+    r.up[e] = (_Float16)(!fin && !(f < 0.f) ? 1.f : 0.f);
+    r.down[e] = (_Float16)(!fin && !(f > 0.f) ? 1.f : 0.f);
+  }
+  return r;
+}
+
+// what the counts of seen infinities and NaN add to a sum: +inf - inf is NaN
+__device__ __forceinline__ float nonfinite_sum(float up, float down) {
+  return (up > 0.f ? __builtin_inff() : 0.f) + (down > 0.f ? -__builtin_inff() : 0.f);
+}
+
+// any element of 8 bf16 (four words) infinite or NaN
+__device__ __forceinline__ bool any_nonfinite_bf16(const u32x4& w) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
+
+// any of 16 e4m3 bytes NaN (0x7f or 0xff; e4m3 has no infinity)
+__device__ __forceinline__ bool any_nonfinite_fp8(const u32x4& w) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad = bad || ((w[i] >> (8 * e)) & 0x7fu) == 0x7fu;
+  return bad;
+}
+
+// One part of a row of a split sequence in the workspace: its sums, then the
+// weighted values, each part of all rows after the other:
+//   stats  float2 [parts][rows]     (maximum in log2 units, sum)
+//   values float  [parts][rows][D]  (not divided by the sum)
+struct AttnParts {
+  float2* stats;
+  float* values;
+  int64_t rows;
+};
+
+}  // namespace tb

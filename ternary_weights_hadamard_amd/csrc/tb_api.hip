@@ -7,28 +7,16 @@
 #include <mutex>
 
 #include "tb.h"
+#include "tb_check.h"
 #include "tb_launch.h"
+
+using namespace tb;
 
 namespace {
 
 constexpr int64_t kGroup = 128;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool dims_ok(int64_t N, int64_t K) { return N > 0 && K > 0 && N % kGroup == 0 && K % kGroup == 0; }
-bool dtype_ok(int d) { return d == TB_F32 || d == TB_BF16; }
-size_t dtype_bytes(int d) { return d == TB_F32 ? 4 : 2; }
-// bytes of the act8 operand of `elems` activations (4 per element + 1/8 of scales)
-size_t act8_bytes(size_t elems) { return elems * 4 + elems / 8; }
-
-// [a, a + na) and [b, b + nb) intersect (byte ranges)
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return na && nb && pa < pb + nb && pb < pa + na;
-}
-
-tb_status launched(hipError_t e) { return e == hipSuccess ? TB_OK : TB_ERR_LAUNCH; }
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // byte sizes of one FWHT segment's input and output
 size_t fwht_in_bytes(int64_t rows, int64_t K, int x_dtype) { return (size_t)rows * (size_t)K * dtype_bytes(x_dtype); }
@@ -188,6 +176,7 @@ const char* tb_status_string(int status) {
     case TB_ERR_UNSUPPORTED: return "TB_ERR_UNSUPPORTED: not implemented";
     case TB_ERR_ALIAS: return "TB_ERR_ALIAS: output overlaps an input";
     case TB_ERR_WORKSPACE: return "TB_ERR_WORKSPACE: the workspace is missing or smaller than the call needs";
+    case TB_ERR_VALUE: return "TB_ERR_VALUE: a scalar argument is outside its range";
     default: return "unknown tb_status";
   }
 }

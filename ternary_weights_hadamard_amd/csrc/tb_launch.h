@@ -42,4 +42,15 @@ hipError_t launch_gemm_ternary_splitk(const uint16_t* x, int64_t M, const uint32
                                       int64_t N, int64_t K, void* y, int y_dtype, float* workspace,
                                       size_t workspace_bytes, bool rotate, hipStream_t stream);
 
+hipError_t launch_block_norm(const tb_block_norm_args& a, hipStream_t stream);
+// vocabulary entries one workgroup sums
+constexpr int64_t kVerifySlice = 2048;
+hipError_t launch_verify_draft(const tb_verify_draft_args& a, hipStream_t stream);
+hipError_t launch_paged_append(const tb_paged_cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                               int64_t v_stride, hipStream_t stream);
+// parts the positions are split into when the workspace allows (1: none), and their bytes
+int attn_splits(const tb_paged_attention_args& a);
+size_t attn_part_bytes(const tb_paged_attention_args& a, int splits);
+hipError_t launch_paged_attention(const tb_paged_attention_args& a, int splits, hipStream_t stream);
+
 }  // namespace tb

@@ -23,11 +23,13 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtb.so")
 
-TB_F32, TB_BF16, TB_ACT8 = 0, 1, 2
+TB_F32, TB_BF16, TB_ACT8, TB_FP8 = 0, 1, 2, 3
 TB_FMT_DENSE, TB_FMT_24, TB_FMT_DENSE_MINERR, TB_FMT_DENSE_RESID = 0, 1, 2, 3
 TB_EFLAG_NONFINITE, TB_EFLAG_SCALE_OVF = 1, 2
 TB_GEMV_MAX_BATCH = 16
 TB_MAX_SEGMENTS = 8
+TB_NORM_MAX_C = 32768
+TB_MAX_DRAFT = 64
 TB_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _lib = None
@@ -60,6 +62,33 @@ class GemvSegment(ctypes.Structure):
                 ("planes", ctypes.c_int64), ("parts", ctypes.c_int64)]
 
 
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("y", _vp), ("resid", _vp), ("w_post", _vp), ("w_pre", _vp), ("gate", _vp), ("h", _vp), ("z", _vp),
+                ("rows", _i64), ("C", _i64), ("rows_per_gate", _i64), ("parts", _int), ("y_dtype", _int),
+                ("h_dtype", _int), ("w_dtype", _int), ("gate_dtype", _int), ("z_dtype", _int), ("rotate_in", _int),
+                ("rotate_out", _int), ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp),
+                ("cu_q", _vp), ("kv_len", _vp), ("n_pages", _i64), ("table_stride", _i64), ("table_width", _i64),
+                ("B", _i64), ("total_q", _i64), ("max_q", _i64), ("cache_dtype", _int), ("page", _int),
+                ("heads_kv", _int), ("head_dim", _int)]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", PagedCache), ("q", _vp), ("out", _vp), ("lse", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("q_stride", _i64), ("max_kv", _i64), ("window", _i64),
+                ("heads_q", _int), ("out_dtype", _int), ("scale", ctypes.c_float), ("reserved", _int)]
+
+
+class VerifyDraftArgs(ctypes.Structure):
+    _fields_ = [("p", _vp), ("q", _vp), ("drafts", _vp), ("u", _vp), ("u_next", _vp), ("cu_draft", _vp),
+                ("accepted", _vp), ("tokens", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+                ("B", _i64), ("total", _i64), ("vocab", _i64), ("p_stride", _i64), ("q_stride", _i64),
+                ("max_draft", _int), ("p_dtype", _int), ("q_dtype", _int), ("reserved", _int)]
+
+
 SIGNATURES = {
     "tb_status_string": (ctypes.c_char_p, [_int]),
     "tb_version": (_int, []),
@@ -81,6 +110,12 @@ SIGNATURES = {
     "tb_ternary_gemm_splitk_workspace": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "tb_ternary_gemm_splitk": (_int, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, ctypes.c_size_t, _vp]),
     "tb_ternary_gemm_rotated": (_int, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, ctypes.c_size_t, _vp]),
+    "tb_block_norm": (_int, [ctypes.POINTER(BlockNormArgs), _vp]),
+    "tb_paged_append": (_int, [ctypes.POINTER(PagedCache), _vp, _i64, _vp, _i64, _vp]),
+    "tb_paged_attention_workspace": (ctypes.c_size_t, [ctypes.POINTER(PagedAttentionArgs)]),
+    "tb_paged_attention": (_int, [ctypes.POINTER(PagedAttentionArgs), _vp]),
+    "tb_verify_draft_workspace": (ctypes.c_size_t, [_i64, _i64]),
+    "tb_verify_draft": (_int, [ctypes.POINTER(VerifyDraftArgs), _vp]),
 }
 
 
@@ -426,3 +461,270 @@ def tb_ternary_gemm_rotated(x, codes, scales, y=None, out_dtype=torch.bfloat16, 
     _check(lib().tb_ternary_gemm_rotated(_p(x), m, _p(codes), _p(scales), n, k, _p(y), _dt(y), _p(workspace),
                                          wbytes, _stream(stream)), "tb_ternary_gemm_rotated")
     return y
+
+
+# ------------------------------------------------------- serving operators
+
+_FLOATS = {torch.float32: TB_F32, torch.bfloat16: TB_BF16}
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`: allocated for that stream, so that its
+    memory is neither still in use elsewhere nor given away before the call is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _float_dt(t, what):
+    d = _FLOATS.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{what} must be float32 or bfloat16 (got {t.dtype})")
+    return d
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must be on {dev} (got one on {t.device})")
+
+
+def tb_block_norm(y, resid=None, w_post=None, w_pre=None, gate=None, rows_per_gate=1, alpha=1.0, eps=1e-6, y_parts=1,
+                  rotate_in=False, rotate_out=False, h=None, z=None, h_dtype=None, z_dtype=torch.bfloat16,
+                  with_h=True, stream=None):
+    """The boundary of a block: u = the sum of y's parts (rotated back if
+    rotate_in), normed with w_post if given; h = resid + alpha * gate * u; z =
+    norm of h with w_pre (rotated if rotate_out).  Returns (h, z).
+    y [rows, C] fp32 or bf16 ([y_parts, rows, C] fp32 with y_parts > 1), or None
+    (h = resid, not returned: only the norm).  resid [rows, C] or None.  w_post,
+    w_pre [C] of one dtype; without w_pre there is no z.  gate [gates, C]: row r
+    takes gate row r // rows_per_gate.  h (resid itself for in place) and z are
+    made when not given; z_dtype torch.uint8 writes the act8 operand."""
+    _dev(y, resid, w_post, w_pre, gate, h, z)
+    first = resid if y is None else y
+    _need(first is not None, "tb_block_norm: y or resid must be given")
+    parts = int(y_parts)
+    if y is not None and parts > 1:
+        _need(y.dim() == 3 and y.shape[0] == parts, f"tb_block_norm: y_parts={parts} needs y [{parts}, rows, C]")
+    else:
+        _need(first.dim() == 2, "tb_block_norm: y must be [rows, C]")
+    rows, ch = first.shape[-2], first.shape[-1]
+    dev = first.device
+    _same_device(dev, y, resid, w_post, w_pre, gate, h, z)
+    _need(resid is None or tuple(resid.shape) == (rows, ch), f"tb_block_norm: resid must be [{rows}, {ch}]")
+    for w in (w_post, w_pre):
+        _need(w is None or tuple(w.shape) == (ch,), f"tb_block_norm: w_post and w_pre must be [{ch}]")
+    _need(w_post is None or w_pre is None or w_post.dtype == w_pre.dtype, "tb_block_norm: w_post and w_pre differ in dtype")
+    if gate is not None:
+        rows_per_gate = int(rows_per_gate)
+        _need(rows_per_gate >= 1, "tb_block_norm: rows_per_gate must be at least 1")
+        _need(gate.dim() == 2 and gate.shape[1] == ch and gate.shape[0] * rows_per_gate >= rows,
+              f"tb_block_norm: gate must be [{-(-rows // rows_per_gate)}, {ch}] at rows_per_gate {rows_per_gate}")
+    if y is None or not with_h:
+        _need(h is None, "tb_block_norm: no h without y or with with_h=False")
+    elif h is None:
+        h = _empty((rows, ch), resid.dtype if resid is not None else h_dtype or y.dtype, dev, stream)
+    _need(h is None or tuple(h.shape) == (rows, ch), f"tb_block_norm: h must be [{rows}, {ch}]")
+    _need(h is None or resid is None or h.dtype == resid.dtype, "tb_block_norm: h and resid differ in dtype")
+    if w_pre is None:
+        _need(z is None, "tb_block_norm: z needs w_pre")
+    elif z is None:
+        if z_dtype == torch.uint8:
+            z = _empty(tb_act8_bytes(rows, ch), torch.uint8, dev, stream)
+        else:
+            z = _empty((rows, ch), z_dtype, dev, stream)
+    elif z.dtype == torch.uint8:
+        _need(z.numel() == tb_act8_bytes(rows, ch), f"tb_block_norm: z must hold {tb_act8_bytes(rows, ch)} bytes")
+    else:
+        _need(tuple(z.shape) == (rows, ch), f"tb_block_norm: z must be [{rows}, {ch}]")
+    w = w_post if w_post is not None else w_pre
+    zd = TB_F32 if z is None else TB_ACT8 if z.dtype == torch.uint8 else _float_dt(z, "tb_block_norm: z")
+    s = resid if resid is not None else h
+    args = BlockNormArgs(
+        _addr(y), _addr(resid), _addr(w_post), _addr(w_pre), _addr(gate), _addr(h), _addr(z), rows, ch, rows_per_gate,
+        parts, TB_F32 if y is None else _float_dt(y, "tb_block_norm: y"),
+        TB_F32 if s is None else _float_dt(s, "tb_block_norm: resid and h"),
+        TB_F32 if w is None else _float_dt(w, "tb_block_norm: w_post and w_pre"),
+        TB_F32 if gate is None else _float_dt(gate, "tb_block_norm: gate"), zd, int(rotate_in), int(rotate_out),
+        alpha, eps)
+    _check(lib().tb_block_norm(args, _stream(stream)), "tb_block_norm")
+    return h, z
+
+
+def _token_rows(t, heads, d, where):
+    """Elements between tokens of a [tokens, heads, d] tensor whose tokens are
+    contiguous inside (a slice of a fused projection's output)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{where} must be bfloat16 [tokens, {heads}, {d}] (got {t.dtype} {tuple(t.shape)})")
+    if not t.is_cuda or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{where}: a token's heads must be contiguous on the device")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+
+
+def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_scale, v_scale):
+    _dev(k_cache, v_cache, cu_q, kv_len, k_scale, v_scale)
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.dtype != v_cache.dtype:
+        raise ValueError(f"{where}: k_cache must be [pages, heads, page, d], v_cache [pages, heads, d, page], one dtype")
+    pages, heads, page, d = k_cache.shape
+    if v_cache.shape != (pages, heads, d, page):
+        raise ValueError(f"{where}: v_cache must be [{pages}, {heads}, {d}, {page}] (got {tuple(v_cache.shape)})")
+    if k_cache.dtype == torch.bfloat16:
+        kind = TB_BF16
+    elif k_cache.dtype == torch.float8_e4m3fn:
+        kind = TB_FP8
+    else:
+        raise TypeError(f"{where}: the cache must be bfloat16 or float8_e4m3fn (got {k_cache.dtype})")
+    b = kv_len.shape[0]
+    if not (cu_q.dtype == kv_len.dtype == block_table.dtype == torch.int32):
+        raise TypeError(f"{where}: block_table, cu_q and kv_len must be int32")
+    if kv_len.dim() != 1 or cu_q.shape != (b + 1,) or block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError(f"{where}: kv_len must be [B], cu_q [B + 1], block_table [B, entries]")
+    if not block_table.is_cuda or (block_table.numel() and block_table.stride(1) != 1):
+        raise ValueError(f"{where}: a sequence's block_table entries must be contiguous on the device")
+    for sc in (k_scale, v_scale):
+        if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):
+            raise ValueError(f"{where}: k_scale and v_scale must be float32 [{heads}], of an 8-bit cache")
+    _same_device(tokens.device, k_cache, v_cache, block_table, cu_q, kv_len, k_scale, v_scale)
+    width = block_table.shape[1]
+    stride = block_table.stride(0) if b > 1 else width
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
+                      cu_q.data_ptr(), kv_len.data_ptr(), pages, stride, width, b, tokens.shape[0], max_q, kind, page,
+                      heads, d)
+
+
+def tb_paged_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_scale=None, v_scale=None, stream=None):
+    """Write the new tokens' keys and values (bf16 [tokens, heads, d], slices of
+    a fused projection allowed) into the pages of their positions: sequence b's
+    tokens are rows cu_q[b]..cu_q[b + 1] - 1 and its last positions below
+    kv_len[b].  k_cache [pages, heads, page, d], v_cache [pages, heads, d, page],
+    bf16 or float8_e4m3fn (codes of x / scale[head]); max_q is at least every
+    sequence's new tokens."""
+    cache = _paged_cache("tb_paged_append", k, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
+    _same_device(k.device, v)
+    ks = _token_rows(k, cache.heads_kv, cache.head_dim, "tb_paged_append: k")
+    vs = _token_rows(v, cache.heads_kv, cache.head_dim, "tb_paged_append: v")
+    _need(v.shape[0] == k.shape[0], "tb_paged_append: k and v differ in tokens")
+    _check(lib().tb_paged_append(cache, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "tb_paged_append")
+
+
+def _attention_args(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale, window, k_scale, v_scale,
+                    out_dt):
+    where = "tb_paged_attention"
+    cache = _paged_cache(where, q, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
+    heads = q.shape[1] if q.dim() == 3 else 0
+    stride = _token_rows(q, heads, cache.head_dim, where + ": q")
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    return PagedAttentionArgs(cache, q.data_ptr(), None, None, None, 0, stride, int(max_kv), int(window), heads, out_dt,
+                              scale, 0)
+
+
+def tb_paged_attention_workspace(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, window=0):
+    """Bytes of the workspace tb_paged_attention splits the positions into."""
+    args = _attention_args(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, None, window, None, None,
+                           TB_BF16)
+    return int(lib().tb_paged_attention_workspace(args))
+
+
+def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale=None, window=0,
+                       k_scale=None, v_scale=None, out=None, out_dtype=torch.bfloat16, lse=None, with_lse=False,
+                       workspace=None, stream=None):
+    """Attention of each sequence's new tokens q (bf16 [tokens, heads, d]) over
+    its cached positions, causal, the last `window` of them only if window > 0;
+    the cache as in tb_paged_append, which comes first.  max_kv is the most
+    positions a sequence is likely to hold (it only decides the split).  scale
+    defaults to 1 / sqrt(d).  Returns out [tokens, heads, d], and (out, lse) if
+    `lse` (fp32 [tokens, heads]) is given or with_lse; rows that see nothing
+    are 0 (lse -inf).  `workspace`: a device tensor of
+    tb_paged_attention_workspace bytes, allocated here when None."""
+    if out is not None:
+        _dev(out)
+        out_dt = _float_dt(out, "tb_paged_attention: out")
+        _need(out.shape == q.shape, f"tb_paged_attention: out must be {tuple(q.shape)}")
+    else:
+        out = _empty(q.shape, out_dtype, q.device, stream)
+        out_dt = _float_dt(out, "tb_paged_attention: out")
+    args = _attention_args(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale, window, k_scale,
+                           v_scale, out_dt)
+    if lse is not None:
+        _dev(lse)
+        _need(lse.dtype == torch.float32 and lse.shape == q.shape[:2],
+              f"tb_paged_attention: lse must be float32 {tuple(q.shape[:2])}")
+    elif with_lse:
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
+    L = lib()
+    if workspace is None:
+        nbytes = L.tb_paged_attention_workspace(args)
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, q.device, stream)
+    else:
+        _dev(workspace)
+    _same_device(q.device, out, lse, workspace)
+    args.out, args.lse = out.data_ptr(), _addr(lse)
+    if workspace is not None:
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(L.tb_paged_attention(args, _stream(stream)), "tb_paged_attention")
+    return out if lse is None else (out, lse)
+
+
+def tb_verify_draft_workspace(batch, vocab):
+    return int(lib().tb_verify_draft_workspace(int(batch), int(vocab)))
+
+
+def _prob_rows(t, what):
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [rows, vocab] on the device, a row contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def tb_verify_draft(p, q, drafts, u, u_next, cu_draft, max_draft, accepted=None, tokens=None, workspace=None,
+                    stream=None):
+    """Verify drafted tokens: sequence b's drafts are rows cu_draft[b].. of
+    drafts (int32), u (fp32) and q (the drafter's probabilities [total, vocab],
+    or None for a certain drafter), its T + 1 target rows start at row
+    cu_draft[b] + b of p [total + B, vocab].  Draft j is kept while u * q < p;
+    then one token is drawn with u_next [B] from max(p - q, 0), or from p after
+    the last.  Returns (accepted int32 [B], tokens int32 [B, max_draft + 1]:
+    the kept tokens, the drawn one, then -1)."""
+    where = "tb_verify_draft"
+    _dev(drafts, u, u_next, cu_draft, accepted, tokens, workspace)
+    b, total = u_next.shape[0], drafts.shape[0]
+    max_draft = int(max_draft)
+    ps = _prob_rows(p, where + ": p")
+    vocab = p.shape[1]
+    _need(p.shape[0] == total + b, f"{where}: p must have {total + b} rows (drafts + sequences)")
+    qs = 0
+    if q is not None:
+        qs = _prob_rows(q, where + ": q")
+        _need(q.shape == (total, vocab), f"{where}: q must be [{total}, {vocab}]")
+    _need(drafts.dtype == cu_draft.dtype == torch.int32, f"{where}: drafts and cu_draft must be int32")
+    _need(u.dtype == u_next.dtype == torch.float32, f"{where}: u and u_next must be float32")
+    _need(drafts.dim() == 1 and u.shape == drafts.shape and u_next.dim() == 1 and cu_draft.shape == (b + 1,),
+          f"{where}: drafts and u must be [total], u_next [B], cu_draft [B + 1]")
+    dev = p.device
+    if accepted is None:
+        accepted = _empty(b, torch.int32, dev, stream)
+    if tokens is None:
+        tokens = _empty((b, max(max_draft, 0) + 1), torch.int32, dev, stream)
+    _need(accepted.dtype == tokens.dtype == torch.int32 and accepted.shape == (b,)
+          and tokens.shape == (b, max_draft + 1), f"{where}: accepted must be int32 [{b}], tokens int32 [{b}, {max_draft + 1}]")
+    L = lib()
+    if workspace is None:
+        workspace = _empty(max(L.tb_verify_draft_workspace(b, vocab), 16), torch.uint8, dev, stream)
+    _same_device(dev, q, drafts, u, u_next, cu_draft, accepted, tokens, workspace)
+    args = VerifyDraftArgs(p.data_ptr(), _addr(q), drafts.data_ptr(), u.data_ptr(), u_next.data_ptr(),
+                           cu_draft.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), b, total, vocab, ps, qs, max_draft,
+                           _float_dt(p, where + ": p"), TB_F32 if q is None else _float_dt(q, where + ": q"), 0)
+    _check(L.tb_verify_draft(args, _stream(stream)), where)
+    return accepted, tokens
