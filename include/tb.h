@@ -596,6 +596,7 @@ TB_API tb_status tb_block_norm(const tb_block_norm_args* args, void* stream);
  * at a negative position has none.
  */
 #define TB_MAX_PAGE 1024
+#define TB_MAX_POSITIONS ((int64_t)1 << 30)            /* table_width * page              */
 #define TB_MAX_TOKENS ((int64_t)1 << 27)               /* total_q and max_q              */
 #define TB_MAX_ROWS ((int64_t)1 << 27)                 /* max_q * heads_q of an attention */
 

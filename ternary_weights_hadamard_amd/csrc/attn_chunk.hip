@@ -1,0 +1,386 @@
+// Attention over the paged cache for many rows: chunks of prompts, and drafted
+// tokens of many heads (include/tb.h, tb_paged_attention).
+//
+// Mathematics.  A wave keeps 32 rows (token, head of one key/value head) as
+// the columns of S' = K Q' (v_mfma 32x32x16): a lane holds half of a row's
+// scores, so a row's maximum is one exchange between two lanes, and with the
+// positions behind the matrix rows of K permuted, the eight weights a lane
+// forms of each 16 positions are, as they are, its operand of O' = V' P'.
+// Weights never leave their lane.
+//
+// What bounds it: the matrix unit, the vector unit (scores -> weights) and the
+// LDS reads of the operands take about as long as one another (for 64
+// positions and 32 rows of 128: 1024 cycles of each), so the kernel lives from
+// overlapping them: two workgroups of four waves per CU, a tile of 64
+// positions of K and V double buffered in LDS and loaded by the
+// global-to-LDS path while the tile before it is worked on.
+#include "attn_common.h"
+#include "attn_launch.h"
+
+namespace tb {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;  // rows of a workgroup
+constexpr int kTile = 64;           // positions of a tile
+
+__device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(const f16x8& a, const f16x8& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+template <bool FP8>
+struct Value;
+template <>
+struct Value<false> {
+  typedef uint16_t Elem;
+  typedef bf16x8 V8;
+  static __device__ __forceinline__ __bf16 narrow(float x) { return (__bf16)x; }
+};
+template <>
+struct Value<true> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
+  typedef uint8_t Elem;
+  typedef f16x8 V8;
+  static __device__ __forceinline__ _Float16 narrow(float x) { return (_Float16)x; }
+};
+
+// 16-byte chunks of the two tiles in LDS.  Row r of K (a position) has D / 8 of
+// them, row r of V (a channel) kTile / 8; chunk c of a row lies at c ^ f(r), so
+// that the lanes of a read, which take the same chunk of different rows, fall
+// on different banks.
+template <int D>
+__device__ __forceinline__ int k_chunk(int row, int c) {
+  return row * (D / 8) + (c ^ (row & (D / 8 - 1)));
+}
+__device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ (row & 7)); }
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_attention_args a, AttnPlan plan) {
+  typedef typename Value<FP8>::Elem Elem;
+  typedef typename Value<FP8>::V8 V8;
+  constexpr int KK = D / 16;   // steps of a score tile
+  constexpr int DT = D / 32;   // 32-channel tiles of O'
+  constexpr int kChunks = kTile * D / 8;  // 16-byte chunks of a tile of K, and of V
+  __shared__ __align__(16) u32x4 lds[2][2][kChunks];
+
+  const tb_paged_cache& c = a.cache;
+  const int64_t b = blockIdx.z;
+  const int group = a.heads_q / c.heads_kv;
+  const int64_t width = c.n_pages > 0 ? c.table_width : 0;
+  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
+  const int64_t n = s.n < c.max_q ? s.n : c.max_q;
+  const int64_t nrows = n * group;
+  if (!plan.by_chunk(nrows)) return;
+  const int splits = plan.chunk_splits;
+  const int split = blockIdx.x % (unsigned)splits, item = blockIdx.x / (unsigned)splits;
+  const int head = item % c.heads_kv;
+  // the last rows see the most positions: they go first
+  const int64_t row_tiles = (nrows + kRows - 1) / kRows;
+  const int64_t rt = row_tiles - 1 - item / c.heads_kv;
+  if (rt < 0) return;
+  const int64_t r0 = rt * kRows;
+  const int64_t r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
+  const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(r_last / group), a.window);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i32 = lane & 31, half = lane >> 5;
+
+  // the lane's row, and its wave's first and last
+  const int64_t r = r0 + wave * 32 + i32;
+  const bool row_live = r < nrows;
+  const int tok = row_live ? (int)(r / group) : 0;
+  const int hq = head * group + (row_live ? (int)(r % group) : 0);
+  const int64_t pos = (int64_t)s.first_pos + tok;
+  const int64_t low = a.window > 0 ? pos - a.window : -1;
+  const int64_t w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
+  const int64_t w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
+  const int64_t pos_first = (int64_t)s.first_pos + w_first / group, pos_last = (int64_t)s.first_pos + w_last / group;
+
+  // scores are scaled by |scale|; its sign goes into the queries.  A scale of
+  // 0 is taken as the smallest number, so that an unseen -inf stays one.
+  float scale2 = a.scale * kLog2e * (FP8 && c.k_scale ? c.k_scale[head] : 1.f);
+  const uint32_t flip = scale2 < 0.f ? 0x80008000u : 0u;
+  scale2 = fmaxf(fabsf(scale2), 1.17549435e-38f);
+  bf16x8 q[KK];
+  {
+    const uint16_t* qp =
+        static_cast<const uint16_t*>(a.q) + (s.row0 + tok) * a.q_stride + (int64_t)hq * D + 8 * half;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (row_live) w = *reinterpret_cast<const u32x4*>(qp + 16 * kk);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] ^= flip;
+      q[kk] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+
+  const int first_tile = span.begin / kTile;
+  const int tiles = span.end > span.begin ? (span.end + kTile - 1) / kTile - first_tile : 0;
+  const int per = (tiles + splits - 1) / splits;
+  const int t_begin = split * per, t_end = t_begin + per < tiles ? t_begin + per : tiles;
+
+  const int32_t* table = c.block_table + b * c.table_stride;
+  const int shift = __builtin_ctz(c.page);
+  const int64_t page_elems = (int64_t)c.page * D, page_step = (int64_t)c.heads_kv * page_elems;
+  const Elem* kc = static_cast<const Elem*>(c.k_cache) + head * page_elems;
+  const Elem* vc = static_cast<const Elem*>(c.v_cache) + head * page_elems;
+
+  // Staging.  bf16: a wave moves whole kilobytes from global memory to LDS,
+  // lane i to the i-th 16 bytes, so the lanes read permuted chunks of their
+  // rows.  8-bit: 16 values a lane through registers, widened on the way.
+  //
+  // A tile is four runs of 16 positions, each in one page.  What a lane loads
+  // of V lies in run v_run, the same for all its loads, so it looks up that
+  // run's page (-1: none, or nobody sees it; its entry is not read then), and
+  // lane kHolder * g thereby holds run g's.  What a wave loads of K with one
+  // instruction lies in one run.
+  constexpr int kPer = FP8 ? 16 : 8;                               // positions (or channels) of a 16-byte load
+  constexpr int kLoads = kTile * D / kPer / (64 * kWaves);         // loads of a lane, for K and for V
+  constexpr int kStep = FP8 ? 64 * kWaves / (D / 16) : 64 * kWaves / (D / 8);        // rows of K between them
+  constexpr int vStep = 64 * kWaves / (kTile / kPer);              // rows of V between them
+  constexpr int kHolder = FP8 ? 1 : 2;
+  const int tid = wave * 64 + lane;
+  const int k_row = tid / (D / kPer), v_row = tid / (kTile / kPer);  // of the first load
+  const int k_ch = FP8 ? tid % (D / 16) : (tid % (D / 8)) ^ (k_row & (D / 8 - 1));
+  const int v_ch = FP8 ? tid % 4 : (tid % 8) ^ (v_row & 7);
+  const int v_run = FP8 ? v_ch : v_ch >> 1;
+  const int k_off = (k_row & 15) * D + k_ch * kPer;                 // inside a run
+  const int v_off = v_row * c.page + (v_ch * kPer & 15);
+  auto lookup = [&](int t) -> int {
+    const int x = (first_tile + t) * kTile + 16 * v_run;
+    if (t >= t_end || (x | (c.page - 1)) < span.begin || x >= span.end) return -1;
+    return paged_page(table, c.table_width, c.n_pages, x >> shift);
+  };
+  auto run_page = [](int pages, int g) { return __builtin_amdgcn_readlane(pages, kHolder * g); };
+  u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
+  auto stage = [&](int t, int pages, int buf) {
+    const int x0 = (first_tile + t) * kTile;
+    const Elem* vp = vc + (pages < 0 ? 0 : pages) * page_step + ((x0 + 16 * v_run) & (c.page - 1)) + v_off;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int run = (i * kStep + __builtin_amdgcn_readfirstlane(k_row)) >> 4;
+      const int page = run_page(pages, run);
+      const Elem* kp = kc + (page < 0 ? 0 : page) * page_step + (int64_t)((x0 + 16 * run) & (c.page - 1)) * D;
+      if constexpr (FP8) {
+        kr[i] = *reinterpret_cast<const u32x4*>(kp + k_off);
+        vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
+      } else {
+        const int at = i * 64 * kWaves + wave * 64;  // the wave's first chunk
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(kp + k_off),
+                                         (__attribute__((address_space(3))) uint32_t*)&lds[buf][0][at], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) uint32_t*)(vp + i * vStep * c.page),
+            (__attribute__((address_space(3))) uint32_t*)&lds[buf][1][at], 16, 0, 0);
+      }
+    }
+  };
+  auto widen = [&](int buf) {  // 8-bit: the staged registers into LDS
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int kw = i * kStep + k_row, vw = i * vStep + v_row;
+        lds[buf][0][k_chunk<D>(kw, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
+        lds[buf][0][k_chunk<D>(kw, 2 * k_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][2], kr[i][3]}));
+        lds[buf][1][v_chunk(vw, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
+        lds[buf][1][v_chunk(vw, 2 * v_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][2], vr[i][3]}));
+      }
+    }
+  };
+
+  // matrix row m of a score tile stands for position key(m) of its 32: a
+  // lane's score registers 0..7 are then positions 8 half + 0..7, 8..15 are 16 more
+  const int key = 16 * (i32 >> 4) + 8 * ((i32 >> 2) & 1) + 4 * ((i32 >> 3) & 1) + (i32 & 3);
+
+  float m = -__builtin_inff(), l = 0.f;  // maximum (log2 units) that the weights are relative to, and the lane's sum
+  f32x16 o[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[dt][e] = 0.f;
+
+  int pages = lookup(t_begin);
+  if (t_begin < t_end) {
+    stage(t_begin, pages, 0);
+    widen(0);
+  }
+  int pages_next = lookup(t_begin + 1);
+  for (int t = t_begin; t < t_end; ++t) {
+    const int buf = (t - t_begin) & 1;
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's share of the tile is in LDS
+    __syncthreads();
+    if (t + 1 < t_end) stage(t + 1, pages_next, buf ^ 1);
+    const int pages_after = lookup(t + 2);
+    const int x0 = (first_tile + t) * kTile;
+    // does any row of the wave see any of it
+    const bool any = x0 <= pos_last && (a.window <= 0 || x0 + kTile - 1 > pos_first - a.window);
+    if (any) {
+      f32x16 sc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[u][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+          sc[u] = mfma32(__builtin_bit_cast(bf16x8, lds[buf][0][k_chunk<D>(32 * u + key, 2 * kk + half)]), q[kk], sc[u]);
+      }
+
+      // The lane's scores: register 8 k + e of tile u is position 32 u + 16 k + 8 half + e.
+      uint32_t there = 0xfu;  // which of the tile's runs exist
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (run_page(pages, g) < 0) there &= ~(1u << g);
+      const bool full = there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > pos_last - a.window);
+      uint32_t seen = 0xffffffffu;  // bit 16 u + register
+      if (!full) {
+        seen = 0;
+        const int64_t rel = (int64_t)x0 + 8 * half;
+        const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 63 ? 63 : pos - rel) : -1;
+        const int lo = (int)(low - rel < -1 ? -1 : low - rel > 63 ? 63 : low - rel);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int x = 32 * u + 16 * (e >> 3) + (e & 7);
+            const bool see = x <= hi && x > lo && ((there >> (2 * u + (e >> 3))) & 1u);
+            seen |= (see ? 1u : 0u) << (16 * u + e);
+            sc[u][e] = see ? sc[u][e] : -__builtin_inff();
+          }
+      }
+
+      float top = sc[0][0];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[u][e]);
+      float t0, t1;
+      swap_halves(top, t0, t1);
+      top = fmaxf(t0, t1) * scale2;
+      // The weights stay relative to an older maximum while the new one is
+      // less than 2^8 above it: nothing is rounded more (they are at most 2^8),
+      // and the values' sums are rarely rescaled.
+      if (__ballot(top > m + 8.f) != 0) {
+        const float m_new = fmaxf(m, top);
+        const float alpha = m_new == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
+        m = m_new;
+        l *= alpha;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[dt][e] *= alpha;
+      }
+      const float base = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          sc[u][e] = exp2_fast(fmaf(sc[u][e], scale2, -base));
+          l += sc[u][e];
+        }
+
+      bool bad = false;
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < kChunks / 64; ++i) {
+          const u32x4 w = lds[buf][1][i * 64 + lane];
+          if constexpr (FP8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              bad = bad || (w[e] & 0x7c00u) == 0x7c00u || (w[e] & 0x7c000000u) == 0x7c000000u;
+          } else {
+            bad = bad || any_nonfinite_bf16(w);
+          }
+        }
+      }
+      if (__ballot(bad) == 0) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          V8 w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+            o[dt] = mfma32(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
+        }
+      } else {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          V8 w, see;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
+            see[e] = Value<FP8>::narrow((seen >> (8 * kb + e)) & 1u ? 1.f : 0.f);
+          }
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) {
+            const SplitValues<V8> sv =
+                split_values(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]));
+            f32x16 count;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) count[e] = 0.f;
+            o[dt] = mfma32(sv.finite, w, o[dt]);
+            const f32x16 up = mfma32(sv.up, see, count);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(up[e], 0.f);
+            const f32x16 down = mfma32(sv.down, see, count);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(0.f, down[e]);
+          }
+        }
+      }
+    }
+    pages = pages_next;
+    pages_next = pages_after;
+    widen(buf ^ 1);
+  }
+
+  // the row's sum, and its output: register 4 j + e of tile dt is channel 32 dt + 8 j + 4 half + e
+  {
+    float a0, a1;
+    swap_halves(l, a0, a1);
+    l = a0 + a1;
+  }
+  if (!row_live) return;
+  const int64_t at = (s.row0 + tok) * a.heads_q + hq;
+  if (splits > 1) {
+    const int64_t pr = (int64_t)split * plan.rows + at;
+    if (half == 0) plan.stats[pr] = float2{m, l};
+    if (l == 0.f) return;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(plan.values + pr * D + 32 * dt + 8 * j + 4 * half) =
+            f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
+    return;
+  }
+  const RowScale rs = row_scale(a, head, at, half == 0, m, l);
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      write4(a, at * D + 32 * dt + 8 * j + 4 * half,
+             f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]}, rs);
+}
+
+}  // namespace
+
+hipError_t launch_attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream) {
+  const tb_paged_cache& c = a.cache;
+  const int64_t row_tiles = (c.max_q * (a.heads_q / c.heads_kv) + kRows - 1) / kRows;
+  const dim3 grid((unsigned)(row_tiles * c.heads_kv * plan.chunk_splits), 1, (unsigned)c.B), block(64 * kWaves);
+  const bool f8 = c.cache_dtype == TB_FP8;
+  if (c.head_dim == 64) {
+    if (f8) hipLaunchKernelGGL((attn_chunk_kernel<64, true>), grid, block, 0, stream, a, plan);
+    else hipLaunchKernelGGL((attn_chunk_kernel<64, false>), grid, block, 0, stream, a, plan);
+  } else {
+    if (f8) hipLaunchKernelGGL((attn_chunk_kernel<128, true>), grid, block, 0, stream, a, plan);
+    else hipLaunchKernelGGL((attn_chunk_kernel<128, false>), grid, block, 0, stream, a, plan);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace tb

@@ -119,14 +119,4 @@ __device__ __forceinline__ bool any_nonfinite_fp8(const u32x4& w) {
   return bad;
 }
 
-// One part of a row of a split sequence in the workspace: its sums, then the
-// weighted values, each part of all rows after the other:
-//   stats  float2 [parts][rows]     (maximum in log2 units, sum)
-//   values float  [parts][rows][D]  (not divided by the sum)
-struct AttnParts {
-  float2* stats;
-  float* values;
-  int64_t rows;
-};
-
 }  // namespace tb

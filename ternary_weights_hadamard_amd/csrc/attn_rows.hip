@@ -18,7 +18,7 @@
 // LDS; positions are also split over workgroups until the GPU is full, and the
 // parts are joined by a second launch.
 #include "attn_common.h"
-#include "tb_launch.h"
+#include "attn_launch.h"
 
 namespace tb {
 
@@ -50,43 +50,8 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// A row's output and log-sum-exp: `v` are its DL weighted sums from channel d0
-// on, `top` (log2 units) and `total` its statistics.
-template <int DL>
-__device__ __forceinline__ void write_row(const tb_paged_attention_args& a, int64_t at, int head, int d0,
-                                          const float (&v)[DL], float top, float total) {
-  const tb_paged_cache& c = a.cache;
-  const float vs = c.cache_dtype == TB_FP8 && c.v_scale ? c.v_scale[head] : 1.f;
-  const float f = total == 0.f ? 0.f : vs / total;
-  if (a.lse && d0 == 0) a.lse[at] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * kLn2;
-  const int64_t i = at * c.head_dim + d0;
-#pragma unroll
-  for (int e = 0; e < DL; e += 4) {
-    const f32x4 w = {v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f};
-    if (a.out_dtype == TB_F32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + i + e) = w;
-    } else {
-      u32x2 h;
-      h[0] = f32_to_bf16_rne(w[0]) | (f32_to_bf16_rne(w[1]) << 16);
-      h[1] = f32_to_bf16_rne(w[2]) | (f32_to_bf16_rne(w[3]) << 16);
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + i + e) = h;
-    }
-  }
-}
-
-// The workspace of `splits` parts: statistics after the values.
-AttnParts attn_parts(const tb_paged_attention_args& a, int splits) {
-  AttnParts p{nullptr, nullptr, a.cache.total_q * a.heads_q};
-  if (splits > 1) {
-    p.values = static_cast<float*>(a.workspace);
-    p.stats = reinterpret_cast<float2*>(p.values + (int64_t)splits * p.rows * a.cache.head_dim);
-  }
-  return p;
-}
-
 template <int D, bool FP8>
-__global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attention_args a, AttnParts parts,
-                                                               int splits) {
+__global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attention_args a, AttnPlan plan) {
   typedef Ops<FP8> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
@@ -100,6 +65,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
 
   const tb_paged_cache& c = a.cache;
   const int64_t b = blockIdx.z;
+  const int splits = plan.rows_splits;
   const int split = blockIdx.x % (unsigned)splits, item = blockIdx.x / (unsigned)splits;
   const int head = item % c.heads_kv, rt = item / c.heads_kv;
   const int group = a.heads_q / c.heads_kv;
@@ -110,7 +76,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
   const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
   const int64_t n = s.n < c.max_q ? s.n : c.max_q;
   const int64_t nrows = n * group, r0 = (int64_t)rt * 16;
-  if (r0 >= nrows) return;
+  if (r0 >= nrows || plan.by_chunk(nrows)) return;
   const int64_t rl = r0 + 15 < nrows ? r0 + 15 : nrows - 1;  // last row
   const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(rl / group), a.window);
 
@@ -368,96 +334,35 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
   }
   const int64_t at = (s.row0 + (r0 + orow) / group) * a.heads_q + head * group + (r0 + orow) % group;
   if (splits > 1) {
-    const int64_t pr = (int64_t)split * parts.rows + at;
-    if (d0 == 0) parts.stats[pr] = float2{top, total};
+    const int64_t pr = (int64_t)split * plan.rows + at;
+    if (d0 == 0) plan.stats[pr] = float2{top, total};
+    if (total == 0.f) return;
 #pragma unroll
     for (int e = 0; e < DL; e += 4)
-      *reinterpret_cast<f32x4*>(parts.values + pr * D + d0 + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
+      *reinterpret_cast<f32x4*>(plan.values + pr * D + d0 + e) = f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]};
     return;
   }
-  write_row<DL>(a, at, head, d0, v, top, total);
-}
-
-// The parts of split sequences joined, 16 rows (token, head of one key/value
-// head) per workgroup as in the kernel that wrote them.
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args a, AttnParts parts, int splits) {
-  constexpr int DL = D / 16;
-  const tb_paged_cache& c = a.cache;
-  const int64_t b = blockIdx.z;
-  const int head = blockIdx.x % (unsigned)c.heads_kv, rt = blockIdx.x / (unsigned)c.heads_kv;
-  const int group = a.heads_q / c.heads_kv;
-  const int64_t width = c.n_pages > 0 ? c.table_width : 0;
-  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
-  const int64_t n = s.n < c.max_q ? s.n : c.max_q;
-  const int64_t r = (int64_t)rt * 16 + (threadIdx.x >> 4);
-  if (r >= n * group) return;
-  const int d0 = (threadIdx.x & 15) * DL;
-  const int64_t at = (s.row0 + r / group) * a.heads_q + head * group + r % group;
-  float top = -__builtin_inff();
-  for (int p = 0; p < splits; ++p) top = fmaxf(top, parts.stats[p * parts.rows + at].x);
-  const float base = top == -__builtin_inff() ? 0.f : top;
-  float total = 0.f, v[DL];
+  const RowScale rs = row_scale(a, head, at, d0 == 0, top, total);
 #pragma unroll
-  for (int e = 0; e < DL; ++e) v[e] = 0.f;
-  for (int p = 0; p < splits; ++p) {
-    const int64_t pr = p * parts.rows + at;
-    const float2 st = parts.stats[pr];
-    const float f = exp2_fast(st.x - base);
-    total = fmaf(st.y, f, total);
-#pragma unroll
-    for (int e = 0; e < DL; e += 4) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(parts.values + pr * D + d0 + e);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[e + k] = fmaf(x[k], f, v[e + k]);
-    }
-  }
-  write_row<DL>(a, at, head, d0, v, top, total);
-}
-
-template <int D>
-hipError_t launch(const tb_paged_attention_args& a, int splits, hipStream_t stream) {
-  const tb_paged_cache& c = a.cache;
-  const int64_t row_tiles = (c.max_q * (a.heads_q / c.heads_kv) + 15) / 16;
-  const AttnParts parts = attn_parts(a, splits);
-  const unsigned items = (unsigned)(row_tiles * c.heads_kv);
-  const dim3 grid(items * (unsigned)splits, 1, (unsigned)c.B);
-  if (c.cache_dtype == TB_FP8)
-    hipLaunchKernelGGL((attn_rows_kernel<D, true>), grid, dim3(64 * kWaves), 0, stream, a, parts,
-                       splits);
-  else
-    hipLaunchKernelGGL((attn_rows_kernel<D, false>), grid, dim3(64 * kWaves), 0, stream, a, parts,
-                       splits);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits == 1) return e;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(items, 1, grid.z), dim3(256), 0, stream, a, parts, splits);
-  return hipGetLastError();
+  for (int e = 0; e < DL; e += 4) write4(a, at * D + d0 + e, f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}, rs);
 }
 
 }  // namespace
 
-// Workgroups that fill the GPU (two for each of 256 CUs), with at least four
-// tiles a wave; at most 64 parts.
-int attn_splits(const tb_paged_attention_args& a) {
+hipError_t launch_attn_rows(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream) {
   const tb_paged_cache& c = a.cache;
-  const int64_t row_tiles = (c.max_q * (a.heads_q / c.heads_kv) + 15) / 16;
-  const int64_t base = row_tiles * c.heads_kv * c.B;
-  const int64_t tile = c.cache_dtype == TB_FP8 ? 64 : 32;
-  const int64_t keys = a.window > 0 && a.window + c.max_q < a.max_kv ? a.window + c.max_q : a.max_kv;
-  int64_t s = base > 0 ? (512 + base - 1) / base : 1;
-  const int64_t most = keys / (tile * kWaves * 2);
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-}
-
-size_t attn_part_bytes(const tb_paged_attention_args& a, int splits) {
-  if (splits <= 1) return 0;
-  return (size_t)splits * (size_t)a.cache.total_q * (size_t)a.heads_q * ((size_t)a.cache.head_dim + 2) * sizeof(float);
-}
-
-hipError_t launch_paged_attention(const tb_paged_attention_args& a, int splits, hipStream_t stream) {
-  if (a.cache.head_dim == 64) return launch<64>(a, splits, stream);
-  return launch<128>(a, splits, stream);
+  int64_t rows = c.max_q * (a.heads_q / c.heads_kv);
+  if (rows > plan.few) rows = plan.few;
+  const dim3 grid((unsigned)((rows + 15) / 16 * c.heads_kv * plan.rows_splits), 1, (unsigned)c.B), block(64 * kWaves);
+  const bool f8 = c.cache_dtype == TB_FP8;
+  if (c.head_dim == 64) {
+    if (f8) hipLaunchKernelGGL((attn_rows_kernel<64, true>), grid, block, 0, stream, a, plan);
+    else hipLaunchKernelGGL((attn_rows_kernel<64, false>), grid, block, 0, stream, a, plan);
+  } else {
+    if (f8) hipLaunchKernelGGL((attn_rows_kernel<128, true>), grid, block, 0, stream, a, plan);
+    else hipLaunchKernelGGL((attn_rows_kernel<128, false>), grid, block, 0, stream, a, plan);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace tb

@@ -70,7 +70,8 @@ tb_status check_cache_sizes(const tb_paged_cache& c) {
   if (c.B < 0 || c.B > 65535 || c.heads_kv < 1 || c.heads_kv > 65535 || c.n_pages < 0 || c.n_pages > INT32_MAX)
     return TB_ERR_SHAPE;
   if (c.total_q < 0 || c.total_q > TB_MAX_TOKENS || c.max_q < 0 || c.max_q > TB_MAX_TOKENS) return TB_ERR_SHAPE;
-  if (c.table_width < 0 || c.table_width > INT32_MAX || c.table_stride < c.table_width) return TB_ERR_SHAPE;
+  if (c.table_width < 0 || c.table_stride < c.table_width) return TB_ERR_SHAPE;
+  if (c.table_width > TB_MAX_POSITIONS / c.page) return TB_ERR_SHAPE;
   return TB_OK;
 }
 

@@ -67,7 +67,7 @@ CACHE_REFUSALS = [
     (DTYPE, dict(cache_dtype=F32)), (SHAPE, dict(head_dim=96)), (SHAPE, dict(page=8)), (SHAPE, dict(page=48)),
     (SHAPE, dict(page=2048)), (SHAPE, dict(B=-1)), (SHAPE, dict(B=65536)), (SHAPE, dict(heads_kv=0)),
     (SHAPE, dict(n_pages=-1)), (SHAPE, dict(total_q=-1)), (SHAPE, dict(max_q=-1)), (SHAPE, dict(table_width=5)),
-    (SHAPE, dict(table_width=-1)), (SHAPE, dict(total_q=(1 << 27) + 1)),
+    (SHAPE, dict(table_width=-1)), (SHAPE, dict(table_width=(1 << 26) + 1, table_stride=1 << 27)), (SHAPE, dict(total_q=(1 << 27) + 1)),
     (NULL, dict(k_cache=None)), (NULL, dict(v_cache=None)), (NULL, dict(block_table=None)), (NULL, dict(cu_q=None)),
     (NULL, dict(kv_len=None)), (ALIGN, dict(k_cache=A + 8)), (ALIGN, dict(v_cache=B + 2)), (ALIGN, dict(cu_q=D + 1)),
     (ALIGN, dict(block_table=C + 2)), (ALIGN, dict(kv_len=D + 4098)), (ALIGN, dict(k_scale=G + 2)),
