@@ -22,8 +22,9 @@ namespace tb {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kRows = 32 * kWaves;  // rows of a workgroup
-constexpr int kTile = 64;           // positions of a tile
+constexpr int kRows = kChunkTile;       // rows of a workgroup: 32 a wave
+constexpr int kTile = kChunkPositions;  // positions of a tile
+static_assert(kRows == 32 * kWaves && kTile == 64, "the lane layouts below");
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -73,9 +74,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
   const int64_t n = s.n < c.max_q ? s.n : c.max_q;
   const int64_t nrows = n * group;
-  if (!plan.by_chunk(nrows)) return;
-  const int splits = plan.chunk_splits;
-  const int split = blockIdx.x % (unsigned)splits, item = blockIdx.x / (unsigned)splits;
+  if (!plan.is_chunk(nrows)) return;
+  const int split = blockIdx.x % (unsigned)plan.by_chunk.splits, item = blockIdx.x / (unsigned)plan.by_chunk.splits;
   const int head = item % c.heads_kv;
   // the last rows see the most positions: they go first
   const int64_t row_tiles = (nrows + kRows - 1) / kRows;
@@ -84,6 +84,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   const int64_t r0 = rt * kRows;
   const int64_t r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
   const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(r_last / group), a.window);
+  const TileSpan all = tile_span(span, kTile);
+  const int parts = plan.by_chunk.parts(all.count), first_tile = all.first;
+  if (split >= parts) return;
+  const int t_begin = split * plan.by_chunk.tiles;
+  const int t_end = split + 1 == parts ? all.count : t_begin + plan.by_chunk.tiles;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i32 = lane & 31, half = lane >> 5;
@@ -98,6 +103,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   const int64_t w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
   const int64_t w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
   const int64_t pos_first = (int64_t)s.first_pos + w_first / group, pos_last = (int64_t)s.first_pos + w_last / group;
+  // and of the workgroup
+  const int64_t all_first = (int64_t)s.first_pos + r0 / group, all_last = (int64_t)s.first_pos + r_last / group;
 
   // scores are scaled by |scale|; its sign goes into the queries.  A scale of
   // 0 is taken as the smallest number, so that an unseen -inf stays one.
@@ -117,11 +124,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
       q[kk] = __builtin_bit_cast(bf16x8, w);
     }
   }
-
-  const int first_tile = span.begin / kTile;
-  const int tiles = span.end > span.begin ? (span.end + kTile - 1) / kTile - first_tile : 0;
-  const int per = (tiles + splits - 1) / splits;
-  const int t_begin = split * per, t_end = t_begin + per < tiles ? t_begin + per : tiles;
 
   const int32_t* table = c.block_table + b * c.table_stride;
   const int shift = __builtin_ctz(c.page);
@@ -215,10 +217,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
     if (t + 1 < t_end) stage(t + 1, pages_next, buf ^ 1);
     const int pages_after = lookup(t + 2);
     const int x0 = (first_tile + t) * kTile;
-    // does any row of the wave see any of it
+    uint32_t there = 0xfu;  // which of the tile's runs exist
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (run_page(pages, g) < 0) there &= ~(1u << g);
+    // does any row of the wave see any of it; do all of the workgroup's see all of it
     const bool any = x0 <= pos_last && (a.window <= 0 || x0 + kTile - 1 > pos_first - a.window);
+    const bool all_full = there == 0xfu && x0 + kTile - 1 <= all_first && (a.window <= 0 || x0 > all_last - a.window);
+    uint32_t seen = any ? 0xffffffffu : 0u;  // bit 16 u + register
+    f32x16 sc[2];
     if (any) {
-      f32x16 sc[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -229,12 +237,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
       }
 
       // The lane's scores: register 8 k + e of tile u is position 32 u + 16 k + 8 half + e.
-      uint32_t there = 0xfu;  // which of the tile's runs exist
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if (run_page(pages, g) < 0) there &= ~(1u << g);
       const bool full = there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > pos_last - a.window);
-      uint32_t seen = 0xffffffffu;  // bit 16 u + register
       if (!full) {
         seen = 0;
         const int64_t rel = (int64_t)x0 + 8 * half;
@@ -280,56 +283,57 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
           sc[u][e] = exp2_fast(fmaf(sc[u][e], scale2, -base));
           l += sc[u][e];
         }
+    }
 
+    // Values that are not finite (attn_common.h): looked for in the tiles that
+    // some row sees in part, each wave in its share; where there are any, every
+    // wave counts its rows', and then they are 0 in LDS.
+    if (!all_full) {
       bool bad = false;
-      if (!full) {
 #pragma unroll
-        for (int i = 0; i < kChunks / 64; ++i) {
-          const u32x4 w = lds[buf][1][i * 64 + lane];
-          if constexpr (FP8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              bad = bad || (w[e] & 0x7c00u) == 0x7c00u || (w[e] & 0x7c000000u) == 0x7c000000u;
-          } else {
-            bad = bad || any_nonfinite_bf16(w);
-          }
-        }
+      for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
+        const u32x4 w = lds[buf][1][i * 64 * kWaves + tid];
+        bad = bad || (FP8 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w));
       }
-      if (__ballot(bad) == 0) {
+      if (__syncthreads_or(bad)) {
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          V8 w;
+        for (int dt = 0; dt < DT; ++dt) {
+          f32x16 up, down;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
+          for (int e = 0; e < 16; ++e) up[e] = down[e] = 0.f;
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-            o[dt] = mfma32(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
-        }
-      } else {
+          for (int kb = 0; kb < 4; ++kb) {
+            V8 see, v = __builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]);
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          V8 w, see;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
-            see[e] = Value<FP8>::narrow((seen >> (8 * kb + e)) & 1u ? 1.f : 0.f);
+            for (int e = 0; e < 8; ++e) see[e] = (seen >> (8 * kb + e)) & 1u ? 1.f : 0.f;
+            const Nonfinite<V8> nf = take_nonfinite(v);
+            up = mfma32(nf.up, see, up);
+            down = mfma32(nf.down, see, down);
           }
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) {
-            const SplitValues<V8> sv =
-                split_values(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]));
-            f32x16 count;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) count[e] = 0.f;
-            o[dt] = mfma32(sv.finite, w, o[dt]);
-            const f32x16 up = mfma32(sv.up, see, count);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(up[e], 0.f);
-            const f32x16 down = mfma32(sv.down, see, count);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(0.f, down[e]);
-          }
+          for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(up[e], down[e]);
+          __builtin_amdgcn_sched_barrier(0);  // one at a time: this path is rare, its registers are not to count
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
+          V8 v = __builtin_bit_cast(V8, lds[buf][1][i * 64 * kWaves + tid]);
+          take_nonfinite(v);
+          lds[buf][1][i * 64 * kWaves + tid] = __builtin_bit_cast(u32x4, v);
+        }
+        __syncthreads();
+      }
+    }
+
+    if (any) {
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        V8 w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+          o[dt] = mfma32(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
       }
     }
     pages = pages_next;
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   }
   if (!row_live) return;
   const int64_t at = (s.row0 + tok) * a.heads_q + hq;
-  if (splits > 1) {
+  if (parts > 1) {
     const int64_t pr = (int64_t)split * plan.rows + at;
     if (half == 0) plan.stats[pr] = float2{m, l};
     if (l == 0.f) return;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
 hipError_t launch_attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream) {
   const tb_paged_cache& c = a.cache;
   const int64_t row_tiles = (c.max_q * (a.heads_q / c.heads_kv) + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(row_tiles * c.heads_kv * plan.chunk_splits), 1, (unsigned)c.B), block(64 * kWaves);
+  const dim3 grid((unsigned)(row_tiles * c.heads_kv * plan.by_chunk.splits), 1, (unsigned)c.B), block(64 * kWaves);
   const bool f8 = c.cache_dtype == TB_FP8;
   if (c.head_dim == 64) {
     if (f8) hipLaunchKernelGGL((attn_chunk_kernel<64, true>), grid, block, 0, stream, a, plan);

@@ -61,36 +61,24 @@ __device__ __forceinline__ f16x8 fp8_to_f16(const u32x2& w) {
 // Values that are not finite must reach only the tokens that see their
 // position, and a matrix instruction multiplies every value with every token's
 // weight, 0 where the token does not see it.  In the rare tile where both
-// occur the values go in with these elements replaced by 0, and whether a
-// token sees a +inf (or NaN), a -inf (or NaN) is counted by two more products
-// with 1 in those places.
+// occur, two products with 1 in the places of +inf (or NaN) and -inf (or NaN)
+// first count what each token sees of them, and the values then go in with
+// these elements replaced by 0.
 template <typename V8>
-struct SplitValues {
-  V8 finite, up, down;
+struct Nonfinite {
+  V8 up, down;
 };
 
-__device__ __forceinline__ SplitValues<bf16x8> split_values(const bf16x8& v) {
-  SplitValues<bf16x8> r;
+template <typename V8>
+__device__ __forceinline__ Nonfinite<V8> take_nonfinite(V8& v) {
+  Nonfinite<V8> r;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float f = (float)v[e];
     const bool fin = fabsf(f) < __builtin_inff();
-    r.finite[e] = fin ? v[e] : (__bf16)0.f;
-    r.up[e] = (__bf16)(!fin && !(f < 0.f) ? 1.f : 0.f);
-    r.down[e] = (__bf16)(!fin && !(f > 0.f) ? 1.f : 0.f);
-  }
-  return r;
-}
-
-__device__ __forceinline__ SplitValues<f16x8> split_values(const f16x8& v) {
-  SplitValues<f16x8> r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float f = (float)v[e];
-    const bool fin = fabsf(f) < __builtin_inff();
-    r.finite[e] = fin ? v[e] : (_Float16)0.f;
-    r.up[e] = (_Float16)(!fin && !(f < 0.f) ? 1.f : 0.f);
-    r.down[e] = (_Float16)(!fin && !(f > 0.f) ? 1.f : 0.f);
+    r.up[e] = !fin && !(f < 0.f) ? 1.f : 0.f;
+    r.down[e] = !fin && !(f > 0.f) ? 1.f : 0.f;
+    if (!fin) v[e] = 0.f;
   }
   return r;
 }
@@ -109,6 +97,15 @@ __device__ __forceinline__ bool any_nonfinite_bf16(const u32x4& w) {
   return bad;
 }
 
+// any element of 8 fp16 (four words) infinite or NaN
+__device__ __forceinline__ bool any_nonfinite_f16(const u32x4& w) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad = bad || (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+  return bad;
+}
+
 // any of 16 e4m3 bytes NaN (0x7f or 0xff; e4m3 has no infinity)
 __device__ __forceinline__ bool any_nonfinite_fp8(const u32x4& w) {
   bool bad = false;
@@ -117,6 +114,16 @@ __device__ __forceinline__ bool any_nonfinite_fp8(const u32x4& w) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) bad = bad || ((w[i] >> (8 * e)) & 0x7fu) == 0x7fu;
   return bad;
+}
+
+// 16 e4m3 bytes with NaN replaced by 0
+__device__ __forceinline__ u32x4 drop_nonfinite_fp8(u32x4 w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (((w[i] >> (8 * e)) & 0x7fu) == 0x7fu) w[i] &= ~(0xffu << (8 * e));
+  return w;
 }
 
 }  // namespace tb

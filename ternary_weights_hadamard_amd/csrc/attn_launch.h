@@ -9,20 +9,49 @@ namespace tb {
 // Rows are the (token, head) pairs of one key/value head of one sequence.  A
 // sequence with few of them goes to the kernel for few rows, the others to
 // the chunk kernel; a launch's workgroups for sequences that are not its own
-// end at once.  Each kind's positions are split over its own number of parts.
-// A part's statistics and weighted values in the workspace, parts of all rows
-// after one another:
+// end at once.
+//
+// The positions that a workgroup's rows see are cut into parts of a fixed
+// length, so that sequences of different lengths give equal pieces of work;
+// only the last part of a launch's `splits` takes what is left.  A row tile
+// with one part is written by its kernel, the others are joined from the
+// workspace, where the parts of all rows lie after one another:
 //   values  float  [parts][rows][D]  (not divided by the sum)
 //   stats   float2 [parts][rows]     (maximum in log2 units, sum; no values are
 //                                     written or read where the sum is 0)
+struct AttnSplit {
+  int splits;  // most parts (the grid's)
+  int tiles;   // tiles of a part
+  // parts that a row tile with this many tiles of positions is cut into
+  __host__ __device__ int parts(int all) const {
+    const int p = (all + tiles - 1) / tiles;
+    return p < 1 ? 1 : p > splits ? splits : p;
+  }
+};
+
 struct AttnPlan {
-  int64_t few;  // most rows of the first kind
-  int64_t rows; // total_q * heads_q
-  int rows_splits, chunk_splits;
+  int64_t few;   // most rows of the first kind
+  int64_t rows;  // total_q * heads_q
+  AttnSplit by_rows, by_chunk;
   float* values;
   float2* stats;
-  __host__ __device__ bool by_chunk(int64_t nrows) const { return nrows > few; }
+  __host__ __device__ bool is_chunk(int64_t nrows) const { return nrows > few; }
 };
+
+constexpr int kRowsTile = 16;    // rows of a workgroup: few rows,
+constexpr int kChunkTile = 128;  // and chunks
+// positions of a tile: few rows (the cache's type), and chunks
+__host__ __device__ constexpr int rows_positions(bool fp8) { return fp8 ? 64 : 32; }
+constexpr int kChunkPositions = 64;
+
+// The tiles of positions that the rows r0 .. r0 + rows - 1 see: [first, first + count).
+struct TileSpan {
+  int first, count;
+};
+__device__ __forceinline__ TileSpan tile_span(const PagedSpan& p, int positions) {
+  const int first = p.begin / positions;
+  return TileSpan{first, p.end > p.begin ? (p.end + positions - 1) / positions - first : 0};
+}
 
 hipError_t launch_attn_rows(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream);
 hipError_t launch_attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream);

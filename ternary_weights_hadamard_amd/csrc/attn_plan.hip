@@ -20,7 +20,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args 
   const int64_t n = s.n < c.max_q ? s.n : c.max_q, nrows = n * group;
   const int64_t r = (int64_t)rt * 16 + (threadIdx.x >> 4);
   if (r >= nrows) return;
-  const int splits = plan.by_chunk(nrows) ? plan.chunk_splits : plan.rows_splits;
+  // the parts of the row's tile, as its kernel cut them
+  const bool chunk = plan.is_chunk(nrows);
+  const int64_t size = chunk ? kChunkTile : kRowsTile, r0 = r / size * size;
+  const int64_t rl = r0 + size - 1 < nrows ? r0 + size - 1 : nrows - 1;
+  const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(rl / group), a.window);
+  const TileSpan all = tile_span(span, chunk ? kChunkPositions : rows_positions(c.cache_dtype == TB_FP8));
+  const int splits = (chunk ? plan.by_chunk : plan.by_rows).parts(all.count);
   if (splits == 1) return;  // written by its kernel
   const int d0 = (threadIdx.x & 15) * DL;
   const int64_t at = (s.row0 + r / group) * a.heads_q + head * group + r % group;
@@ -48,12 +54,15 @@ __global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args 
   for (int e = 0; e < DL; e += 4) write4(a, at * D + d0 + e, f32x4{v[e], v[e + 1], v[e + 2], v[e + 3]}, rs);
 }
 
-// Parts that bring `items` workgroups to `want`, each with at least `least` positions; at most 64.
-int split_to(int64_t items, int64_t want, int64_t keys, int64_t least) {
-  int64_t s = items > 0 ? (want + items - 1) / items : 1;
-  const int64_t most = keys / least;
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+// Parts of the `keys` positions that bring `items` workgroups to about `want`:
+// at least `least` tiles each, at most 64 of them.
+AttnSplit split_to(int64_t items, int64_t want, int64_t keys, int positions, int least) {
+  const int64_t all = (keys + positions - 1) / positions;
+  int64_t tiles = (items * all + want - 1) / want;
+  if (tiles < least) tiles = least;
+  if (tiles < (all + 63) / 64) tiles = (all + 63) / 64;
+  const int64_t parts = (all + tiles - 1) / tiles;
+  return AttnSplit{(int)(parts < 1 ? 1 : parts), (int)tiles};
 }
 
 AttnPlan plan_of(const tb_paged_attention_args& a) {
@@ -62,10 +71,14 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   p.few = 32;
   p.rows = c.total_q * a.heads_q;
   const int64_t most = c.max_q * (a.heads_q / c.heads_kv);
-  const int64_t keys = a.window > 0 && a.window + c.max_q < a.max_kv ? a.window + c.max_q : a.max_kv;
+  int64_t keys = a.window > 0 && a.window + c.max_q < a.max_kv ? a.window + c.max_q : a.max_kv;
+  if (keys > TB_MAX_POSITIONS) keys = TB_MAX_POSITIONS;
   const int64_t few = most < p.few ? most : p.few;
-  p.rows_splits = split_to((few + 15) / 16 * c.heads_kv * c.B, 512, keys, c.cache_dtype == TB_FP8 ? 512 : 256);
-  p.chunk_splits = most > p.few ? split_to((most + 127) / 128 * c.heads_kv * c.B, 512, keys, 512) : 1;
+  p.by_rows = split_to((few + kRowsTile - 1) / kRowsTile * c.heads_kv * c.B, 1024, keys,
+                       rows_positions(c.cache_dtype == TB_FP8), 8);
+  p.by_chunk = AttnSplit{1, 1 << 30};
+  if (most > p.few)
+    p.by_chunk = split_to((most + kChunkTile - 1) / kChunkTile * c.heads_kv * c.B, 1024, keys, kChunkPositions, 8);
   return p;
 }
 
@@ -73,7 +86,7 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
 
 int attn_splits(const tb_paged_attention_args& a) {
   const AttnPlan p = plan_of(a);
-  return p.rows_splits > p.chunk_splits ? p.rows_splits : p.chunk_splits;
+  return p.by_rows.splits > p.by_chunk.splits ? p.by_rows.splits : p.by_chunk.splits;
 }
 
 size_t attn_part_bytes(const tb_paged_attention_args& a, int splits) {
@@ -85,7 +98,7 @@ hipError_t launch_paged_attention(const tb_paged_attention_args& a, int splits, 
   const tb_paged_cache& c = a.cache;
   AttnPlan p = plan_of(a);
   if (splits == 1) {
-    p.rows_splits = p.chunk_splits = 1;
+    p.by_rows.splits = p.by_chunk.splits = 1;
   } else {
     p.values = static_cast<float*>(a.workspace);
     p.stats = reinterpret_cast<float2*>(p.values + (int64_t)splits * p.rows * c.head_dim);

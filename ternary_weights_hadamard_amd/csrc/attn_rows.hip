@@ -51,12 +51,13 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attention_args a, AttnPlan plan) {
+__global__ void __launch_bounds__(64 * kWaves, 2) attn_rows_kernel(tb_paged_attention_args a, AttnPlan plan,
+                                                                  int row_tiles) {
   typedef Ops<FP8> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
   constexpr int NB = O::kBlocks;      // 32-position blocks of a tile
-  constexpr int T = 32 * NB;          // positions of a tile
+  constexpr int T = rows_positions(FP8);  // positions of a tile
   constexpr int S = 2 * NB;           // 16-row score tiles of a tile
   constexpr int KL = D / 32 / NB;     // 16-byte loads of a key row per lane
   constexpr int DT = D / 16;          // 16-row tiles of O'
@@ -65,20 +66,27 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
 
   const tb_paged_cache& c = a.cache;
   const int64_t b = blockIdx.z;
-  const int splits = plan.rows_splits;
-  const int split = blockIdx.x % (unsigned)splits, item = blockIdx.x / (unsigned)splits;
-  const int head = item % c.heads_kv, rt = item / c.heads_kv;
   const int group = a.heads_q / c.heads_kv;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, q4 = lane >> 4;
-
   const int64_t width = c.n_pages > 0 ? c.table_width : 0;
   const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
   const int64_t n = s.n < c.max_q ? s.n : c.max_q;
-  const int64_t nrows = n * group, r0 = (int64_t)rt * 16;
-  if (r0 >= nrows || plan.by_chunk(nrows)) return;
-  const int64_t rl = r0 + 15 < nrows ? r0 + 15 : nrows - 1;  // last row
+  const int64_t nrows = n * group;
+  // Consecutive workgroups go to the eight dies in turn; the row tiles of one
+  // (part, head) read the same positions, so they are eight apart.
+  const int eighth = blockIdx.x & 7, rest = blockIdx.x >> 3;
+  const int rt = rest % row_tiles, pair = rest / row_tiles * 8 + eighth;
+  const int head = pair % c.heads_kv, split = pair / c.heads_kv;
+  const int64_t r0 = (int64_t)rt * kRowsTile;
+  if (r0 >= nrows || split >= plan.by_rows.splits || plan.is_chunk(nrows)) return;
+  const int64_t rl = r0 + kRowsTile - 1 < nrows ? r0 + kRowsTile - 1 : nrows - 1;  // last row
   const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(rl / group), a.window);
+  const TileSpan all = tile_span(span, T);
+  const int parts = plan.by_rows.parts(all.count), first_tile = all.first;
+  if (split >= parts) return;
+  const int t_begin = split * plan.by_rows.tiles;
+  const int t_end = split + 1 == parts ? all.count : t_begin + plan.by_rows.tiles;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i16 = lane & 15, q4 = lane >> 4;
 
   // the lane's row
   const int64_t r = r0 + i16;
@@ -100,12 +108,6 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
     }
   }
   const float scale2 = a.scale * kLog2e * (FP8 && c.k_scale ? c.k_scale[head] : 1.f);
-
-  // the tiles of this workgroup
-  const int first_tile = span.begin / T, tiles = span.end > span.begin ? (span.end + T - 1) / T - first_tile : 0;
-  const int per = (tiles + splits - 1) / splits;
-  const int t_begin = split * per;
-  const int t_end = t_begin + per < tiles ? t_begin + per : tiles;
 
   const int32_t* table = c.block_table + b * c.table_stride;
   const int shift = __builtin_ctz(c.page);
@@ -230,69 +232,58 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
       for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
     }
 
-    bool bad = false;
     if (!full) {
+      bool bad = false;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) bad = bad || (FP8 ? any_nonfinite_fp8(vr[dt]) : any_nonfinite_bf16(vr[dt]));
-    }
-    if (__ballot(bad) == 0) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        // Weights are rounded to 11 bits (fp16: every e4m3 value is exact in
-        // it) or, for bf16 values, given as the sum of two bf16 numbers (16
-        // bits): the matrix unit has room, and one bf16 would add an error as
-        // large as the output's own rounding.
-        V8 w, rest;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = sc[2 * nb + (e >> 2)][e & 3];
-          if constexpr (FP8) {
-            w[e] = (_Float16)p;
-          } else {
-            w[e] = (__bf16)p;
-            rest[e] = (__bf16)(p - (float)w[e]);
-          }
-        }
+      if (__ballot(bad) != 0) {
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
-          if constexpr (FP8) {
-            o[dt] = mfma16(fp8_to_f16(u32x2{vr[dt][2 * nb], vr[dt][2 * nb + 1]}), w, o[dt]);
-          } else {
-            const bf16x8 v = __builtin_bit_cast(bf16x8, vr[dt]);
-            o[dt] = mfma16(v, w, o[dt]);
-            o[dt] = mfma16(v, rest, o[dt]);
-          }
-        }
-      }
-    } else {
-#pragma unroll 1
-      for (int nb = 0; nb < NB; ++nb) {
-        V8 w, rest, see;
+          f32x4 up = {0.f, 0.f, 0.f, 0.f}, down = up;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = NB == 2 && nb == 1 ? sc[S - 2 + (e >> 2)][e & 3] : sc[e >> 2][e & 3];
-          const bool k = (seen >> (8 * nb + e)) & 1u;
-          if constexpr (FP8) {
-            w[e] = (_Float16)p;
-            see[e] = (_Float16)(k ? 1.f : 0.f);
-          } else {
-            w[e] = (__bf16)p;
-            rest[e] = (__bf16)(p - (float)w[e]);
-            see[e] = (__bf16)(k ? 1.f : 0.f);
-          }
-        }
+          for (int nb = 0; nb < NB; ++nb) {
+            V8 v, see;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          V8 v;
-          if constexpr (FP8) v = fp8_to_f16(nb ? u32x2{vr[dt][2], vr[dt][3]} : u32x2{vr[dt][0], vr[dt][1]});
-          else v = __builtin_bit_cast(bf16x8, vr[dt]);
-          const SplitValues<V8> sv = split_values(v);
-          const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-          const f32x4 up = mfma16(sv.up, see, zero), down = mfma16(sv.down, see, zero);
-          o[dt] = mfma16(sv.finite, w, o[dt]);
-          if constexpr (!FP8) o[dt] = mfma16(sv.finite, rest, o[dt]);
+            for (int e = 0; e < 8; ++e) see[e] = (seen >> (8 * nb + e)) & 1u ? 1.f : 0.f;
+            if constexpr (FP8) v = fp8_to_f16(u32x2{vr[dt][2 * nb], vr[dt][2 * nb + 1]});
+            else v = __builtin_bit_cast(bf16x8, vr[dt]);
+            const Nonfinite<V8> nf = take_nonfinite(v);
+            up = mfma16(nf.up, see, up);
+            down = mfma16(nf.down, see, down);
+            if constexpr (!FP8) vr[dt] = __builtin_bit_cast(u32x4, v);
+          }
+          if constexpr (FP8) vr[dt] = drop_nonfinite_fp8(vr[dt]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[dt][e] += nonfinite_sum(up[e], down[e]);
+          __builtin_amdgcn_sched_barrier(0);  // one at a time: this path is rare, its registers are not to count
+        }
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      // Weights are rounded to 11 bits (fp16: every e4m3 value is exact in
+      // it) or, for bf16 values, given as the sum of two bf16 numbers (16
+      // bits): the matrix unit has room, and one bf16 would add an error as
+      // large as the output's own rounding.
+      V8 w, low_w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = sc[2 * nb + (e >> 2)][e & 3];
+        if constexpr (FP8) {
+          w[e] = (_Float16)p;
+        } else {
+          w[e] = (__bf16)p;
+          low_w[e] = (__bf16)(p - (float)w[e]);
+        }
+      }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        if constexpr (FP8) {
+          o[dt] = mfma16(fp8_to_f16(u32x2{vr[dt][2 * nb], vr[dt][2 * nb + 1]}), w, o[dt]);
+        } else {
+          const bf16x8 v = __builtin_bit_cast(bf16x8, vr[dt]);
+          o[dt] = mfma16(v, w, o[dt]);
+          o[dt] = mfma16(v, low_w, o[dt]);
         }
       }
     }
@@ -333,7 +324,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_rows_kernel(tb_paged_attenti
     for (int w = 0; w < kWaves; ++w) v[e] += sm_o[w][orow][d0 + e];
   }
   const int64_t at = (s.row0 + (r0 + orow) / group) * a.heads_q + head * group + (r0 + orow) % group;
-  if (splits > 1) {
+  if (parts > 1) {
     const int64_t pr = (int64_t)split * plan.rows + at;
     if (d0 == 0) plan.stats[pr] = float2{top, total};
     if (total == 0.f) return;
@@ -353,14 +344,16 @@ hipError_t launch_attn_rows(const tb_paged_attention_args& a, const AttnPlan& pl
   const tb_paged_cache& c = a.cache;
   int64_t rows = c.max_q * (a.heads_q / c.heads_kv);
   if (rows > plan.few) rows = plan.few;
-  const dim3 grid((unsigned)((rows + 15) / 16 * c.heads_kv * plan.rows_splits), 1, (unsigned)c.B), block(64 * kWaves);
+  const int row_tiles = (int)((rows + kRowsTile - 1) / kRowsTile);
+  const int64_t pairs = (int64_t)c.heads_kv * plan.by_rows.splits;
+  const dim3 grid((unsigned)((pairs + 7) / 8 * 8 * row_tiles), 1, (unsigned)c.B), block(64 * kWaves);
   const bool f8 = c.cache_dtype == TB_FP8;
   if (c.head_dim == 64) {
-    if (f8) hipLaunchKernelGGL((attn_rows_kernel<64, true>), grid, block, 0, stream, a, plan);
-    else hipLaunchKernelGGL((attn_rows_kernel<64, false>), grid, block, 0, stream, a, plan);
+    if (f8) hipLaunchKernelGGL((attn_rows_kernel<64, true>), grid, block, 0, stream, a, plan, row_tiles);
+    else hipLaunchKernelGGL((attn_rows_kernel<64, false>), grid, block, 0, stream, a, plan, row_tiles);
   } else {
-    if (f8) hipLaunchKernelGGL((attn_rows_kernel<128, true>), grid, block, 0, stream, a, plan);
-    else hipLaunchKernelGGL((attn_rows_kernel<128, false>), grid, block, 0, stream, a, plan);
+    if (f8) hipLaunchKernelGGL((attn_rows_kernel<128, true>), grid, block, 0, stream, a, plan, row_tiles);
+    else hipLaunchKernelGGL((attn_rows_kernel<128, false>), grid, block, 0, stream, a, plan, row_tiles);
   }
   return hipGetLastError();
 }
