@@ -14,17 +14,14 @@
 // overlapping them: two workgroups of four waves per CU, a tile of 64
 // positions of K and V double buffered in LDS and loaded by the
 // global-to-LDS path while the tile before it is worked on.
-#include "attn_common.h"
-#include "attn_launch.h"
+#pragma once
+
+#include "attn_rows.h"
 
 namespace tb {
 
-namespace {
-
-constexpr int kWaves = 4;
-constexpr int kRows = kChunkTile;       // rows of a workgroup: 32 a wave
-constexpr int kTile = kChunkPositions;  // positions of a tile
-static_assert(kRows == 32 * kWaves && kTile == 64, "the lane layouts below");
+constexpr int kTile = kChunkPositions;
+static_assert(kChunkTile == 32 * kAttnWaves && kTile == 64, "the lane layouts below");
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -34,15 +31,15 @@ __device__ __forceinline__ f32x16 mfma32(const f16x8& a, const f16x8& b, const f
 }
 
 template <bool FP8>
-struct Value;
+struct ChunkOps;
 template <>
-struct Value<false> {
+struct ChunkOps<false> {
   typedef uint16_t Elem;
   typedef bf16x8 V8;
   static __device__ __forceinline__ __bf16 narrow(float x) { return (__bf16)x; }
 };
 template <>
-struct Value<true> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
+struct ChunkOps<true> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
   typedef uint8_t Elem;
   typedef f16x8 V8;
   static __device__ __forceinline__ _Float16 narrow(float x) { return (_Float16)x; }
@@ -58,32 +55,38 @@ __device__ __forceinline__ int k_chunk(int row, int c) {
 }
 __device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ (row & 7)); }
 
+template <int D>
+struct ChunkShared {
+  u32x4 tile[2][2][kTile * D / 8];  // [buffer][K, V][16-byte chunk]
+};
+
+// Workgroup `block` of the chunks of sequence b.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_attention_args a, AttnPlan plan) {
-  typedef typename Value<FP8>::Elem Elem;
-  typedef typename Value<FP8>::V8 V8;
+__device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block,
+                                           int64_t b, ChunkShared<D>& sm) {
+  typedef typename ChunkOps<FP8>::Elem Elem;
+  typedef typename ChunkOps<FP8>::V8 V8;
   constexpr int KK = D / 16;   // steps of a score tile
   constexpr int DT = D / 32;   // 32-channel tiles of O'
   constexpr int kChunks = kTile * D / 8;  // 16-byte chunks of a tile of K, and of V
-  __shared__ __align__(16) u32x4 lds[2][2][kChunks];
+  constexpr int kWaves = kAttnWaves, kRows = kChunkTile;
+  auto& lds = sm.tile;
 
   const tb_paged_cache& c = a.cache;
-  const int64_t b = blockIdx.z;
-  const int group = a.heads_q / c.heads_kv;
-  const int64_t width = c.n_pages > 0 ? c.table_width : 0;
-  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, width * c.page);
-  const int64_t n = s.n < c.max_q ? s.n : c.max_q;
-  const int64_t nrows = n * group;
+  const int group = plan.group;
+  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, plan.capacity);
+  const int nrows = (s.n < (int)c.max_q ? s.n : (int)c.max_q) * group;
   if (!plan.is_chunk(nrows)) return;
-  const int split = blockIdx.x % (unsigned)plan.by_chunk.splits, item = blockIdx.x / (unsigned)plan.by_chunk.splits;
-  const int head = item % c.heads_kv;
+  const unsigned item = block / (unsigned)plan.by_chunk.splits;
+  const int split = block - item * plan.by_chunk.splits;
+  const int head = item % (unsigned)c.heads_kv;
   // the last rows see the most positions: they go first
-  const int64_t row_tiles = (nrows + kRows - 1) / kRows;
-  const int64_t rt = row_tiles - 1 - item / c.heads_kv;
+  const int rt = (nrows + kRows - 1) / kRows - 1 - (int)(item / (unsigned)c.heads_kv);
   if (rt < 0) return;
-  const int64_t r0 = rt * kRows;
-  const int64_t r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
-  const PagedSpan span = paged_span(s, (int)(r0 / group), (int)(r_last / group), a.window);
+  const int r0 = rt * kRows;
+  const int r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
+  const int j_first = (unsigned)r0 / (unsigned)group, j_last = (unsigned)r_last / (unsigned)group;
+  const PagedSpan span = paged_span(s, j_first, j_last, a.window);
   const TileSpan all = tile_span(span, kTile);
   const int parts = plan.by_chunk.parts(all.count), first_tile = all.first;
   if (split >= parts) return;
@@ -94,17 +97,18 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   const int i32 = lane & 31, half = lane >> 5;
 
   // the lane's row, and its wave's first and last
-  const int64_t r = r0 + wave * 32 + i32;
+  const int r = r0 + wave * 32 + i32;
   const bool row_live = r < nrows;
-  const int tok = row_live ? (int)(r / group) : 0;
-  const int hq = head * group + (row_live ? (int)(r % group) : 0);
-  const int64_t pos = (int64_t)s.first_pos + tok;
-  const int64_t low = a.window > 0 ? pos - a.window : -1;
-  const int64_t w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
-  const int64_t w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
-  const int64_t pos_first = (int64_t)s.first_pos + w_first / group, pos_last = (int64_t)s.first_pos + w_last / group;
+  const int tok = row_live ? (int)((unsigned)r / (unsigned)group) : 0;
+  const int hq = head * group + (row_live ? r - tok * group : 0);
+  const int pos = s.first_pos + tok;
+  const int64_t low = a.window > 0 ? (int64_t)pos - a.window : -1;
+  const int w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
+  const int w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
+  const int pos_first = s.first_pos + (int)((unsigned)w_first / (unsigned)group);
+  const int pos_last = s.first_pos + (int)((unsigned)w_last / (unsigned)group);
   // and of the workgroup
-  const int64_t all_first = (int64_t)s.first_pos + r0 / group, all_last = (int64_t)s.first_pos + r_last / group;
+  const int all_first = s.first_pos + j_first, all_last = s.first_pos + j_last;
 
   // scores are scaled by |scale|; its sign goes into the queries.  A scale of
   // 0 is taken as the smallest number, so that an unseen -inf stays one.
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
   }
 
   const int32_t* table = c.block_table + b * c.table_stride;
-  const int shift = __builtin_ctz(c.page);
+  const int shift = plan.shift;
   const int64_t page_elems = (int64_t)c.page * D, page_step = (int64_t)c.heads_kv * page_elems;
   const Elem* kc = static_cast<const Elem*>(c.k_cache) + head * page_elems;
   const Elem* vc = static_cast<const Elem*>(c.v_cache) + head * page_elems;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
       for (int kb = 0; kb < 4; ++kb) {
         V8 w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = Value<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
+        for (int e = 0; e < 8; ++e) w[e] = ChunkOps<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
           o[dt] = mfma32(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
@@ -368,23 +372,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) attn_chunk_kernel(tb_paged_att
     for (int j = 0; j < 4; ++j)
       write4(a, at * D + 32 * dt + 8 * j + 4 * half,
              f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]}, rs);
-}
-
-}  // namespace
-
-hipError_t launch_attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream) {
-  const tb_paged_cache& c = a.cache;
-  const int64_t row_tiles = (c.max_q * (a.heads_q / c.heads_kv) + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(row_tiles * c.heads_kv * plan.by_chunk.splits), 1, (unsigned)c.B), block(64 * kWaves);
-  const bool f8 = c.cache_dtype == TB_FP8;
-  if (c.head_dim == 64) {
-    if (f8) hipLaunchKernelGGL((attn_chunk_kernel<64, true>), grid, block, 0, stream, a, plan);
-    else hipLaunchKernelGGL((attn_chunk_kernel<64, false>), grid, block, 0, stream, a, plan);
-  } else {
-    if (f8) hipLaunchKernelGGL((attn_chunk_kernel<128, true>), grid, block, 0, stream, a, plan);
-    else hipLaunchKernelGGL((attn_chunk_kernel<128, false>), grid, block, 0, stream, a, plan);
-  }
-  return hipGetLastError();
 }
 
 }  // namespace tb

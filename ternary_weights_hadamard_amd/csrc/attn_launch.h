@@ -1,5 +1,4 @@
-// The plan of a tb_paged_attention call, the kernels it launches, and the
-// output of a row.
+// The plan of a tb_paged_attention call and the output of a row.
 #pragma once
 
 #include "attn_common.h"
@@ -11,14 +10,15 @@ namespace tb {
 // the chunk kernel; a launch's workgroups for sequences that are not its own
 // end at once.
 //
-// The positions that a workgroup's rows see are cut into parts of a fixed
-// length, so that sequences of different lengths give equal pieces of work;
-// only the last part of a launch's `splits` takes what is left.  A row tile
-// with one part is written by its kernel, the others are joined from the
-// workspace, where the parts of all rows lie after one another:
-//   values  float  [parts][rows][D]  (not divided by the sum)
-//   stats   float2 [parts][rows]     (maximum in log2 units, sum; no values are
-//                                     written or read where the sum is 0)
+// Chunks: the positions that a row tile sees are cut into parts of a fixed
+// length (the last part of a launch's `splits` takes what is left).  Few rows:
+// all tiles of all items stand in one line that is cut into equal pieces, each
+// with the parts of at most two items.  An item in one part is written by its
+// kernel, the others are joined from the workspace:
+//   values, stats            [part][row]: of chunks, row of total_q * heads_q
+//   rows_values, rows_stats  [2 pieces + 0 or 1][row of the item]
+// with D floats (not divided by the sum) and a float2 (maximum in log2 units,
+// sum) a row.  A chunk's part with a sum of 0 has no values.
 struct AttnSplit {
   int splits;  // most parts (the grid's)
   int tiles;   // tiles of a part
@@ -30,12 +30,24 @@ struct AttnSplit {
 };
 
 struct AttnPlan {
-  int64_t few;   // most rows of the first kind
-  int64_t rows;  // total_q * heads_q
-  AttnSplit by_rows, by_chunk;
-  float* values;
-  float2* stats;
+  int64_t few;       // most rows of the first kind
+  int64_t rows;      // total_q * heads_q
+  int64_t capacity;  // positions that the table has room for
+  int group;         // query heads of a key/value head
+  int shift;         // log2 of a page's positions
+  int pieces;        // workgroups of the first kind; 0: one for each item, in one part
+  int least;         // tiles of a piece
+  int slot_rows;     // rows of a slot of the workspace
+  unsigned chunk_blocks;  // workgroups of the second kind for each sequence
+  AttnSplit by_chunk;
+  float *values, *rows_values;
+  float2 *stats, *rows_stats;
   __host__ __device__ bool is_chunk(int64_t nrows) const { return nrows > few; }
+  // tiles of a piece of a line of `total`
+  __host__ __device__ int64_t piece(int64_t total) const {
+    const int64_t per = (total + pieces - 1) / pieces;
+    return per < least ? least : per;
+  }
 };
 
 constexpr int kRowsTile = 16;    // rows of a workgroup: few rows,
@@ -52,9 +64,6 @@ __device__ __forceinline__ TileSpan tile_span(const PagedSpan& p, int positions)
   const int first = p.begin / positions;
   return TileSpan{first, p.end > p.begin ? (p.end + positions - 1) / positions - first : 0};
 }
-
-hipError_t launch_attn_rows(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream);
-hipError_t launch_attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, hipStream_t stream);
 
 // What a row's weighted values are multiplied with; its log-sum-exp is
 // written on the way (`first`: by the one lane that does).

@@ -48,9 +48,8 @@ constexpr int64_t kVerifySlice = 2048;
 hipError_t launch_verify_draft(const tb_verify_draft_args& a, hipStream_t stream);
 hipError_t launch_paged_append(const tb_paged_cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                                int64_t v_stride, hipStream_t stream);
-// parts the positions are split into when the workspace allows (1: none), and their bytes
-int attn_splits(const tb_paged_attention_args& a);
-size_t attn_part_bytes(const tb_paged_attention_args& a, int splits);
-hipError_t launch_paged_attention(const tb_paged_attention_args& a, int splits, hipStream_t stream);
+// bytes of the workspace that positions are split with (0: none is used)
+size_t attn_part_bytes(const tb_paged_attention_args& a);
+hipError_t launch_paged_attention(const tb_paged_attention_args& a, bool split, hipStream_t stream);
 
 }  // namespace tb

@@ -152,7 +152,7 @@ size_t tb_paged_attention_workspace(const tb_paged_attention_args* args) {
   if (!args || check_attention_sizes(*args) != TB_OK) return 0;
   const tb_paged_cache& c = args->cache;
   if (c.B == 0 || c.total_q == 0 || c.max_q == 0) return 0;
-  return attn_part_bytes(*args, attn_splits(*args));
+  return attn_part_bytes(*args);
 }
 
 tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream) {
@@ -165,12 +165,11 @@ tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream) 
   if (st != TB_OK) return st;
   if (!a.q || !a.out) return TB_ERR_NULL;
   if (!aligned16(a.q) || !aligned16(a.out) || !aligned16(a.workspace) || !aligned4(a.lse)) return TB_ERR_ALIGN;
-  int splits = attn_splits(a);
-  const size_t need = attn_part_bytes(a, splits);
-  if (need && (!a.workspace || a.workspace_bytes < need)) splits = 1;
+  const size_t need = attn_part_bytes(a);
+  const bool split = need > 0 && a.workspace && a.workspace_bytes >= need;
   const size_t cb = cache_bytes(c), rows = (size_t)c.total_q * (size_t)a.heads_q;
   const Range out{a.out, rows * c.head_dim * dtype_bytes(a.out_dtype)}, lse{a.lse, rows * 4};
-  const Range ws{a.workspace, splits > 1 ? need : 0};
+  const Range ws{a.workspace, split ? need : 0};
   const Range ins[] = {{c.k_cache, cb},
                        {c.v_cache, cb},
                        {a.q, strided_bytes(c.total_q, a.q_stride, (int64_t)a.heads_q * c.head_dim, 2)},
@@ -183,7 +182,7 @@ tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream) 
       overlap(out.p, out.bytes, lse.p, lse.bytes) || overlap(ws.p, ws.bytes, out.p, out.bytes) ||
       overlap(ws.p, ws.bytes, lse.p, lse.bytes))
     return TB_ERR_ALIAS;
-  return launched(launch_paged_attention(a, splits, as_stream(stream)));
+  return launched(launch_paged_attention(a, split, as_stream(stream)));
 }
 
 size_t tb_verify_draft_workspace(int64_t B, int64_t vocab) {
