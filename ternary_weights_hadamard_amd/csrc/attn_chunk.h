@@ -60,10 +60,12 @@ struct ChunkShared {
   u32x4 tile[2][2][kTile * D / 8];  // [buffer][K, V][16-byte chunk]
 };
 
-// Workgroup `block` of the chunks of sequence b.
+// Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
+// it), or a part of it into the workspace's slot.
 template <int D, bool FP8>
-__device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block,
-                                           int64_t b, ChunkShared<D>& sm) {
+__device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                                const LineItem& it, int t_begin, int t_stop, int64_t slot,
+                                                ChunkShared<D>& sm) {
   typedef typename ChunkOps<FP8>::Elem Elem;
   typedef typename ChunkOps<FP8>::V8 V8;
   constexpr int KK = D / 16;   // steps of a score tile
@@ -73,27 +75,14 @@ __device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, con
   auto& lds = sm.tile;
 
   const tb_paged_cache& c = a.cache;
-  const int group = plan.group;
-  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, plan.capacity);
-  const int nrows = (s.n < (int)c.max_q ? s.n : (int)c.max_q) * group;
-  if (!plan.is_chunk(nrows)) return;
-  const unsigned item = block / (unsigned)plan.by_chunk.splits;
-  const int split = block - item * plan.by_chunk.splits;
-  const int head = item % (unsigned)c.heads_kv;
-  // the last rows see the most positions: they go first
-  const int rt = (nrows + kRows - 1) / kRows - 1 - (int)(item / (unsigned)c.heads_kv);
-  if (rt < 0) return;
-  const int r0 = rt * kRows;
+  const int group = plan.group, head = it.head, nrows = it.seq.rows;
+  const PagedSeq& s = it.seq.seq;
+  const PagedSpan& span = it.span;
+  const int r0 = it.rt * kRows;
   const int r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
-  const int j_first = (unsigned)r0 / (unsigned)group, j_last = (unsigned)r_last / (unsigned)group;
-  const PagedSpan span = paged_span(s, j_first, j_last, a.window);
-  const TileSpan all = tile_span(span, kTile);
-  const int parts = plan.by_chunk.parts(all.count), first_tile = all.first;
-  if (split >= parts) return;
-  const int t_begin = split * plan.by_chunk.tiles;
-  const int t_end = split + 1 == parts ? all.count : t_begin + plan.by_chunk.tiles;
-
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j_first = uniform((unsigned)r0 / (unsigned)group), j_last = uniform((unsigned)r_last / (unsigned)group);
+  const int first_tile = it.held.first, t_end = t_stop < it.held.count ? t_stop : it.held.count;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int i32 = lane & 31, half = lane >> 5;
 
   // the lane's row, and its wave's first and last
@@ -105,8 +94,8 @@ __device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, con
   const int64_t low = a.window > 0 ? (int64_t)pos - a.window : -1;
   const int w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
   const int w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
-  const int pos_first = s.first_pos + (int)((unsigned)w_first / (unsigned)group);
-  const int pos_last = s.first_pos + (int)((unsigned)w_last / (unsigned)group);
+  const int pos_first = uniform(s.first_pos + (int)((unsigned)w_first / (unsigned)group));
+  const int pos_last = uniform(s.first_pos + (int)((unsigned)w_last / (unsigned)group));
   // and of the workgroup
   const int all_first = s.first_pos + j_first, all_last = s.first_pos + j_last;
 
@@ -129,7 +118,7 @@ __device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, con
     }
   }
 
-  const int32_t* table = c.block_table + b * c.table_stride;
+  const int32_t* table = c.block_table + it.b * c.table_stride;
   const int shift = plan.shift;
   const int64_t page_elems = (int64_t)c.page * D, page_step = (int64_t)c.heads_kv * page_elems;
   const Elem* kc = static_cast<const Elem*>(c.k_cache) + head * page_elems;
@@ -353,15 +342,14 @@ __device__ __forceinline__ void attn_chunk(const tb_paged_attention_args& a, con
   }
   if (!row_live) return;
   const int64_t at = (s.row0 + tok) * a.heads_q + hq;
-  if (parts > 1) {
-    const int64_t pr = (int64_t)split * plan.rows + at;
-    if (half == 0) plan.stats[pr] = float2{m, l};
-    if (l == 0.f) return;
+  if (slot >= 0) {
+    const int64_t pr = slot * kRows + (r - r0);
+    if (half == 0) plan.chunk_line.stats[pr] = float2{m, l};
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(plan.values + pr * D + 32 * dt + 8 * j + 4 * half) =
+        *reinterpret_cast<f32x4*>(plan.chunk_line.values + pr * D + 32 * dt + 8 * j + 4 * half) =
             f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
     return;
   }

@@ -5,58 +5,42 @@
 
 namespace tb {
 
-// Rows are the (token, head) pairs of one key/value head of one sequence.  A
-// sequence with few of them goes to the kernel for few rows, the others to
-// the chunk kernel; a launch's workgroups for sequences that are not its own
-// end at once.
-//
-// Chunks: the positions that a row tile sees are cut into parts of a fixed
-// length (the last part of a launch's `splits` takes what is left).  Few rows:
-// all tiles of all items stand in one line that is cut into equal pieces, each
-// with the parts of at most two items.  An item in one part is written by its
-// kernel, the others are joined from the workspace:
-//   values, stats            [part][row]: of chunks, row of total_q * heads_q
-//   rows_values, rows_stats  [2 pieces + 0 or 1][row of the item]
-// with D floats (not divided by the sum) and a float2 (maximum in log2 units,
-// sum) a row.  A chunk's part with a sum of 0 has no values.
-struct AttnSplit {
-  int splits;  // most parts (the grid's)
-  int tiles;   // tiles of a part
-  // parts that a row tile with this many tiles of positions is cut into
-  __host__ __device__ int parts(int all) const {
-    const int p = (all + tiles - 1) / tiles;
-    return p < 1 ? 1 : p > splits ? splits : p;
+// A sequence with few rows (attn_line.h) goes to the kernel for those, the
+// others to the chunk kernel.  Parts in the workspace, for each kind:
+//   values  float  [2 pieces][rows of a row tile][D]  (not divided by the sum)
+//   stats   float2 [2 pieces][rows of a row tile]     (maximum in log2 units, sum)
+struct AttnLine {
+  int pieces;     // workgroups; 0: one for each item, none is in parts
+  int least;      // tiles of a piece
+  int row_tiles;  // most of a sequence
+  int slot_rows;  // rows of a slot
+  float* values;
+  float2* stats;
+  // tiles of a piece of a line of `total`
+  __host__ __device__ int64_t piece(int64_t total) const {
+    const int64_t sum = total + pieces - 1;
+    const int64_t per = sum >> 32 == 0 ? (int64_t)((uint32_t)sum / (uint32_t)pieces) : sum / pieces;
+    return per < least ? least : per;
   }
 };
 
 struct AttnPlan {
   int64_t few;       // most rows of the first kind
-  int64_t rows;      // total_q * heads_q
   int64_t capacity;  // positions that the table has room for
   int group;         // query heads of a key/value head
   int shift;         // log2 of a page's positions
-  int pieces;        // workgroups of the first kind; 0: one for each item, in one part
-  int least;         // tiles of a piece
-  int slot_rows;     // rows of a slot of the workspace
-  unsigned chunk_blocks;  // workgroups of the second kind for each sequence
-  AttnSplit by_chunk;
-  float *values, *rows_values;
-  float2 *stats, *rows_stats;
+  unsigned chunk_blocks;  // workgroups of chunks: they come first
+  AttnLine rows_line, chunk_line;
   __host__ __device__ bool is_chunk(int64_t nrows) const { return nrows > few; }
-  // tiles of a piece of a line of `total`
-  __host__ __device__ int64_t piece(int64_t total) const {
-    const int64_t per = (total + pieces - 1) / pieces;
-    return per < least ? least : per;
-  }
 };
 
-constexpr int kRowsTile = 16;    // rows of a workgroup: few rows,
+constexpr int kRowsTile = 16;    // rows of a row tile: few rows,
 constexpr int kChunkTile = 128;  // and chunks
 // positions of a tile: few rows (the cache's type), and chunks
 __host__ __device__ constexpr int rows_positions(bool fp8) { return fp8 ? 64 : 32; }
 constexpr int kChunkPositions = 64;
 
-// The tiles of positions that the rows r0 .. r0 + rows - 1 see: [first, first + count).
+// The tiles that hold a span's positions: first .. first + count - 1.
 struct TileSpan {
   int first, count;
 };

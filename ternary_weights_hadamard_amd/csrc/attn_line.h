@@ -1,0 +1,245 @@
+// How the work of a tb_paged_attention call is cut.
+//
+// Rows are the (token, head) pairs of one key/value head of one sequence, in
+// tiles; positions are in tiles too.  An item is one row tile of one key/value
+// head of one sequence: it reads the position tiles that some of its rows see.
+// The tiles of all items of a kind stand in one line, ordered by sequence, row
+// tile and head, and the line is cut into equal pieces, one for each workgroup
+// that the GPU holds, so that batches of mixed lengths end everywhere at once.
+// A piece covers some items whole, which it writes, and parts of at most two,
+// which go to the workspace and are joined by a second launch.  Nothing is
+// read back to the host: every workgroup finds its piece from cu_q and kv_len.
+#pragma once
+
+#include "attn_launch.h"
+
+namespace tb {
+
+// a value that is the same in every lane, in scalar registers
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// A sequence as one kind sees it.
+struct LineSeq {
+  PagedSeq seq;
+  int rows;  // 0: it is of the other kind
+};
+
+template <bool CHUNK, bool FP8>
+struct LineKind {
+  static constexpr int kRows = CHUNK ? kChunkTile : kRowsTile;
+  static constexpr int kPositions = CHUNK ? kChunkPositions : rows_positions(FP8);
+
+  static __device__ __forceinline__ LineSeq sequence(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b) {
+    const tb_paged_cache& c = a.cache;
+    LineSeq s;
+    s.seq = paged_seq(c.cu_q, c.kv_len, b, c.total_q, plan.capacity);
+    const int rows = (s.seq.n < (int)c.max_q ? s.seq.n : (int)c.max_q) * plan.group;
+    s.rows = plan.is_chunk(rows) == CHUNK ? rows : 0;
+    return s;
+  }
+  static __device__ __forceinline__ PagedSpan span(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                                   const LineSeq& s, int rt) {
+    const int r0 = rt * kRows, rl = r0 + kRows - 1 < s.rows ? r0 + kRows - 1 : s.rows - 1;
+    return paged_span(s.seq, (unsigned)r0 / (unsigned)plan.group, (unsigned)rl / (unsigned)plan.group, a.window);
+  }
+  // Tiles of the row tile's items in the line: those that hold a position it
+  // sees, or one (empty) in which its rows are written.
+  static __device__ __forceinline__ int tiles(const tb_paged_attention_args& a, const AttnPlan& plan, const LineSeq& s,
+                                              int rt) {
+    const int n = tile_span(span(a, plan, s, rt), kPositions).count;
+    return n > 1 ? n : 1;
+  }
+  // of all row tiles of the sequence, for one head
+  static __device__ __forceinline__ int64_t tiles(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                                  const LineSeq& s) {
+    int64_t n = 0;
+    for (int rt = 0; rt * kRows < s.rows; ++rt) n += tiles(a, plan, s, rt);
+    return n;
+  }
+};
+
+struct LineItem {
+  int64_t start;  // of its first tile in the line
+  int tiles;      // in the line
+  int64_t b;
+  int rt, head;
+  LineSeq seq;
+  PagedSpan span;
+  TileSpan held;  // the tiles that hold a position some row sees
+};
+
+// an item, the same in every lane, in scalar registers
+__device__ __forceinline__ LineItem uniform_item(const LineItem& x) {
+  LineItem r;
+  r.start = uniform64(x.start);
+  r.tiles = uniform(x.tiles);
+  r.b = uniform64(x.b);
+  r.rt = uniform(x.rt);
+  r.head = uniform(x.head);
+  r.seq.seq.row0 = uniform64(x.seq.seq.row0);
+  r.seq.seq.n = uniform(x.seq.seq.n);
+  r.seq.seq.keys = uniform(x.seq.seq.keys);
+  r.seq.seq.first_pos = uniform(x.seq.seq.first_pos);
+  r.seq.rows = uniform(x.seq.rows);
+  r.span.begin = uniform(x.span.begin);
+  r.span.end = uniform(x.span.end);
+  r.held.first = uniform(x.held.first);
+  r.held.count = uniform(x.held.count);
+  return r;
+}
+
+// The line of one kind.  Whole waves use it together, with the same arguments
+// in every lane.
+template <bool CHUNK, bool FP8>
+struct Line {
+  typedef LineKind<CHUNK, FP8> K;
+  LineSeq own;    // of sequence b0 + lane, of the last 64 looked at
+  int64_t up;     // tiles of the sequences b0 .. b0 + lane
+  int64_t total;  // tiles of the line
+
+  __device__ __forceinline__ void look(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b0) {
+    const int lane = threadIdx.x & 63;
+    own.rows = 0;
+    up = 0;
+    if (b0 + lane < a.cache.B) {
+      own = K::sequence(a, plan, b0 + lane);
+      up = K::tiles(a, plan, own) * a.cache.heads_kv;
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int64_t t = __shfl_up(up, m);
+      if (lane >= m) up += t;
+    }
+  }
+  __device__ __forceinline__ Line(const tb_paged_attention_args& a, const AttnPlan& plan) {
+    total = 0;
+    for (int64_t b0 = 0; b0 < a.cache.B; b0 += 64) {
+      look(a, plan, b0);
+      total += lane64(up, 63);
+    }
+  }
+  // nothing looked at yet: only find(.., true) may be called
+  __device__ __forceinline__ Line() : up(0), total(0) {}
+  // The item that holds tile `at` < total.
+  __device__ __forceinline__ LineItem find(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at,
+                                           bool again = false) {
+    LineItem it{};
+    int64_t before = 0;
+    for (int64_t b0 = 0; b0 < a.cache.B; b0 += 64) {
+      if (again || a.cache.B > 64) look(a, plan, b0);  // else it holds them since it was made
+      const uint64_t past = __ballot(before + up > at);
+      if (past != 0) {
+        const int l = uniform(__builtin_ctzll(past));
+        it.b = b0 + l;
+        it.start = before + (l > 0 ? lane64(up, l - 1) : 0);
+        it.seq.rows = __builtin_amdgcn_readlane(own.rows, l);
+        it.seq.seq.row0 = lane64(own.seq.row0, l);
+        it.seq.seq.n = __builtin_amdgcn_readlane(own.seq.n, l);
+        it.seq.seq.keys = __builtin_amdgcn_readlane(own.seq.keys, l);
+        it.seq.seq.first_pos = __builtin_amdgcn_readlane(own.seq.first_pos, l);
+        break;
+      }
+      before += lane64(up, 63);
+    }
+    const int64_t heads = a.cache.heads_kv;
+    for (it.rt = 0;; ++it.rt) {
+      it.tiles = K::tiles(a, plan, it.seq, it.rt);
+      if (at - it.start < heads * it.tiles) break;
+      it.start += heads * it.tiles;
+    }
+    it.head = (int)((unsigned)(at - it.start) / (unsigned)it.tiles);  // heads * tiles of one row tile: 32 bits
+    it.start += (int64_t)it.head * it.tiles;
+    it.span = K::span(a, plan, it.seq, it.rt);
+    it.held = tile_span(it.span, K::kPositions);
+    return uniform_item(it);
+  }
+  // Where the items of sequence b start.
+  __device__ __forceinline__ int64_t before(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b) {
+    int64_t n = 0;
+    for (int64_t b0 = 0; b0 <= b; b0 += 64) {
+      if (a.cache.B > 64) look(a, plan, b0);
+      if (b - b0 < 64) return n + (b > b0 ? lane64(up, (int)(b - b0) - 1) : 0);
+      n += lane64(up, 63);
+    }
+    return n;
+  }
+};
+
+// The parts of the item whose tiles stand at start .. start + tiles - 1 of a
+// line of pieces of `per` tiles.
+struct LineParts {
+  int64_t first;  // piece
+  int count;
+  int64_t slot0;  // of the first part; part p > 0 has slot 2 (first + p)
+  __device__ __forceinline__ int64_t slot(int p) const { return p == 0 ? slot0 : 2 * (first + p); }
+};
+__device__ __forceinline__ LineParts line_parts(int64_t start, int tiles, int64_t per) {
+  LineParts r;
+  const int64_t last = start + tiles - 1;
+  if (last >> 32 == 0 && per >> 32 == 0) {  // 64-bit divisions are long
+    r.first = (uint32_t)start / (uint32_t)per;
+    r.count = (int)((uint32_t)last / (uint32_t)per - (uint32_t)r.first) + 1;
+  } else {
+    r.first = start / per;
+    r.count = (int)(last / per - r.first) + 1;
+  }
+  // a piece's first part has slot 2 piece, the part it ends with slot 2 piece + 1
+  r.slot0 = 2 * r.first + (r.first * per < start ? 1 : 0);
+  return r;
+}
+
+// What a workgroup does: all parts of its piece of the line, or, if the line is
+// not cut, its item.  part(item, t0, t1, slot) does tiles t0 .. t1 - 1 of an
+// item, all of them if slot < 0; LDS is free for it when it is called.
+template <bool CHUNK, bool FP8, typename F>
+__device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block, F part) {
+  typedef LineKind<CHUNK, FP8> K;
+  const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
+  if (cut.pieces == 0) {
+    LineItem it{};
+    const unsigned heads = (unsigned)a.cache.heads_kv, row_tiles = (unsigned)cut.row_tiles;
+    it.head = block % heads;
+    it.b = block / heads / row_tiles;
+    it.seq = K::sequence(a, plan, it.b);
+    // the last rows of a sequence see the most positions: they go first
+    it.rt = (it.seq.rows + K::kRows - 1) / K::kRows - 1 - (int)(block / heads % row_tiles);
+    if (it.rt < 0 || it.seq.rows == 0) return;
+    it.span = K::span(a, plan, it.seq, it.rt);
+    it.held = tile_span(it.span, K::kPositions);
+    it.tiles = it.held.count > 1 ? it.held.count : 1;
+    it = uniform_item(it);
+    part(it, 0, it.tiles, (int64_t)-1);
+    return;
+  }
+  LineItem it;
+  int64_t at, end;
+  {
+    Line<CHUNK, FP8> line(a, plan);
+    const int64_t per = cut.piece(line.total);
+    at = uniform64((int64_t)block * per);
+    end = uniform64(at + per < line.total ? at + per : line.total);
+    if (at >= end) return;
+    it = line.find(a, plan, at);
+  }
+  for (int nth = 0;; nth = 1) {
+    const int t0 = uniform((int)(at - it.start));
+    const int t1 = uniform(it.start + it.tiles < end ? it.tiles : (int)(end - it.start));
+    part(it, t0, t1, t0 == 0 && t1 == it.tiles ? (int64_t)-1 : 2 * (int64_t)block + nth);
+    at = it.start + t1;
+    if (at >= end) return;
+    __syncthreads();  // the next part writes the LDS that this one reads
+    // looked up again: what a lane knew of the sequences was not kept in registers meanwhile
+    it = Line<CHUNK, FP8>().find(a, plan, at, true);
+  }
+}
+
+}  // namespace tb

@@ -16,16 +16,11 @@
 // tiles of a wave are in flight: each half of a tile's registers is loaded
 // again, for the tile after the next, as soon as its product is formed.
 //
-// Work is cut by bytes, not by sequence: the tiles of all (sequence, head)
-// items stand in one line, and each of the two workgroups a CU holds takes an
-// equal piece of it, so that batches of mixed lengths end everywhere at once.
-// A piece covers some items whole, which it writes, and parts of at most two,
-// which a second launch joins.  Inside a workgroup the four waves take the
-// item's row tiles and, if it has fewer than four, its tiles in turn; they
+// The four waves of a workgroup take the position tiles of a part in turn and
 // join through LDS.
 #pragma once
 
-#include "attn_launch.h"
+#include "attn_line.h"
 
 namespace tb {
 
@@ -61,114 +56,11 @@ struct RowsShared {
   float o[kAttnWaves][16][D + 4];
 };
 
-// One (sequence, head) of the sequences with few rows, and its tiles in the
-// line of all of them.  A sequence that sees nothing still has one (empty)
-// tile, in which its rows are written.
-struct RowsItem {
-  int64_t start;  // of its first tile in the line
-  int tiles;      // of the line: at least 1
-  int b, head, rows;
-  PagedSeq seq;
-  PagedSpan span;
-  int first_tile, count;  // the tiles that some row sees
-};
-
-struct RowsSeq {
-  PagedSeq seq;
-  PagedSpan span;
-  TileSpan tiles;
-  int rows;  // 0: not of this kind
-};
-
-__device__ __forceinline__ RowsSeq rows_seq(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b) {
-  const tb_paged_cache& c = a.cache;
-  RowsSeq r;
-  r.seq = paged_seq(c.cu_q, c.kv_len, b, c.total_q, plan.capacity);
-  const int n = r.seq.n < (int)c.max_q ? r.seq.n : (int)c.max_q;
-  r.rows = plan.is_chunk((int64_t)n * plan.group) ? 0 : n * plan.group;
-  r.span = paged_span(r.seq, 0, n - 1, a.window);
-  r.tiles = tile_span(r.span, rows_positions(c.cache_dtype == TB_FP8));
-  return r;
-}
-
-// tiles of the line for each head of the sequence
-__device__ __forceinline__ int line_tiles(const RowsSeq& r) {
-  return r.rows == 0 ? 0 : r.tiles.count > 1 ? r.tiles.count : 1;
-}
-
-// a value that is the same in every lane, in scalar registers
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return uniform64(v);
-}
-
-// Tiles in the line.  Whole waves call this and get the same answer.
-__device__ __forceinline__ int64_t rows_total(const tb_paged_attention_args& a, const AttnPlan& plan) {
-  int64_t n = 0;
-  for (int64_t b = threadIdx.x & 63; b < a.cache.B; b += 64) n += line_tiles(rows_seq(a, plan, b));
-  return wave_sum64(n) * a.cache.heads_kv;
-}
-
-// Tiles before sequence b in the line (b < B).
-__device__ __forceinline__ int64_t rows_before(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b) {
-  int64_t n = 0;
-  for (int64_t x = threadIdx.x & 63; x < b; x += 64) n += line_tiles(rows_seq(a, plan, x));
-  return wave_sum64(n) * a.cache.heads_kv;
-}
-
-// The item that holds tile `at` of the line (at < total).
-__device__ __forceinline__ RowsItem rows_item_at(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at) {
-  const int lane = threadIdx.x & 63, heads = a.cache.heads_kv;
-  int64_t before = 0;
-  RowsItem it;
-  for (int64_t b0 = 0; b0 < a.cache.B; b0 += 64) {
-    int64_t up = 0;  // inclusive prefix over the lanes
-    if (b0 + lane < a.cache.B) up = (int64_t)line_tiles(rows_seq(a, plan, b0 + lane)) * heads;
-    const int64_t own = up;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int64_t t = __shfl_up(up, m);
-      if (lane >= m) up += t;
-    }
-    const uint64_t past = __ballot(before + up > at);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      it.start = uniform64(before + __shfl(up - own, l));
-      it.b = __builtin_amdgcn_readfirstlane((int)b0 + l);
-      break;
-    }
-    before = uniform64(before + __shfl(up, 63));
-  }
-  const RowsSeq r = rows_seq(a, plan, it.b);
-  it.tiles = line_tiles(r);
-  it.head = __builtin_amdgcn_readfirstlane((int)((at - it.start) / it.tiles));
-  it.start += (int64_t)it.head * it.tiles;
-  // the same in every lane: kept in scalar registers
-  it.rows = __builtin_amdgcn_readfirstlane(r.rows);
-  it.tiles = __builtin_amdgcn_readfirstlane(it.tiles);
-  it.seq.row0 = uniform64(r.seq.row0);
-  it.seq.n = __builtin_amdgcn_readfirstlane(r.seq.n);
-  it.seq.keys = __builtin_amdgcn_readfirstlane(r.seq.keys);
-  it.seq.first_pos = __builtin_amdgcn_readfirstlane(r.seq.first_pos);
-  it.span.begin = __builtin_amdgcn_readfirstlane(r.span.begin);
-  it.span.end = __builtin_amdgcn_readfirstlane(r.span.end);
-  it.first_tile = __builtin_amdgcn_readfirstlane(r.tiles.first);
-  it.count = __builtin_amdgcn_readfirstlane(r.tiles.count);
-  return it;
-}
-
 // Tiles t0 .. t1 - 1 of an item: its output (slot < 0: they are all of it), or
 // a part of it into the workspace's slot.
 template <int D, bool FP8>
 __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a, const AttnPlan& plan,
-                                               const RowsItem& it, int t0, int t1, int64_t slot, RowsShared<D>& sm) {
+                                               const LineItem& it, int t0, int t1, int64_t slot, RowsShared<D>& sm) {
   typedef RowOps<FP8> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
@@ -179,24 +71,15 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   constexpr int DT = D / 16;              // 16-row tiles of O'
 
   const tb_paged_cache& c = a.cache;
-  const int group = plan.group, head = it.head;
-  const int64_t b = it.b;
-  const PagedSeq& s = it.seq;
-  const int nrows = it.rows, row_tiles = (nrows + 15) >> 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = plan.group, head = it.head, nrows = it.seq.rows;  // one row tile: r is the row of the sequence
+  const PagedSeq& s = it.seq.seq;
+  const PagedSpan& span = it.span;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int i16 = lane & 15, q4 = lane >> 4;
-  // the wave's row tile, and its place among the waves of that tile
-  const int rt_bits = row_tiles == 1 ? 0 : row_tiles == 2 ? 1 : 2;
-  const int rt = wave & ((1 << rt_bits) - 1), turn = wave >> rt_bits, step_t = kAttnWaves >> rt_bits;
-  const int r0 = rt * kRowsTile;
-  const bool wave_live = r0 < nrows;
-  const int rl = r0 + kRowsTile - 1 < nrows ? r0 + kRowsTile - 1 : nrows - 1;  // last row
-  const int j0 = (unsigned)(wave_live ? r0 : 0) / (unsigned)group, j1 = (unsigned)rl / (unsigned)group;
-  const PagedSpan span = it.span;
-  const int first_tile = it.first_tile;
-  const int t_end = !wave_live ? 0 : t1 < it.count ? t1 : it.count;
+  const int j1 = uniform((unsigned)(nrows - 1) / (unsigned)group);  // last token
+  const int first_tile = it.held.first, t_end = t1 < it.held.count ? t1 : it.held.count;
 
-  const int32_t* table = c.block_table + b * c.table_stride;
+  const int32_t* table = c.block_table + it.b * c.table_stride;
   const int shift = plan.shift, page = c.page;
   const int64_t page_step = (int64_t)c.heads_kv * page * D;
   const Elem* kc = static_cast<const Elem*>(c.k_cache) + (int64_t)head * page * D;
@@ -244,13 +127,13 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     for (int dt = 0; dt < DT; ++dt) x.v[dt] = *reinterpret_cast<const u32x4*>(p + 16 * dt * page);
   };
 
-  int t = t0 + turn;
+  int t = t0 + wave;
   Tile ta;
   const Pages pa = lookup(t);
-  Pages ahead = lookup(t + step_t);
+  Pages ahead = lookup(t + kAttnWaves);
 
   // the lane's row
-  const int r = r0 + i16;
+  const int r = i16;
   const bool row_live = r < nrows;
   const int tok = row_live ? (int)((unsigned)r / (unsigned)group) : 0;
   const int hq = head * group + (row_live ? r - tok * group : 0);
@@ -284,7 +167,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     // looked up before that tile's loads: loads return in order, and the next
     // step waits for this one's answer only
     const Pages now = ahead;
-    ahead = lookup(t + 2 * step_t);
+    ahead = lookup(t + 2 * kAttnWaves);
     f32x4 sc[S];
 #pragma unroll
     for (int st = 0; st < S; ++st) {
@@ -300,7 +183,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
         }
       }
     }
-    load_keys(x, t + step_t, now);
+    load_keys(x, t + kAttnWaves, now);
 
     // scores in log2 units; what the row does not see is -inf.  The lane's
     // scores and its values are of the same positions, so of one page.
@@ -309,7 +192,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[st][e] *= scale2;
     // every row of the tile sees every position of it
-    const bool full = __ballot(pv < 0) == 0 && x0 + T - 1 <= s.first_pos + j0 &&
+    const bool full = __ballot(pv < 0) == 0 && x0 + T - 1 <= s.first_pos &&
                       (a.window <= 0 || x0 > (int64_t)s.first_pos + j1 - a.window);
     uint32_t seen = 0xffffffffu;  // bit 4 st + e
     if (!full) {
@@ -406,14 +289,14 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
         }
       }
     }
-    load_values(x, t + step_t, now);
+    load_values(x, t + kAttnWaves, now);
   };
   while (t < t_end) {
     step(ta, t);
-    t += step_t;
+    t += kAttnWaves;
   }
 
-  // the waves' sums joined: each scales its values to its row tile's common maximum
+  // the waves' sums joined: each scales its values to the common maximum
   l = sum_over_rows(l);
   if (q4 == 0) {
     sm.max[wave][i16] = m;
@@ -422,73 +305,41 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   __syncthreads();
   {
     float top = -__builtin_inff();
-    for (int w = rt; w < kAttnWaves; w += 1 << rt_bits) top = fmaxf(top, sm.max[w][i16]);
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w][i16]);
     const float f = exp2_fast(m - (top == -__builtin_inff() ? 0.f : top));
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(&sm.o[wave][i16][16 * dt + 4 * q4]) = o[dt] * f;
   }
   __syncthreads();
   constexpr int DL = D / 16;  // channels of a thread: 16 threads a row
-  const int d0 = (threadIdx.x & 15) * DL;
-  for (int k = 0; k < row_tiles; ++k) {
-    const int x = threadIdx.x >> 4, row = 16 * k + x;
-    if (row >= nrows) break;
-    float top = -__builtin_inff(), total = 0.f;
-    for (int w = k; w < kAttnWaves; w += 1 << rt_bits) top = fmaxf(top, sm.max[w][x]);
-    const float base = top == -__builtin_inff() ? 0.f : top;
-    f32x4 v[DL / 4];
+  const int d0 = (threadIdx.x & 15) * DL, row = threadIdx.x >> 4;
+  if (row >= nrows) return;
+  float top = -__builtin_inff(), total = 0.f;
 #pragma unroll
-    for (int e = 0; e < DL / 4; ++e) v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int w = k; w < kAttnWaves; w += 1 << rt_bits) {
-      total = fmaf(sm.sum[w][x], exp2_fast(sm.max[w][x] - base), total);
+  for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w][row]);
+  const float base = top == -__builtin_inff() ? 0.f : top;
+  f32x4 v[DL / 4];
 #pragma unroll
-      for (int e = 0; e < DL / 4; ++e) v[e] += *reinterpret_cast<const f32x4*>(&sm.o[w][x][d0 + 4 * e]);
-    }
-    if (slot >= 0) {
-      const int64_t pr = slot * plan.slot_rows + row;
-      if (d0 == 0) plan.rows_stats[pr] = float2{top, total};
+  for (int e = 0; e < DL / 4; ++e) v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < DL / 4; ++e) *reinterpret_cast<f32x4*>(plan.rows_values + pr * D + d0 + 4 * e) = v[e];
-    } else {
-      const int otok = (unsigned)row / (unsigned)group;
-      const int64_t at = (s.row0 + otok) * a.heads_q + head * group + (row - otok * group);
-      const RowScale rs = row_scale(a, head, at, d0 == 0, top, total);
+  for (int w = 0; w < kAttnWaves; ++w) {
+    total = fmaf(sm.sum[w][row], exp2_fast(sm.max[w][row] - base), total);
 #pragma unroll
-      for (int e = 0; e < DL / 4; ++e) write4(a, at * D + d0 + 4 * e, v[e], rs);
-    }
+    for (int e = 0; e < DL / 4; ++e) v[e] += *reinterpret_cast<const f32x4*>(&sm.o[w][row][d0 + 4 * e]);
   }
-}
-
-// Piece `block` of the items with few rows.
-template <int D, bool FP8>
-__device__ __forceinline__ void attn_rows(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block,
-                                          RowsShared<D>& sm) {
-  const int64_t total = rows_total(a, plan), per = plan.piece(total);
-  int64_t at = (int64_t)block * per;
-  const int64_t end = at + per < total ? at + per : total;
-  bool first = true;
-  while (at < end) {
-    const RowsItem it = rows_item_at(a, plan, at);
-    const int t0 = (int)(at - it.start);
-    const int64_t past = it.start + it.tiles;
-    const int t1 = (int)((past < end ? past : end) - it.start);
-    attn_rows_part<D, FP8>(a, plan, it, t0, t1, t0 == 0 && t1 == it.tiles ? -1 : 2 * (int64_t)block + (first ? 0 : 1), sm);
-    at = it.start + t1;
-    first = false;
-    if (at < end) __syncthreads();  // the next part writes the LDS that this one reads
+  if (slot >= 0) {
+    const int64_t pr = slot * kRowsTile + row;
+    if (d0 == 0) plan.rows_line.stats[pr] = float2{top, total};
+#pragma unroll
+    for (int e = 0; e < DL / 4; ++e) *reinterpret_cast<f32x4*>(plan.rows_line.values + pr * D + d0 + 4 * e) = v[e];
+    return;
   }
-}
-
-// Item `block` of B * heads_kv, in one part.
-template <int D, bool FP8>
-__device__ __forceinline__ void attn_rows_whole(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block,
-                                                RowsShared<D>& sm) {
-  const unsigned heads = (unsigned)a.cache.heads_kv;
-  const RowsSeq r = rows_seq(a, plan, block / heads);
-  if (r.rows == 0) return;
-  const RowsItem it{0, line_tiles(r), (int)(block / heads), (int)(block % heads), r.rows, r.seq, r.span, r.tiles.first,
-                    r.tiles.count};
-  attn_rows_part<D, FP8>(a, plan, it, 0, it.tiles, -1, sm);
+  const int otok = (unsigned)row / (unsigned)group;
+  const int64_t at = (s.row0 + otok) * a.heads_q + head * group + (row - otok * group);
+  const RowScale rs = row_scale(a, head, at, d0 == 0, top, total);
+#pragma unroll
+  for (int e = 0; e < DL / 4; ++e) write4(a, at * D + d0 + 4 * e, v[e], rs);
 }
 
 }  // namespace tb

@@ -118,7 +118,7 @@ def test_attention_workspace():
         return tb.lib().tb_paged_attention_workspace(tb.PagedAttentionArgs(**a))
 
     assert ws() == 0                                         # short: one part
-    row = (128 + 2) * 4 * 6 * 8
+    row = (128 + 2) * 4                                      # values and two statistics
     long = ws(max_kv=1 << 16)
     assert long > 0 and long % row == 0
     assert ws(max_kv=1 << 16, window=64) <= long
