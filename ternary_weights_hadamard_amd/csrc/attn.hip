@@ -11,19 +11,19 @@ namespace {
 // no more registers or LDS than the chunks do.
 template <int D, bool FP8, bool ROWS, bool CHUNK>
 __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_attention_args a, AttnPlan plan) {
-  union Shared {
-    RowsShared<D> rows;
-    ChunkShared<D> chunk;
-  };
-  __shared__ __align__(16) unsigned char shared[CHUNK ? sizeof(Shared) : sizeof(RowsShared<D>)];
+  constexpr int kBuffer = CHUNK ? kChunkPositions * D * 2 : kRowsTile * (D + 4) * 4;  // bytes
+  static_assert(kBuffer >= kRowsTile * (D + 4) * 4, "both kinds share the buffers");
+  __shared__ u32x4 b0[kBuffer / 16], b1[kBuffer / 16], b2[kBuffer / 16], b3[kBuffer / 16];
+  __shared__ float stats[2][16 * kAttnWaves];
+  const AttnShared sm{{b0, b1, b2, b3}, stats[0], stats[1]};
   if (CHUNK && (!ROWS || blockIdx.x < plan.chunk_blocks)) {
     if constexpr (CHUNK)
       run_line<true, FP8>(a, plan, blockIdx.x, [&](const LineItem& it, int t0, int t1, int64_t slot) {
-        attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, *reinterpret_cast<ChunkShared<D>*>(shared));
+        attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
       });
   } else if constexpr (ROWS) {
     run_line<false, FP8>(a, plan, blockIdx.x - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot) {
-      attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, *reinterpret_cast<RowsShared<D>*>(shared));
+      attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
     });
   }
 }

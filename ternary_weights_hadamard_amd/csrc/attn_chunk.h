@@ -53,26 +53,20 @@ template <int D>
 __device__ __forceinline__ int k_chunk(int row, int c) {
   return row * (D / 8) + (c ^ (row & (D / 8 - 1)));
 }
-__device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ (row & 7)); }
-
-template <int D>
-struct ChunkShared {
-  u32x4 tile[2][2][kTile * D / 8];  // [buffer][K, V][16-byte chunk]
-};
+__device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ ((row >> 1) & 7)); }
 
 // Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
 // it), or a part of it into the workspace's slot.
 template <int D, bool FP8>
 __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
                                                 const LineItem& it, int t_begin, int t_stop, int64_t slot,
-                                                ChunkShared<D>& sm) {
+                                                const AttnShared& sm) {
   typedef typename ChunkOps<FP8>::Elem Elem;
   typedef typename ChunkOps<FP8>::V8 V8;
   constexpr int KK = D / 16;   // steps of a score tile
   constexpr int DT = D / 32;   // 32-channel tiles of O'
   constexpr int kChunks = kTile * D / 8;  // 16-byte chunks of a tile of K, and of V
   constexpr int kWaves = kAttnWaves, kRows = kChunkTile;
-  auto& lds = sm.tile;
 
   const tb_paged_cache& c = a.cache;
   const int group = plan.group, head = it.head, nrows = it.seq.rows;
@@ -131,17 +125,16 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   // A tile is four runs of 16 positions, each in one page.  What a lane loads
   // of V lies in run v_run, the same for all its loads, so it looks up that
   // run's page (-1: none, or nobody sees it; its entry is not read then), and
-  // lane kHolder * g thereby holds run g's.  What a wave loads of K with one
+  // holder(g) is a lane that thereby holds run g's.  What a wave loads of K with one
   // instruction lies in one run.
   constexpr int kPer = FP8 ? 16 : 8;                               // positions (or channels) of a 16-byte load
   constexpr int kLoads = kTile * D / kPer / (64 * kWaves);         // loads of a lane, for K and for V
   constexpr int kStep = FP8 ? 64 * kWaves / (D / 16) : 64 * kWaves / (D / 8);        // rows of K between them
   constexpr int vStep = 64 * kWaves / (kTile / kPer);              // rows of V between them
-  constexpr int kHolder = FP8 ? 1 : 2;
   const int tid = wave * 64 + lane;
   const int k_row = tid / (D / kPer), v_row = tid / (kTile / kPer);  // of the first load
   const int k_ch = FP8 ? tid % (D / 16) : (tid % (D / 8)) ^ (k_row & (D / 8 - 1));
-  const int v_ch = FP8 ? tid % 4 : (tid % 8) ^ (v_row & 7);
+  const int v_ch = FP8 ? tid % 4 : (tid % 8) ^ ((v_row >> 1) & 7);
   const int v_run = FP8 ? v_ch : v_ch >> 1;
   const int k_off = (k_row & 15) * D + k_ch * kPer;                 // inside a run
   const int v_off = v_row * c.page + (v_ch * kPer & 15);
@@ -150,9 +143,10 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     if (t >= t_end || (x | (c.page - 1)) < span.begin || x >= span.end) return -1;
     return paged_page(table, c.table_width, c.n_pages, x >> shift);
   };
-  auto run_page = [](int pages, int g) { return __builtin_amdgcn_readlane(pages, kHolder * g); };
+  auto holder = [&](int g) { return FP8 ? g : 2 * g ^ 4 * (wave & 1); };  // bf16: row v_row of lanes 0..7 is 8 wave
+  auto run_page = [&](int pages, int g) { return __builtin_amdgcn_readlane(pages, holder(g)); };
   u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
-  auto stage = [&](int t, int pages, int buf) {
+  auto stage = [&](int t, int pages, u32x4* k_to, u32x4* v_to) {
     const int x0 = (first_tile + t) * kTile;
     const Elem* vp = vc + (pages < 0 ? 0 : pages) * page_step + ((x0 + 16 * v_run) & (c.page - 1)) + v_off;
 #pragma unroll
@@ -166,22 +160,22 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       } else {
         const int at = i * 64 * kWaves + wave * 64;  // the wave's first chunk
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(kp + k_off),
-                                         (__attribute__((address_space(3))) uint32_t*)&lds[buf][0][at], 16, 0, 0);
+                                         (__attribute__((address_space(3))) uint32_t*)&k_to[at], 16, 0, 0);
         __builtin_amdgcn_global_load_lds(
             (const __attribute__((address_space(1))) uint32_t*)(vp + i * vStep * c.page),
-            (__attribute__((address_space(3))) uint32_t*)&lds[buf][1][at], 16, 0, 0);
+            (__attribute__((address_space(3))) uint32_t*)&v_to[at], 16, 0, 0);
       }
     }
   };
-  auto widen = [&](int buf) {  // 8-bit: the staged registers into LDS
+  auto widen = [&](u32x4* k_to, u32x4* v_to) {  // 8-bit: the staged registers into LDS
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int kw = i * kStep + k_row, vw = i * vStep + v_row;
-        lds[buf][0][k_chunk<D>(kw, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
-        lds[buf][0][k_chunk<D>(kw, 2 * k_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][2], kr[i][3]}));
-        lds[buf][1][v_chunk(vw, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
-        lds[buf][1][v_chunk(vw, 2 * v_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][2], vr[i][3]}));
+        k_to[k_chunk<D>(kw, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
+        k_to[k_chunk<D>(kw, 2 * k_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][2], kr[i][3]}));
+        v_to[v_chunk(vw, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
+        v_to[v_chunk(vw, 2 * v_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][2], vr[i][3]}));
       }
     }
   };
@@ -197,17 +191,19 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[dt][e] = 0.f;
 
-  int pages = lookup(t_begin);
+  int pages = lookup(t_begin), pages_next = lookup(t_begin + 1);
   if (t_begin < t_end) {
-    stage(t_begin, pages, 0);
-    widen(0);
+    stage(t_begin, pages, sm.buffer[0], sm.buffer[1]);
+    widen(sm.buffer[0], sm.buffer[1]);
   }
-  int pages_next = lookup(t_begin + 1);
-  for (int t = t_begin; t < t_end; ++t) {
-    const int buf = (t - t_begin) & 1;
+  // Tile t, in k_lds and v_lds, while tile t + 1 is loaded into k_to and v_to.
+  // The four are arrays of their own, and which is which is known when this is
+  // compiled: the compiler then knows that reading the one does not wait for
+  // the loads into the other.
+  auto step = [&](int t, u32x4* k_lds, u32x4* v_lds, u32x4* k_to, u32x4* v_to) {
     __builtin_amdgcn_s_waitcnt(0);  // this wave's share of the tile is in LDS
     __syncthreads();
-    if (t + 1 < t_end) stage(t + 1, pages_next, buf ^ 1);
+    if (t + 1 < t_end) stage(t + 1, pages_next, k_to, v_to);
     const int pages_after = lookup(t + 2);
     const int x0 = (first_tile + t) * kTile;
     uint32_t there = 0xfu;  // which of the tile's runs exist
@@ -221,13 +217,12 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     f32x16 sc[2];
     if (any) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int e = 0; e < 16; ++e) sc[0][e] = sc[1][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sc[u][e] = 0.f;
+      for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          sc[u] = mfma32(__builtin_bit_cast(bf16x8, lds[buf][0][k_chunk<D>(32 * u + key, 2 * kk + half)]), q[kk], sc[u]);
-      }
+        for (int u = 0; u < 2; ++u)
+          sc[u] = mfma32(__builtin_bit_cast(bf16x8, k_lds[k_chunk<D>(32 * u + key, 2 * kk + half)]), q[kk], sc[u]);
 
       // The lane's scores: register 8 k + e of tile u is position 32 u + 16 k + 8 half + e.
       const bool full = there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > pos_last - a.window);
@@ -285,7 +280,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
-        const u32x4 w = lds[buf][1][i * 64 * kWaves + tid];
+        const u32x4 w = v_lds[i * 64 * kWaves + tid];
         bad = bad || (FP8 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w));
       }
       if (__syncthreads_or(bad)) {
@@ -296,7 +291,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
           for (int e = 0; e < 16; ++e) up[e] = down[e] = 0.f;
 #pragma unroll
           for (int kb = 0; kb < 4; ++kb) {
-            V8 see, v = __builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]);
+            V8 see, v = __builtin_bit_cast(V8, v_lds[v_chunk(32 * dt + i32, 2 * kb + half)]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) see[e] = (seen >> (8 * kb + e)) & 1u ? 1.f : 0.f;
             const Nonfinite<V8> nf = take_nonfinite(v);
@@ -310,9 +305,9 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
-          V8 v = __builtin_bit_cast(V8, lds[buf][1][i * 64 * kWaves + tid]);
+          V8 v = __builtin_bit_cast(V8, v_lds[i * 64 * kWaves + tid]);
           take_nonfinite(v);
-          lds[buf][1][i * 64 * kWaves + tid] = __builtin_bit_cast(u32x4, v);
+          v_lds[i * 64 * kWaves + tid] = __builtin_bit_cast(u32x4, v);
         }
         __syncthreads();
       }
@@ -326,12 +321,16 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
         for (int e = 0; e < 8; ++e) w[e] = ChunkOps<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
-          o[dt] = mfma32(__builtin_bit_cast(V8, lds[buf][1][v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
+          o[dt] = mfma32(__builtin_bit_cast(V8, v_lds[v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
       }
     }
     pages = pages_next;
     pages_next = pages_after;
-    widen(buf ^ 1);
+    widen(k_to, v_to);
+  };
+  for (int t = t_begin; t < t_end; t += 2) {
+    step(t, sm.buffer[0], sm.buffer[1], sm.buffer[2], sm.buffer[3]);
+    if (t + 1 < t_end) step(t + 1, sm.buffer[2], sm.buffer[3], sm.buffer[0], sm.buffer[1]);
   }
 
   // the row's sum, and its output: register 4 j + e of tile dt is channel 32 dt + 8 j + 4 half + e

@@ -34,6 +34,7 @@ struct AttnPlan {
   __host__ __device__ bool is_chunk(int64_t nrows) const { return nrows > few; }
 };
 
+constexpr int kAttnWaves = 4;    // waves of a workgroup
 constexpr int kRowsTile = 16;    // rows of a row tile: few rows,
 constexpr int kChunkTile = 128;  // and chunks
 // positions of a tile: few rows (the cache's type), and chunks
@@ -48,6 +49,13 @@ __device__ __forceinline__ TileSpan tile_span(const PagedSpan& p, int positions)
   const int first = p.begin / positions;
   return TileSpan{first, p.end > p.begin ? (p.end + positions - 1) / positions - first : 0};
 }
+
+// A workgroup's LDS.  Few rows: a buffer and 16 of max and of sum for each
+// wave.  Chunks: K, V of a tile, and K, V of the next.
+struct AttnShared {
+  u32x4* buffer[4];
+  float *max, *sum;
+};
 
 // What a row's weighted values are multiplied with; its log-sum-exp is
 // written on the way (`first`: by the one lane that does).

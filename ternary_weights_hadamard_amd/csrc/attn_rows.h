@@ -24,8 +24,6 @@
 
 namespace tb {
 
-constexpr int kAttnWaves = 4;  // waves of a workgroup, of both kernels
-
 template <bool FP8>
 struct RowOps;
 
@@ -50,17 +48,11 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-template <int D>
-struct RowsShared {
-  float max[kAttnWaves][16], sum[kAttnWaves][16];
-  float o[kAttnWaves][16][D + 4];
-};
-
 // Tiles t0 .. t1 - 1 of an item: its output (slot < 0: they are all of it), or
 // a part of it into the workspace's slot.
 template <int D, bool FP8>
 __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a, const AttnPlan& plan,
-                                               const LineItem& it, int t0, int t1, int64_t slot, RowsShared<D>& sm) {
+                                               const LineItem& it, int t0, int t1, int64_t slot, const AttnShared& sm) {
   typedef RowOps<FP8> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
@@ -296,20 +288,26 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     t += kAttnWaves;
   }
 
+  constexpr int kRow = D + 4;  // floats of a row in LDS
   // the waves' sums joined: each scales its values to the common maximum
   l = sum_over_rows(l);
   if (q4 == 0) {
-    sm.max[wave][i16] = m;
-    sm.sum[wave][i16] = l;
+    sm.max[wave * 16 + i16] = m;
+    sm.sum[wave * 16 + i16] = l;
   }
   __syncthreads();
   {
     float top = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w][i16]);
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w * 16 + i16]);
     const float f = exp2_fast(m - (top == -__builtin_inff() ? 0.f : top));
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(&sm.o[wave][i16][16 * dt + 4 * q4]) = o[dt] * f;
+    for (int w = 0; w < kAttnWaves; ++w) {
+      if (w != wave) continue;
+      f32x4* to = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(sm.buffer[w]) + i16 * kRow + 4 * q4);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) to[4 * dt] = o[dt] * f;
+    }
   }
   __syncthreads();
   constexpr int DL = D / 16;  // channels of a thread: 16 threads a row
@@ -317,16 +315,17 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   if (row >= nrows) return;
   float top = -__builtin_inff(), total = 0.f;
 #pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w][row]);
+  for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w * 16 + row]);
   const float base = top == -__builtin_inff() ? 0.f : top;
   f32x4 v[DL / 4];
 #pragma unroll
   for (int e = 0; e < DL / 4; ++e) v[e] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
-    total = fmaf(sm.sum[w][row], exp2_fast(sm.max[w][row] - base), total);
+    total = fmaf(sm.sum[w * 16 + row], exp2_fast(sm.max[w * 16 + row] - base), total);
 #pragma unroll
-    for (int e = 0; e < DL / 4; ++e) v[e] += *reinterpret_cast<const f32x4*>(&sm.o[w][row][d0 + 4 * e]);
+    for (int e = 0; e < DL / 4; ++e)
+      v[e] += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(sm.buffer[w]) + row * kRow + d0 + 4 * e);
   }
   if (slot >= 0) {
     const int64_t pr = slot * kRowsTile + row;
