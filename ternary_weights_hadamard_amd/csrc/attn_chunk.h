@@ -55,6 +55,81 @@ __device__ __forceinline__ int k_chunk(int row, int c) {
 }
 __device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ ((row >> 1) & 7)); }
 
+// Values that are not finite, in a tile that not every row sees all of (the
+// products multiply every value with every row's weight, 0 where it does not
+// see the position).  They are set to 0 in LDS.  Where some row sees one, it is
+// first noted in bits which rows see a +inf (or NaN), and which a -inf (or NaN),
+// in each channel: marks[row][D / 32][2], zero at the start; `marked` says that
+// there are any.  All waves of the workgroup come here together, with the tile
+// in v_lds and a barrier behind them.
+//   x0, there   the tile's first position, and which of its runs of 16 exist
+//   begin, end  the positions that some row sees
+template <int D, bool FP8, int ROWS>
+__device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, uint32_t* marks, bool& marked, int x0, uint32_t there,
+                                                    int begin, int end, int first_pos, int group, int r0, int nrows,
+                                                    int64_t window) {
+  constexpr int kThreads = 64 * kAttnWaves, kChunks = kTile * D / 8;
+  typedef typename ChunkOps<FP8>::V8 V8;
+  const int tid = threadIdx.x;
+  int bad = 0;  // 1: some value is not finite, 2: at a position that some row sees
+#pragma unroll 1
+  for (int i = tid; i < kChunks; i += kThreads) {
+    const u32x4 w = v_lds[i];
+    if (!(FP8 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w))) continue;
+    const int row = i / (kTile / 8), x = x0 + (((i % (kTile / 8)) ^ ((row >> 1) & 7)) * 8);  // of the chunk: v_chunk
+    bad |= x + 8 > begin && x < end ? 3 : 1;
+  }
+  if (!__syncthreads_or(bad)) return;
+  if (__syncthreads_or(bad & 2)) {
+    marked = true;
+    // a thread has one row, and a share of the channels
+    const int row = tid % ROWS, share = tid / ROWS;
+    constexpr int kMine = D / (kThreads / ROWS);
+    const bool live = r0 + row < nrows;
+    const int64_t pos = (int64_t)first_pos + (int)((unsigned)(live ? r0 + row : r0) / (unsigned)group) - x0;
+    const int64_t low = window > 0 ? pos - window : -1;
+#pragma unroll 1
+    for (int d = share * kMine; d < share * kMine + kMine; ++d) {
+      uint32_t up = 0, down = 0;
+#pragma unroll 1
+      for (int ch = 0; ch < kTile / 8; ++ch) {
+        const V8 v = __builtin_bit_cast(V8, v_lds[v_chunk(d, ch)]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = (float)v[e];
+          const int x = 8 * ch + e;
+          if (fabsf(f) < __builtin_inff() || !live || x > pos || x <= low || !((there >> (x >> 4)) & 1u)) continue;
+          if (!(f < 0.f)) up = 1;
+          if (!(f > 0.f)) down = 1;
+        }
+      }
+      if (up | down) {
+        uint32_t* at = marks + (row * (D / 32) + (d >> 5)) * 2;
+        if (up) atomicOr(at, 1u << (d & 31));
+        if (down) atomicOr(at + 1, 1u << (d & 31));
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int i = tid; i < kChunks; i += kThreads) {
+    V8 v = __builtin_bit_cast(V8, v_lds[i]);
+    take_nonfinite(v);
+    v_lds[i] = __builtin_bit_cast(u32x4, v);
+  }
+  __syncthreads();
+}
+
+// What a row's marks add to its channels 32 dt + c .. + 3.
+template <int D>
+__device__ __forceinline__ f32x4 marked_sum(const uint32_t* marks, int row, int dt, int c) {
+  const uint32_t up = marks[(row * (D / 32) + dt) * 2] >> c, down = marks[(row * (D / 32) + dt) * 2 + 1] >> c;
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = nonfinite_sum((up >> e) & 1u ? 1.f : 0.f, (down >> e) & 1u ? 1.f : 0.f);
+  return r;
+}
+
 // Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
 // it), or a part of it into the workspace's slot.
 template <int D, bool FP8>
@@ -65,7 +140,6 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   typedef typename ChunkOps<FP8>::V8 V8;
   constexpr int KK = D / 16;   // steps of a score tile
   constexpr int DT = D / 32;   // 32-channel tiles of O'
-  constexpr int kChunks = kTile * D / 8;  // 16-byte chunks of a tile of K, and of V
   constexpr int kWaves = kAttnWaves, kRows = kChunkTile;
 
   const tb_paged_cache& c = a.cache;
@@ -191,6 +265,9 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[dt][e] = 0.f;
 
+  bool marked = false;
+#pragma unroll
+  for (int i = 0; i < kRows * D / 16 / (64 * kWaves); ++i) sm.marks[i * 64 * kWaves + tid] = 0u;  // a barrier follows
   int pages = lookup(t_begin), pages_next = lookup(t_begin + 1);
   if (t_begin < t_end) {
     stage(t_begin, pages, sm.buffer[0], sm.buffer[1]);
@@ -213,7 +290,6 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     // does any row of the wave see any of it; do all of the workgroup's see all of it
     const bool any = x0 <= pos_last && (a.window <= 0 || x0 + kTile - 1 > pos_first - a.window);
     const bool all_full = there == 0xfu && x0 + kTile - 1 <= all_first && (a.window <= 0 || x0 > all_last - a.window);
-    uint32_t seen = any ? 0xffffffffu : 0u;  // bit 16 u + register
     f32x16 sc[2];
     if (any) {
 #pragma unroll
@@ -227,7 +303,6 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       // The lane's scores: register 8 k + e of tile u is position 32 u + 16 k + 8 half + e.
       const bool full = there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > pos_last - a.window);
       if (!full) {
-        seen = 0;
         const int64_t rel = (int64_t)x0 + 8 * half;
         const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 63 ? 63 : pos - rel) : -1;
         const int lo = (int)(low - rel < -1 ? -1 : low - rel > 63 ? 63 : low - rel);
@@ -237,7 +312,6 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
           for (int e = 0; e < 16; ++e) {
             const int x = 32 * u + 16 * (e >> 3) + (e & 7);
             const bool see = x <= hi && x > lo && ((there >> (2 * u + (e >> 3))) & 1u);
-            seen |= (see ? 1u : 0u) << (16 * u + e);
             sc[u][e] = see ? sc[u][e] : -__builtin_inff();
           }
       }
@@ -255,7 +329,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       // and the values' sums are rarely rescaled.
       if (__ballot(top > m + 8.f) != 0) {
         const float m_new = fmaxf(m, top);
-        const float alpha = m_new == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
+        const float alpha = m == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
         m = m_new;
         l *= alpha;
 #pragma unroll
@@ -273,45 +347,9 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
         }
     }
 
-    // Values that are not finite (attn_common.h): looked for in the tiles that
-    // some row sees in part, each wave in its share; where there are any, every
-    // wave counts its rows', and then they are 0 in LDS.
-    if (!all_full) {
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
-        const u32x4 w = v_lds[i * 64 * kWaves + tid];
-        bad = bad || (FP8 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w));
-      }
-      if (__syncthreads_or(bad)) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          f32x16 up, down;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) up[e] = down[e] = 0.f;
-#pragma unroll
-          for (int kb = 0; kb < 4; ++kb) {
-            V8 see, v = __builtin_bit_cast(V8, v_lds[v_chunk(32 * dt + i32, 2 * kb + half)]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) see[e] = (seen >> (8 * kb + e)) & 1u ? 1.f : 0.f;
-            const Nonfinite<V8> nf = take_nonfinite(v);
-            up = mfma32(nf.up, see, up);
-            down = mfma32(nf.down, see, down);
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[dt][e] += nonfinite_sum(up[e], down[e]);
-          __builtin_amdgcn_sched_barrier(0);  // one at a time: this path is rare, its registers are not to count
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kChunks / (64 * kWaves); ++i) {
-          V8 v = __builtin_bit_cast(V8, v_lds[i * 64 * kWaves + tid]);
-          take_nonfinite(v);
-          v_lds[i * 64 * kWaves + tid] = __builtin_bit_cast(u32x4, v);
-        }
-        __syncthreads();
-      }
-    }
+    if (!all_full)
+      take_nonfinite_tile<D, FP8, kRows>(v_lds, sm.marks, marked, x0, there, span.begin, span.end, s.first_pos, group, r0,
+                                         nrows, a.window);
 
     if (any) {
 #pragma unroll
@@ -340,6 +378,16 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     l = a0 + a1;
   }
   if (!row_live) return;
+  if (marked) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 x = marked_sum<D>(sm.marks, r - r0, dt, 8 * j + 4 * half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[dt][4 * j + e] += x[e];
+      }
+  }
   const int64_t at = (s.row0 + tok) * a.heads_q + hq;
   if (slot >= 0) {
     const int64_t pr = slot * kRows + (r - r0);

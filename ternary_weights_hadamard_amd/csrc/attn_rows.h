@@ -210,7 +210,8 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
       for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[st][e]);
     const float m_new = fmaxf(m, max_over_rows(top));
     const float base = m_new == -__builtin_inff() ? 0.f : m_new;
-    const float alpha = exp2_fast(m - base);
+    // at least the smallest number: a sum may hold an infinity, and keeps it
+    const float alpha = m == -__builtin_inff() ? 1.f : fmaxf(exp2_fast(m - base), 1.17549435e-38f);
     m = m_new;
     float sum = 0.f;
 #pragma unroll

@@ -143,6 +143,45 @@ def test_attention_matches_oracle(shape, cache):
     assert torch.equal(again, out)
 
 
+WIDE = [  # at least 256 rows of a key/value head in a sequence, in one part: the kernel for large chunks
+    ([(130, 333), (1, 70), (257, 257), (0, 5)], 6, 2, 128, 32, 0),
+    ([(100, 1100)], 5, 1, 64, 1024, 0),
+    ([(150, 400), (40, 40)], 4, 1, 128, 64, 37),
+    ([(300, 64), (64, 300)], 4, 1, 64, 16, 0),
+    ([(260, 260), (513, 600)], 2, 2, 128, 16, 0),
+    ([(256, 64)], 1, 1, 128, 16, 0),
+]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: f"{s[0][0][0]}-{s[0][0][1]}-h{s[1]}.{s[2]}-d{s[3]}-p{s[4]}-w{s[5]}")
+def test_attention_of_large_chunks(shape, cache):
+    lens, hq, hkv, d, page, window = shape
+    say(f"large chunks {shape} {cache}")
+    c = Case(lens, hq, hkv, d, page, cache)
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    out, lse = c.attend(window=window, out_dtype=torch.float32, workspace=small)
+    c.check(out, lse, window=window, what="in one part")
+    again, al = c.attend(window=window, out_dtype=torch.float32, workspace=small)
+    assert torch.equal(again, out) and torch.equal(al, lse)
+    for scale in (0.0, -0.7):
+        out, lse = c.attend(window=window, out_dtype=torch.bfloat16, workspace=small, scale=scale)
+        c.check(out, lse, window=window, scale=scale, what=f"scale {scale}")
+
+
+def test_attention_of_many_large_chunks():
+    """Enough row tiles to fill the GPU: in one part although a workspace is there."""
+    c = Case([(300, 300), (5, 900), (290, 700)] * 5, 16, 16, 64, 16, "bf16")
+    out, lse = c.attend(out_dtype=torch.float32)
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    whole, wl = c.attend(out_dtype=torch.float32, workspace=small)
+    torch.cuda.synchronize()
+    big = torch.arange(c.total, device=DEV) % 595
+    big = (big < 300) | (big >= 305)
+    assert torch.equal(out[big], whole[big]) and torch.equal(lse[big], wl[big])
+    c.check(out, lse, what="many")
+
+
 @pytest.mark.parametrize("cache", ["bf16", "fp8"])
 @pytest.mark.parametrize("n,kv,hq,hkv", [(1, 4000, 4, 2), (6, 3001, 8, 2), (70, 2500, 2, 1)])
 def test_attention_split_and_whole(n, kv, hq, hkv, cache):
@@ -163,13 +202,16 @@ def test_attention_split_and_whole(n, kv, hq, hkv, cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "fp8"])
-@pytest.mark.parametrize("n,kv", [(1, 300), (12, 300), (150, 300)])
-def test_attention_unseen_values_do_not_reach_a_row(n, kv, cache):
+@pytest.mark.parametrize("n,kv,whole", [(1, 300, False), (12, 300, False), (150, 300, False), (150, 300, True)])
+def test_attention_unseen_values_do_not_reach_a_row(n, kv, whole, cache):
     """NaN and infinities at positions that a token does not see leave it alone;
     at positions that it sees they give what the formula gives."""
     c = Case([(n, kv), (n, n)], 4, 2, 128, 16, cache)
     window = 40
-    first, fl = c.attend(window=window, out_dtype=torch.float32)
+    kw = dict(window=window, out_dtype=torch.float32)
+    if whole:
+        kw["workspace"] = torch.empty(16, dtype=torch.uint8, device=DEV)
+    first, fl = c.attend(**kw)
     c.check(first, fl, window=window, what="clean")
     page_of = lambda x: (int(c.table[0, x // c.page]), x % c.page)  # noqa: E731
     # what lies before every window, and its table entries
@@ -180,7 +222,7 @@ def test_attention_unseen_values_do_not_reach_a_row(n, kv, cache):
         c.v[i, :, :, s] = float("nan")
     c.table[0, :(low + 1) // c.page] = np.where(np.arange((low + 1) // c.page) % 2, 2**31 - 1, -2**31)
     c.ints()
-    out, lse = c.attend(window=window, out_dtype=torch.float32)
+    out, lse = c.attend(**kw)
     torch.cuda.synchronize()
     assert torch.equal(out, first) and torch.equal(lse, fl)
     # a later token's value: the tokens before it are as they were, it and those that see it are not finite there
@@ -189,7 +231,7 @@ def test_attention_unseen_values_do_not_reach_a_row(n, kv, cache):
         i, s = int(d.table[0, (kv - n + t) // 16]), (kv - n + t) % 16
         d.v[i, 1, 3, s] = float("nan") if cache == "fp8" else float("inf")
         d.k[i, 0, s, 5] = float("nan")
-        out, lse = d.attend(window=window, out_dtype=torch.float32)
+        out, lse = d.attend(**kw)
         torch.cuda.synchronize()
         seen = torch.zeros(2 * n, dtype=torch.bool, device=DEV)
         seen[t:min(n, t + window)] = True
