@@ -1,5 +1,5 @@
 // tb_paged_attention: its kernels, how a call is cut, and its launches.
-#include "attn_wide.h"
+#include "attn_chunk.h"
 #include "tb_launch.h"
 
 namespace tb {
@@ -27,31 +27,6 @@ __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_atten
       attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
     });
   }
-}
-
-// Chunks in whole items of 256 rows: a sequence's last rows, which see the most
-// positions, first.
-template <int D, bool FP8>
-__global__ void __launch_bounds__(64 * kAttnWaves, 1) attn_wide_kernel(tb_paged_attention_args a, AttnPlan plan,
-                                                                       unsigned row_tiles) {
-  constexpr int kBuffer = kChunkPositions * D / 8;
-  __shared__ u32x4 k0[kBuffer], k1[kBuffer], k2[kBuffer], v0[kBuffer], v1[kBuffer], v2[kBuffer];
-  __shared__ uint32_t marks[kWideTile * D / 16];
-  WideShared sm;
-  sm.k[0] = k0, sm.k[1] = k1, sm.k[2] = k2;
-  sm.v[0] = v0, sm.v[1] = v1, sm.v[2] = v2;
-  sm.marks = marks;
-  const unsigned heads = (unsigned)a.cache.heads_kv;
-  LineItem it{};
-  it.head = blockIdx.x % heads;
-  it.b = blockIdx.x / heads / row_tiles;
-  it.seq = LineKind<true, FP8>::sequence(a, plan, it.b);
-  it.rt = (it.seq.rows + kWideTile - 1) / kWideTile - 1 - (int)(blockIdx.x / heads % row_tiles);
-  if (it.rt < 0 || it.seq.rows == 0) return;
-  const int r0 = it.rt * kWideTile, rl = r0 + kWideTile - 1 < it.seq.rows ? r0 + kWideTile - 1 : it.seq.rows - 1;
-  it.span = paged_span(it.seq.seq, (unsigned)r0 / (unsigned)plan.group, (unsigned)rl / (unsigned)plan.group, a.window);
-  it.held = tile_span(it.span, kChunkPositions);
-  attn_wide_part<D, FP8>(a, plan, uniform_item(it), sm);
 }
 
 // The parts of row r's item: of a sequence of the kind, one head.
@@ -209,19 +184,10 @@ hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stre
   const tb_paged_cache& c = a.cache;
   const bool chunk = has_chunk(a, p), rows = has_rows(a, p);
   const int64_t heads = c.B * c.heads_kv;
-  const bool wide = chunk && !p.chunk_line.pieces && most_rows(a) >= kWideTile;
-  if (wide) {
-    const unsigned row_tiles = (unsigned)((most_rows(a) + kWideTile - 1) / kWideTile);
-    hipLaunchKernelGGL((attn_wide_kernel<D, FP8>), dim3((unsigned)(heads * row_tiles)), dim3(64 * kAttnWaves), 0, stream, a,
-                       p, row_tiles);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  p.chunk_blocks = !chunk || wide ? 0 : (unsigned)(p.chunk_line.pieces ? p.chunk_line.pieces : heads * p.chunk_line.row_tiles);
+  p.chunk_blocks = !chunk ? 0 : (unsigned)(p.chunk_line.pieces ? p.chunk_line.pieces : heads * p.chunk_line.row_tiles);
   const unsigned few = !rows ? 0 : (unsigned)(p.rows_line.pieces ? p.rows_line.pieces : heads);
   const dim3 grid(p.chunk_blocks + few), block(64 * kAttnWaves);
-  if (!chunk || (wide && rows)) hipLaunchKernelGGL((attn_kernel<D, FP8, true, false>), grid, block, 0, stream, a, p);
-  else if (wide) return hipSuccess;
+  if (!chunk) hipLaunchKernelGGL((attn_kernel<D, FP8, true, false>), grid, block, 0, stream, a, p);
   else if (!rows) hipLaunchKernelGGL((attn_kernel<D, FP8, false, true>), grid, block, 0, stream, a, p);
   else hipLaunchKernelGGL((attn_kernel<D, FP8, true, true>), grid, block, 0, stream, a, p);
   const hipError_t e = hipGetLastError();

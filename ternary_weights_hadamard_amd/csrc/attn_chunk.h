@@ -8,12 +8,18 @@
 // forms of each 16 positions are, as they are, its operand of O' = V' P'.
 // Weights never leave their lane.
 //
-// What bounds it: the matrix unit, the vector unit (scores -> weights) and the
-// LDS reads of the operands take about as long as one another (for 64
-// positions and 32 rows of 128: 1024 cycles of each), so the kernel lives from
-// overlapping them: two workgroups of four waves per CU, a tile of 64
-// positions of K and V double buffered in LDS and loaded by the
-// global-to-LDS path while the tile before it is worked on.
+// What bounds it: the matrix unit, if the vector work of turning scores into
+// weights runs beside it: for 32 positions and 32 rows of 128 channels the
+// products take 512 cycles, the weights about 300.  Two waves on a SIMD do not
+// overlap the two by themselves (as two phases a tile, the matrix unit was busy
+// 35 % of the time and the vector unit 41 %, one after the other: a wave waits
+// for its operands from LDS, for its products or for the other wave).  So the
+// instruction stream interleaves them: beside each product of the next 32
+// positions' scores two of these scores become weights, and beside the products
+// of these positions' values the maximum of the next scores is taken.  The
+// decision to rescale is what is left outside.  Tiles of 64 positions of K and
+// V are double buffered in LDS by the global-to-LDS path, each loaded one tile
+// ahead; two workgroups of four waves share a CU.
 #pragma once
 
 #include "attn_rows.h"
@@ -28,6 +34,13 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const
 }
 __device__ __forceinline__ f32x16 mfma32(const f16x8& a, const f16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// Until at most N of the wave's loads are still on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  // vmcnt: bits 3..0 and 15..14; the other counters are not waited for
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
 template <bool FP8>
@@ -54,6 +67,17 @@ __device__ __forceinline__ int k_chunk(int row, int c) {
   return row * (D / 8) + (c ^ (row & (D / 8 - 1)));
 }
 __device__ __forceinline__ int v_chunk(int row, int c) { return row * (kTile / 8) + (c ^ ((row >> 1) & 7)); }
+
+// Its argument is in vector registers at this point of the program, and may
+// have changed: what makes it cannot be moved behind, what uses it not before.
+template <typename T>
+__device__ __forceinline__ void hold(T& x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(x));
+#else
+  (void)x;
+#endif
+}
 
 // Values that are not finite, in a tile that not every row sees all of (the
 // products multiply every value with every row's weight, 0 where it does not
@@ -220,36 +244,45 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   auto holder = [&](int g) { return FP8 ? g : 2 * g ^ 4 * (wave & 1); };  // bf16: row v_row of lanes 0..7 is 8 wave
   auto run_page = [&](int pages, int g) { return __builtin_amdgcn_readlane(pages, holder(g)); };
   u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
-  auto stage = [&](int t, int pages, u32x4* k_to, u32x4* v_to) {
+  auto stage_k = [&](int t, int pages, u32x4* to) {
+    const int x0 = (first_tile + t) * kTile;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int run = (i * kStep + uniform(k_row)) >> 4, page = run_page(pages, run);
+      const Elem* kp = kc + (page < 0 ? 0 : page) * page_step + ((x0 + 16 * run) & (c.page - 1)) * D;
+      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(kp + k_off);
+      else
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(kp + k_off),
+                                         (__attribute__((address_space(3))) uint32_t*)&to[i * 64 * kWaves + wave * 64], 16, 0, 0);
+    }
+  };
+  auto stage_v = [&](int t, int pages, u32x4* to) {
     const int x0 = (first_tile + t) * kTile;
     const Elem* vp = vc + (pages < 0 ? 0 : pages) * page_step + ((x0 + 16 * v_run) & (c.page - 1)) + v_off;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int run = (i * kStep + __builtin_amdgcn_readfirstlane(k_row)) >> 4;
-      const int page = run_page(pages, run);
-      const Elem* kp = kc + (page < 0 ? 0 : page) * page_step + (int64_t)((x0 + 16 * run) & (c.page - 1)) * D;
-      if constexpr (FP8) {
-        kr[i] = *reinterpret_cast<const u32x4*>(kp + k_off);
-        vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
-      } else {
-        const int at = i * 64 * kWaves + wave * 64;  // the wave's first chunk
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(kp + k_off),
-                                         (__attribute__((address_space(3))) uint32_t*)&k_to[at], 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) uint32_t*)(vp + i * vStep * c.page),
-            (__attribute__((address_space(3))) uint32_t*)&v_to[at], 16, 0, 0);
-      }
+      if constexpr (FP8) vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
+      else
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(vp + i * vStep * c.page),
+                                         (__attribute__((address_space(3))) uint32_t*)&to[i * 64 * kWaves + wave * 64], 16, 0, 0);
     }
   };
-  auto widen = [&](u32x4* k_to, u32x4* v_to) {  // 8-bit: the staged registers into LDS
+  // 8-bit: the staged registers into LDS
+  auto widen_k = [&](u32x4* to) {
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int kw = i * kStep + k_row, vw = i * vStep + v_row;
-        k_to[k_chunk<D>(kw, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
-        k_to[k_chunk<D>(kw, 2 * k_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][2], kr[i][3]}));
-        v_to[v_chunk(vw, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
-        v_to[v_chunk(vw, 2 * v_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][2], vr[i][3]}));
+        to[k_chunk<D>(i * kStep + k_row, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
+        to[k_chunk<D>(i * kStep + k_row, 2 * k_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][2], kr[i][3]}));
+      }
+    }
+  };
+  auto widen_v = [&](u32x4* to) {
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        to[v_chunk(i * vStep + v_row, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
+        to[v_chunk(i * vStep + v_row, 2 * v_ch + 1)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][2], vr[i][3]}));
       }
     }
   };
@@ -258,117 +291,171 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   // lane's score registers 0..7 are then positions 8 half + 0..7, 8..15 are 16 more
   const int key = 16 * (i32 >> 4) + 8 * ((i32 >> 2) & 1) + 4 * ((i32 >> 3) & 1) + (i32 & 3);
 
-  float m = -__builtin_inff(), l = 0.f;  // maximum (log2 units) that the weights are relative to, and the lane's sum
-  f32x16 o[DT];
+  float m = -__builtin_inff(), base = 0.f;  // maximum (log2 units) that the weights are relative to; the same, or 0
+  float l = 0.f;                            // the lane's sum
+  f32x16 o[DT], sc[2];                      // scores of the first and of the second 32 positions of a tile
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[dt][e] = 0.f;
+  float top = 0.f;  // of the lane's newest scores
+
+  auto runs_of = [&](int pages) -> uint32_t {  // which of a tile's runs exist
+    uint32_t there = 0xfu;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (run_page(pages, g) < 0) there &= ~(1u << g);
+    return there;
+  };
+
+  // New scores (part u of tile t): what the rows do not see out, the maximum,
+  // and the values' sums rescaled if it has grown by more than 2^8.  Until then
+  // weights stay relative to the older one: nothing is rounded more (they are
+  // at most 2^8).
+  auto settle = [&](f32x16& x, int t, int u, uint32_t there) {
+    const int x0 = (first_tile + t) * kTile;
+    if (!(there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > (int64_t)pos_last - a.window))) {
+      const int64_t rel = (int64_t)x0 + 32 * u + 8 * half;
+      const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 31 ? 31 : pos - rel) : -1;
+      const int lo = (int)(low - rel < -1 ? -1 : low - rel > 31 ? 31 : low - rel);
+      top = -__builtin_inff();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int y = 16 * (e >> 3) + (e & 7);
+        const bool see = y <= hi && y > lo && ((there >> (2 * u + (e >> 3))) & 1u);
+        x[e] = see ? x[e] : -__builtin_inff();
+        top = fmaxf(top, x[e]);
+      }
+    }
+    float t0, t1;
+    swap_halves(top, t0, t1);
+    const float row_top = fmaxf(t0, t1) * scale2;
+    if (__ballot(row_top > m + 8.f) != 0) {
+      const float m_new = fmaxf(m, row_top);
+      const float alpha = m == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
+      m = m_new;
+      base = m_new == -__builtin_inff() ? 0.f : m_new;
+      l *= alpha;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[dt][e] *= alpha;
+    }
+  };
+
+  // Scores `now` become weights and their values' sums (part uv of v_lds),
+  // beside the products of the scores `next` (part uk of the keys in k_lds).
+  auto beside = [&](f32x16& now, f32x16& next, const u32x4* k_lds, int uk, const u32x4* v_lds, int uv) {
+    static_assert(2 * DT == KK, "as many products of values as of keys");
+    constexpr int kProducts = 2 * KK, kAhead = 4;
+    constexpr int kScores = 16 / KK;  // scores turned beside a product of keys
+    u32x4 operand[kProducts];
+    V8 w[2];
+    auto load = [&](int i) {  // of product i: the keys' come first
+      operand[i] = i < KK ? k_lds[k_chunk<D>(32 * uk + key, 2 * i + half)]
+                          : v_lds[v_chunk(32 * ((i - KK) % DT) + i32, 2 * (2 * uv + (i - KK) / DT) + half)];
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) next[x] = 0.f;
+    // Each round: an operand from LDS for a later product, a product, and what
+    // the vector unit does meanwhile.  The compiler keeps the rounds as they
+    // are; left to itself it forms the products in a row and then the weights.
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      if (i + kAhead < kProducts) load(i + kAhead);
+      if (i < KK) {
+        next = mfma32(__builtin_bit_cast(bf16x8, operand[i]), q[i], next);
+#pragma unroll
+        for (int k = 0; k < kScores; ++k) {
+          const int x = i * kScores + k;
+          const float p = exp2_fast(fmaf(now[x], scale2, -base));
+          l += p;
+          w[x >> 3][x & 7] = ChunkOps<FP8>::narrow(p);
+        }
+      } else {
+        o[(i - KK) % DT] = mfma32(__builtin_bit_cast(V8, operand[i]), w[(i - KK) / DT], o[(i - KK) % DT]);
+        if (i >= KK + KK / 2) {
+          constexpr int kEach = 32 / KK;
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) {
+            const int x = (i - KK - KK / 2) * kEach + k;
+            top = x == 0 ? next[0] : fmaxf(top, next[x]);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    hold(l);  // here, not where it is next used
+    hold(top);
+  };
 
   bool marked = false;
 #pragma unroll
   for (int i = 0; i < kRows * D / 16 / (64 * kWaves); ++i) sm.marks[i * 64 * kWaves + tid] = 0u;  // a barrier follows
-  int pages = lookup(t_begin), pages_next = lookup(t_begin + 1);
+  const bool idle = r0 + wave * 32 >= nrows;  // the wave has no row: it only loads
+  int p0 = lookup(t_begin), p1 = lookup(t_begin + 1), p2 = lookup(t_begin + 2);
   if (t_begin < t_end) {
-    stage(t_begin, pages, sm.buffer[0], sm.buffer[1]);
-    widen(sm.buffer[0], sm.buffer[1]);
-  }
-  // Tile t, in k_lds and v_lds, while tile t + 1 is loaded into k_to and v_to.
-  // The four are arrays of their own, and which is which is known when this is
-  // compiled: the compiler then knows that reading the one does not wait for
-  // the loads into the other.
-  auto step = [&](int t, u32x4* k_lds, u32x4* v_lds, u32x4* k_to, u32x4* v_to) {
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's share of the tile is in LDS
-    __syncthreads();
-    if (t + 1 < t_end) stage(t + 1, pages_next, k_to, v_to);
-    const int pages_after = lookup(t + 2);
-    const int x0 = (first_tile + t) * kTile;
-    uint32_t there = 0xfu;  // which of the tile's runs exist
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (run_page(pages, g) < 0) there &= ~(1u << g);
-    // does any row of the wave see any of it; do all of the workgroup's see all of it
-    const bool any = x0 <= pos_last && (a.window <= 0 || x0 + kTile - 1 > pos_first - a.window);
-    const bool all_full = there == 0xfu && x0 + kTile - 1 <= all_first && (a.window <= 0 || x0 > all_last - a.window);
-    f32x16 sc[2];
-    if (any) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sc[0][e] = sc[1][e] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          sc[u] = mfma32(__builtin_bit_cast(bf16x8, k_lds[k_chunk<D>(32 * u + key, 2 * kk + half)]), q[kk], sc[u]);
-
-      // The lane's scores: register 8 k + e of tile u is position 32 u + 16 k + 8 half + e.
-      const bool full = there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > pos_last - a.window);
-      if (!full) {
-        const int64_t rel = (int64_t)x0 + 8 * half;
-        const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 63 ? 63 : pos - rel) : -1;
-        const int lo = (int)(low - rel < -1 ? -1 : low - rel > 63 ? 63 : low - rel);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int x = 32 * u + 16 * (e >> 3) + (e & 7);
-            const bool see = x <= hi && x > lo && ((there >> (2 * u + (e >> 3))) & 1u);
-            sc[u][e] = see ? sc[u][e] : -__builtin_inff();
-          }
-      }
-
-      float top = sc[0][0];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[u][e]);
-      float t0, t1;
-      swap_halves(top, t0, t1);
-      top = fmaxf(t0, t1) * scale2;
-      // The weights stay relative to an older maximum while the new one is
-      // less than 2^8 above it: nothing is rounded more (they are at most 2^8),
-      // and the values' sums are rarely rescaled.
-      if (__ballot(top > m + 8.f) != 0) {
-        const float m_new = fmaxf(m, top);
-        const float alpha = m == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
-        m = m_new;
-        l *= alpha;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[dt][e] *= alpha;
-      }
-      const float base = m == -__builtin_inff() ? 0.f : m;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sc[u][e] = exp2_fast(fmaf(sc[u][e], scale2, -base));
-          l += sc[u][e];
-        }
+    stage_k(t_begin, p0, sm.buffer[0]);
+    stage_v(t_begin, p0, sm.buffer[2]);
+    widen_k(sm.buffer[0]);
+    widen_v(sm.buffer[2]);
+    if (t_begin + 1 < t_end) {
+      stage_k(t_begin + 1, p1, sm.buffer[1]);
+      widen_k(sm.buffer[1]);
     }
-
-    if (!all_full)
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (!idle) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) sc[0][x] = sc[1][x] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KK; ++i)
+        sc[0] = mfma32(__builtin_bit_cast(bf16x8, sm.buffer[0][k_chunk<D>(key, 2 * i + half)]), q[i], sc[0]);
+      top = sc[0][0];
+#pragma unroll
+      for (int x = 1; x < 16; ++x) top = fmaxf(top, sc[0][x]);
+      settle(sc[0], t_begin, 0, runs_of(p0));
+    }
+  }
+  // Tile t: K in k_lds, V in v_lds, K of t + 1 in k_next; V of t + 1 goes to
+  // v_next, and K of t + 2, once all scores of t are formed, to k_lds.  The four
+  // are arrays of their own, and which is which is known when this is compiled:
+  // the compiler then knows that reading the one does not wait for the loads
+  // into the other.
+  auto step = [&](int t, u32x4* k_lds, u32x4* k_next, u32x4* v_lds, u32x4* v_next) {
+    // V of t has come: what was issued after it (K of t + 1) may still be on its way
+    if (!FP8 && t + 1 < t_end) wait_loads<kLoads>();
+    else wait_loads<0>();
+    __syncthreads();
+    if (t + 1 < t_end) stage_v(t + 1, p1, v_next);
+    const int p3 = lookup(t + 3);
+    const int x0 = (first_tile + t) * kTile;
+    const uint32_t there = runs_of(p0);
+    if (!(there == 0xfu && x0 + kTile - 1 <= all_first && (a.window <= 0 || x0 > (int64_t)all_last - a.window)))
       take_nonfinite_tile<D, FP8, kRows>(v_lds, sm.marks, marked, x0, there, span.begin, span.end, s.first_pos, group, r0,
                                          nrows, a.window);
-
-    if (any) {
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        V8 w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = ChunkOps<FP8>::narrow(sc[kb >> 1][8 * (kb & 1) + e]);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-          o[dt] = mfma32(__builtin_bit_cast(V8, v_lds[v_chunk(32 * dt + i32, 2 * kb + half)]), w, o[dt]);
-      }
+    if (!idle) {
+      beside(sc[0], sc[1], k_lds, 1, v_lds, 0);
+      settle(sc[1], t, 1, there);
     }
-    pages = pages_next;
-    pages_next = pages_after;
-    widen(k_to, v_to);
+    wait_loads<FP8 ? 0 : kLoads>();  // K of t + 1 has come; V of t + 1, issued after it, may be on its way
+    __syncthreads();
+    if (t + 2 < t_end) stage_k(t + 2, p2, k_lds);
+    if (!idle) {
+      beside(sc[1], sc[0], k_next, 0, v_lds, 1);  // past the last tile: scores of what lies in k_next, not used
+      if (t + 1 < t_end) settle(sc[0], t + 1, 0, runs_of(p1));
+    }
+    widen_v(v_next);
+    if (t + 2 < t_end) widen_k(k_lds);
+    p0 = p1;
+    p1 = p2;
+    p2 = p3;
   };
   for (int t = t_begin; t < t_end; t += 2) {
     step(t, sm.buffer[0], sm.buffer[1], sm.buffer[2], sm.buffer[3]);
-    if (t + 1 < t_end) step(t + 1, sm.buffer[2], sm.buffer[3], sm.buffer[0], sm.buffer[1]);
+    if (t + 1 < t_end) step(t + 1, sm.buffer[1], sm.buffer[0], sm.buffer[3], sm.buffer[2]);
   }
 
   // the row's sum, and its output: register 4 j + e of tile dt is channel 32 dt + 8 j + 4 half + e

@@ -36,8 +36,7 @@ struct AttnPlan {
 
 constexpr int kAttnWaves = 4;    // waves of a workgroup
 constexpr int kRowsTile = 16;    // rows of a row tile: few rows,
-constexpr int kChunkTile = 128;  // chunks,
-constexpr int kWideTile = 256;   // and chunks whose row tiles fill the GPU
+constexpr int kChunkTile = 128;  // and chunks
 // positions of a tile: few rows (the cache's type), and chunks
 __host__ __device__ constexpr int rows_positions(bool fp8) { return fp8 ? 64 : 32; }
 constexpr int kChunkPositions = 64;
@@ -52,17 +51,11 @@ __device__ __forceinline__ TileSpan tile_span(const PagedSpan& p, int positions)
 }
 
 // A workgroup's LDS.  Few rows: a buffer and 16 of max and of sum for each
-// wave.  Chunks: K, V of a tile, and K, V of the next.
+// wave.  Chunks: K of two tiles, V of two tiles.
 struct AttnShared {
   u32x4* buffer[4];
   float *max, *sum;
   uint32_t* marks;  // of chunks: values that are not finite (attn_chunk.h)
-};
-
-// Three tiles of K and of V.
-struct WideShared {
-  u32x4 *k[3], *v[3];
-  uint32_t* marks;
 };
 
 // What a row's weighted values are multiplied with; its log-sum-exp is
