@@ -705,7 +705,7 @@ TB_API tb_status tb_paged_attention(const tb_paged_attention_args* args, void* s
  *   tokens  int32 [B][max_draft + 1]: the kept tokens, the drawn one, then -1
  *           (the drawn one is -1 too if no weight of p_m is positive and finite)
  *   workspace  tb_verify_draft_workspace(B, vocab) bytes of device memory,
- *           16-byte aligned
+ *           16-byte aligned (none up to a vocabulary of 2^15: may be NULL)
  * p, q, u, drafts need only their elements' alignment.
  */
 #define TB_MAX_DRAFT 64
@@ -732,7 +732,8 @@ typedef struct {
   int reserved;  /* must be 0 */
 } tb_verify_draft_args;
 
-/* Workspace bytes of tb_verify_draft.  Host-only; 0 for invalid sizes. */
+/* Workspace bytes of tb_verify_draft.  Host-only; 0 when none is used, and for
+ * invalid sizes. */
 TB_API size_t tb_verify_draft_workspace(int64_t B, int64_t vocab);
 
 TB_API tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream);

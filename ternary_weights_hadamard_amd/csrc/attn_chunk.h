@@ -234,7 +234,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int k_ch = FP8 ? tid % (D / 16) : (tid % (D / 8)) ^ (k_row & (D / 8 - 1));
   const int v_ch = FP8 ? tid % 4 : (tid % 8) ^ ((v_row >> 1) & 7);
   const int v_run = FP8 ? v_ch : v_ch >> 1;
-  const int k_off = (k_row & 15) * D + k_ch * kPer;                 // inside a run
+  const uint32_t k_off = ((k_row & 15) * D + k_ch * kPer) * sizeof(Elem);  // bytes, inside a run
   const int v_off = v_row * c.page + (v_ch * kPer & 15);
   auto lookup = [&](int t) -> int {
     const int x = (first_tile + t) * kTile + 16 * v_run;
@@ -250,9 +250,11 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     for (int i = 0; i < kLoads; ++i) {
       const int run = (i * kStep + uniform(k_row)) >> 4, page = run_page(pages, run);
       const Elem* kp = kc + (page < 0 ? 0 : page) * page_step + ((x0 + 16 * run) & (c.page - 1)) * D;
-      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(kp + k_off);
+      // a uniform address and a 32-bit offset of the lane
+      const char* from = reinterpret_cast<const char*>(kp) + k_off;
+      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(from);
       else
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(kp + k_off),
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
                                          (__attribute__((address_space(3))) uint32_t*)&to[i * 64 * kWaves + wave * 64], 16, 0, 0);
     }
   };

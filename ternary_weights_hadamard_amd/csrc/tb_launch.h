@@ -43,8 +43,10 @@ hipError_t launch_gemm_ternary_splitk(const uint16_t* x, int64_t M, const uint32
                                       size_t workspace_bytes, bool rotate, hipStream_t stream);
 
 hipError_t launch_block_norm(const tb_block_norm_args& a, hipStream_t stream);
-// vocabulary entries one workgroup sums
-constexpr int64_t kVerifySlice = 2048;
+// vocabularies up to this take one launch and no workspace
+constexpr int64_t kVerifyWhole = 1 << 15;
+// vocabulary entries one workgroup sums in larger ones
+constexpr int64_t kVerifySlice = 4096;
 hipError_t launch_verify_draft(const tb_verify_draft_args& a, hipStream_t stream);
 hipError_t launch_paged_append(const tb_paged_cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                                int64_t v_stride, hipStream_t stream);

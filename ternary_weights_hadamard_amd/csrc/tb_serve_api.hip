@@ -37,7 +37,7 @@ tb_status check_norm(const tb_block_norm_args& a) {
       !(dtype_ok(a.z_dtype) || a.z_dtype == TB_ACT8) || !dtype_ok(a.y_dtype))
     return TB_ERR_DTYPE;
   if (a.parts > 1 && a.y_dtype != TB_F32) return TB_ERR_DTYPE;
-  if (a.rows < 0 || a.C <= 0 || a.C % 128 || a.C > TB_NORM_MAX_C || a.parts < 0 || a.parts > TB_MAX_PARTS)
+  if (a.rows < 0 || a.rows > ((int64_t)1 << 35) || a.C <= 0 || a.C % 128 || a.C > TB_NORM_MAX_C || a.parts < 0 || a.parts > TB_MAX_PARTS)
     return TB_ERR_SHAPE;
   if (a.gate && a.rows_per_gate < 1) return TB_ERR_SHAPE;
   if (!isfinite(a.alpha) || !isfinite(a.eps) || !(a.eps > 0.f)) return TB_ERR_VALUE;
@@ -186,8 +186,9 @@ tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream) 
 }
 
 size_t tb_verify_draft_workspace(int64_t B, int64_t vocab) {
-  if (B <= 0 || B > 65535 || vocab <= 0 || vocab > INT32_MAX) return 0;
-  return (size_t)B * (size_t)((vocab + kVerifySlice - 1) / kVerifySlice) * 16;
+  if (B <= 0 || B > 65535 || vocab <= kVerifyWhole || vocab > INT32_MAX) return 0;
+  // two sums a slice, one count a sequence
+  return ((size_t)B * (size_t)((vocab + kVerifySlice - 1) / kVerifySlice) * 16 + (size_t)B * 4 + 15) / 16 * 16;
 }
 
 tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream) {
@@ -208,7 +209,7 @@ tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream) {
       !aligned16(a.workspace))
     return TB_ERR_ALIGN;
   const size_t need = tb_verify_draft_workspace(a.B, a.vocab);
-  if (!a.workspace || a.workspace_bytes < need) return TB_ERR_WORKSPACE;
+  if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return TB_ERR_WORKSPACE;
   const Range ins[] = {{a.p, strided_bytes(a.total + a.B, a.p_stride, a.vocab, pe)},
                        {a.q, strided_bytes(a.total, a.q_stride, a.vocab, qe)},
                        {a.drafts, (size_t)a.total * 4},

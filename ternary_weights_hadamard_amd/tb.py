@@ -153,8 +153,15 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object (2.7 us a call on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return ctypes.c_void_p(_raw_stream(_raw_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -720,11 +727,13 @@ def tb_verify_draft(p, q, drafts, u, u_next, cu_draft, max_draft, accepted=None,
           and tokens.shape == (b, max_draft + 1), f"{where}: accepted must be int32 [{b}], tokens int32 [{b}, {max_draft + 1}]")
     L = lib()
     if workspace is None:
-        workspace = _empty(max(L.tb_verify_draft_workspace(b, vocab), 16), torch.uint8, dev, stream)
+        nbytes = L.tb_verify_draft_workspace(b, vocab)
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, dev, stream)
     _same_device(dev, q, drafts, u, u_next, cu_draft, accepted, tokens, workspace)
     args = VerifyDraftArgs(p.data_ptr(), _addr(q), drafts.data_ptr(), u.data_ptr(), u_next.data_ptr(),
-                           cu_draft.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), b, total, vocab, ps, qs, max_draft,
+                           cu_draft.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), _addr(workspace),
+                           0 if workspace is None else workspace.numel() * workspace.element_size(), b, total, vocab, ps, qs, max_draft,
                            _float_dt(p, where + ": p"), TB_F32 if q is None else _float_dt(q, where + ": q"), 0)
     _check(L.tb_verify_draft(args, _stream(stream)), where)
     return accepted, tokens

@@ -135,6 +135,9 @@ def _verify(**kw):
     return tb.lib().tb_verify_draft(tb.VerifyDraftArgs(**a), None)
 
 
+BIG = dict(vocab=300000, p_stride=300000, q_stride=300000)
+
+
 @built
 @pytest.mark.parametrize("status,kw", [
     (DTYPE, dict(p_dtype=ACT8)), (DTYPE, dict(q_dtype=7)), (SHAPE, dict(B=-1)), (SHAPE, dict(B=65536)),
@@ -143,8 +146,8 @@ def _verify(**kw):
     (NULL, dict(p=None)), (NULL, dict(u=None)), (NULL, dict(u_next=None)), (NULL, dict(drafts=None)),
     (NULL, dict(cu_draft=None)), (NULL, dict(accepted=None)), (NULL, dict(tokens=None)),
     (ALIGN, dict(p=A + 2)), (ALIGN, dict(q=B + 1, q_dtype=BF16)), (ALIGN, dict(u=C + 4098)), (ALIGN, dict(workspace=E + 4)),
-    (WORKSPACE, dict(workspace=None)), (WORKSPACE, dict(workspace_bytes=16)),
-    (ALIAS, dict(tokens=D)), (ALIAS, dict(accepted=C)), (ALIAS, dict(workspace=A)), (ALIAS, dict(tokens=B + 400)),
+    (WORKSPACE, dict(workspace=None, **BIG)), (WORKSPACE, dict(workspace_bytes=16, **BIG)),
+    (ALIAS, dict(tokens=D)), (ALIAS, dict(accepted=C)), (ALIAS, dict(workspace=A, **BIG)), (ALIAS, dict(tokens=B + 400)),
     (0, dict(B=0, p=None)),
 ])
 def test_verify_refusals(status, kw):
@@ -154,7 +157,7 @@ def test_verify_refusals(status, kw):
 @built
 def test_verify_workspace():
     assert tb.tb_verify_draft_workspace(0, 100) == 0 and tb.tb_verify_draft_workspace(1, 0) == 0
-    assert tb.tb_verify_draft_workspace(3, 1) > 0
+    assert tb.tb_verify_draft_workspace(3, 1 << 15) == 0 and tb.tb_verify_draft_workspace(3, (1 << 15) + 1) > 0
 
 
 @built
