@@ -389,6 +389,28 @@ def test_append(lens, hkv, d, page, cache):
     assert torch.equal(gk, k) and torch.equal(gv, v)
 
 
+def test_append_every_value():
+    """All bf16 patterns over the scales of eight heads, each pattern with each
+    scale: the codes are those of the division, bit for bit."""
+    c = Case([(64, 64)], 8, 8, 128, 16, "fp8", poison=False)
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).to(DEV)
+    scales = torch.tensor([1.0, 0.0371, 2.0 / 3, 1e-30, 7e25, 1.7e-12, 449.0, 3e-3], device=DEV)
+    for i in range(8):
+        say(f"append every value, turn {i}")
+        c.new_k, c.new_v = every.view(64, 8, 128), every.flip(0).view(64, 8, 128)
+        c.k_scale, c.v_scale = scales.roll(i).contiguous(), scales.roll(i + 3).contiguous()
+        c.append()
+        torch.cuda.synchronize()
+        pages = torch.from_numpy(c.table[0, :4]).to(DEV)
+        k = c.k[pages].view(torch.uint8).permute(0, 2, 1, 3).reshape(64, 8, 128)
+        v = c.v[pages].view(torch.uint8).permute(0, 3, 1, 2).reshape(64, 8, 128)
+        for got, x, scale in ((k, c.new_k, c.k_scale), (v, c.new_v, c.v_scale)):
+            want = (x.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            nan = torch.isnan(x)
+            assert ((got & 0x7f) == 0x7f)[nan].all()
+            assert torch.equal(got[~nan], want[~nan])
+
+
 def test_append_then_attend():
     """Chunk by chunk through the cache is the whole sequence at once."""
     c = Case([(200, 200)], 4, 2, 128, 32, "bf16", poison=False)
