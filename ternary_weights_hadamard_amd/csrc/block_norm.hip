@@ -8,10 +8,11 @@
 // the in-register butterflies of fwht_lanes.h.  Each norm is one sum over the
 // row: a wave reduction in registers, then one LDS exchange between the waves.
 //
-// What bounds it: HBM for many rows (2048 rows of 5120, y, gate, residual and
-// h in bf16, 105 MB: 22.9 us, 4.6 TB/s), the chain load - sum - sum - store for
-// a few (one row: 4.8 us).  So the arrays of rows are loaded before the first sum, raw, and widened
-// when used, and the weights of a norm before its sum is known.
+// What bounds it: HBM for many rows (2048 rows of 5120, y, gate and residual
+// read, h and z written in bf16, 105 MB: 22.9 us, 4.6 TB/s), the chain load -
+// sum - sum - store for a few (one row: 4.8 us).  So the arrays of rows are
+// loaded before the first sum, raw, and widened when used, and the weights of a
+// norm before its sum is known.
 #include "act8.h"
 #include "fwht_lanes.h"
 #include "tb_common.h"
