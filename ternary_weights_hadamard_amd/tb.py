@@ -495,15 +495,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _need(ok, message):
-    if not ok:
-        raise ValueError(message)
-
-
-def _same_device(dev, *ts):
+def _same_device(first, *ts):
+    index = first.get_device()
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"every tensor must be on {dev} (got one on {t.device})")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on {first.device} (got one on {t.device})")
 
 
 def tb_block_norm(y, resid=None, w_post=None, w_pre=None, gate=None, rows_per_gate=1, alpha=1.0, eps=1e-6, y_parts=1,
@@ -519,41 +515,54 @@ def tb_block_norm(y, resid=None, w_post=None, w_pre=None, gate=None, rows_per_ga
     made when not given; z_dtype torch.uint8 writes the act8 operand."""
     _dev(y, resid, w_post, w_pre, gate, h, z)
     first = resid if y is None else y
-    _need(first is not None, "tb_block_norm: y or resid must be given")
+    if not (first is not None):
+        raise ValueError("tb_block_norm: y or resid must be given")
     parts = int(y_parts)
     if y is not None and parts > 1:
-        _need(y.dim() == 3 and y.shape[0] == parts, f"tb_block_norm: y_parts={parts} needs y [{parts}, rows, C]")
+        if not (y.dim() == 3 and y.shape[0] == parts):
+            raise ValueError(f"tb_block_norm: y_parts={parts} needs y [{parts}, rows, C]")
     else:
-        _need(first.dim() == 2, "tb_block_norm: y must be [rows, C]")
+        if not (first.dim() == 2):
+            raise ValueError("tb_block_norm: y must be [rows, C]")
     rows, ch = first.shape[-2], first.shape[-1]
     dev = first.device
-    _same_device(dev, y, resid, w_post, w_pre, gate, h, z)
-    _need(resid is None or tuple(resid.shape) == (rows, ch), f"tb_block_norm: resid must be [{rows}, {ch}]")
+    _same_device(first, y, resid, w_post, w_pre, gate, h, z)
+    if not (resid is None or resid.shape == (rows, ch)):
+        raise ValueError(f"tb_block_norm: resid must be [{rows}, {ch}]")
     for w in (w_post, w_pre):
-        _need(w is None or tuple(w.shape) == (ch,), f"tb_block_norm: w_post and w_pre must be [{ch}]")
-    _need(w_post is None or w_pre is None or w_post.dtype == w_pre.dtype, "tb_block_norm: w_post and w_pre differ in dtype")
+        if not (w is None or w.shape == (ch,)):
+            raise ValueError(f"tb_block_norm: w_post and w_pre must be [{ch}]")
+    if not (w_post is None or w_pre is None or w_post.dtype == w_pre.dtype):
+        raise ValueError("tb_block_norm: w_post and w_pre differ in dtype")
     if gate is not None:
         rows_per_gate = int(rows_per_gate)
-        _need(rows_per_gate >= 1, "tb_block_norm: rows_per_gate must be at least 1")
-        _need(gate.dim() == 2 and gate.shape[1] == ch and gate.shape[0] * rows_per_gate >= rows,
-              f"tb_block_norm: gate must be [{-(-rows // rows_per_gate)}, {ch}] at rows_per_gate {rows_per_gate}")
+        if rows_per_gate < 1:
+            raise ValueError("tb_block_norm: rows_per_gate must be at least 1")
+        if not (gate.dim() == 2 and gate.shape[1] == ch and gate.shape[0] * rows_per_gate >= rows):
+            raise ValueError(f"tb_block_norm: gate must be [{-(-rows // rows_per_gate)}, {ch}] at rows_per_gate {rows_per_gate}")
     if y is None or not with_h:
-        _need(h is None, "tb_block_norm: no h without y or with with_h=False")
+        if h is not None:
+            raise ValueError("tb_block_norm: no h without y or with with_h=False")
     elif h is None:
         h = _empty((rows, ch), resid.dtype if resid is not None else h_dtype or y.dtype, dev, stream)
-    _need(h is None or tuple(h.shape) == (rows, ch), f"tb_block_norm: h must be [{rows}, {ch}]")
-    _need(h is None or resid is None or h.dtype == resid.dtype, "tb_block_norm: h and resid differ in dtype")
+    if not (h is None or h.shape == (rows, ch)):
+        raise ValueError(f"tb_block_norm: h must be [{rows}, {ch}]")
+    if not (h is None or resid is None or h.dtype == resid.dtype):
+        raise ValueError("tb_block_norm: h and resid differ in dtype")
     if w_pre is None:
-        _need(z is None, "tb_block_norm: z needs w_pre")
+        if z is not None:
+            raise ValueError("tb_block_norm: z needs w_pre")
     elif z is None:
         if z_dtype == torch.uint8:
             z = _empty(tb_act8_bytes(rows, ch), torch.uint8, dev, stream)
         else:
             z = _empty((rows, ch), z_dtype, dev, stream)
     elif z.dtype == torch.uint8:
-        _need(z.numel() == tb_act8_bytes(rows, ch), f"tb_block_norm: z must hold {tb_act8_bytes(rows, ch)} bytes")
+        if not (z.numel() == tb_act8_bytes(rows, ch)):
+            raise ValueError(f"tb_block_norm: z must hold {tb_act8_bytes(rows, ch)} bytes")
     else:
-        _need(tuple(z.shape) == (rows, ch), f"tb_block_norm: z must be [{rows}, {ch}]")
+        if not (z.shape == (rows, ch)):
+            raise ValueError(f"tb_block_norm: z must be [{rows}, {ch}]")
     w = w_post if w_post is not None else w_pre
     zd = TB_F32 if z is None else TB_ACT8 if z.dtype == torch.uint8 else _float_dt(z, "tb_block_norm: z")
     s = resid if resid is not None else h
@@ -601,7 +610,7 @@ def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max
     for sc in (k_scale, v_scale):
         if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):
             raise ValueError(f"{where}: k_scale and v_scale must be float32 [{heads}], of an 8-bit cache")
-    _same_device(tokens.device, k_cache, v_cache, block_table, cu_q, kv_len, k_scale, v_scale)
+    _same_device(tokens, k_cache, v_cache, block_table, cu_q, kv_len, k_scale, v_scale)
     width = block_table.shape[1]
     stride = block_table.stride(0) if b > 1 else width
     return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
@@ -617,10 +626,11 @@ def tb_paged_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_
     bf16 or float8_e4m3fn (codes of x / scale[head]); max_q is at least every
     sequence's new tokens."""
     cache = _paged_cache("tb_paged_append", k, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
-    _same_device(k.device, v)
+    _same_device(k, v)
     ks = _token_rows(k, cache.heads_kv, cache.head_dim, "tb_paged_append: k")
     vs = _token_rows(v, cache.heads_kv, cache.head_dim, "tb_paged_append: v")
-    _need(v.shape[0] == k.shape[0], "tb_paged_append: k and v differ in tokens")
+    if not (v.shape[0] == k.shape[0]):
+        raise ValueError("tb_paged_append: k and v differ in tokens")
     _check(lib().tb_paged_append(cache, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "tb_paged_append")
 
 
@@ -657,7 +667,8 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
     if out is not None:
         _dev(out)
         out_dt = _float_dt(out, "tb_paged_attention: out")
-        _need(out.shape == q.shape, f"tb_paged_attention: out must be {tuple(q.shape)}")
+        if not (out.shape == q.shape):
+            raise ValueError(f"tb_paged_attention: out must be {tuple(q.shape)}")
     else:
         out = _empty(q.shape, out_dtype, q.device, stream)
         out_dt = _float_dt(out, "tb_paged_attention: out")
@@ -665,8 +676,8 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
                            v_scale, out_dt)
     if lse is not None:
         _dev(lse)
-        _need(lse.dtype == torch.float32 and lse.shape == q.shape[:2],
-              f"tb_paged_attention: lse must be float32 {tuple(q.shape[:2])}")
+        if not (lse.dtype == torch.float32 and lse.shape == q.shape[:2]):
+            raise ValueError(f"tb_paged_attention: lse must be float32 {tuple(q.shape[:2])}")
     elif with_lse:
         lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     L = lib()
@@ -676,7 +687,7 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
             workspace = _empty(nbytes, torch.uint8, q.device, stream)
     else:
         _dev(workspace)
-    _same_device(q.device, out, lse, workspace)
+    _same_device(q, out, lse, workspace)
     args.out, args.lse = out.data_ptr(), _addr(lse)
     if workspace is not None:
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -709,31 +720,35 @@ def tb_verify_draft(p, q, drafts, u, u_next, cu_draft, max_draft, accepted=None,
     max_draft = int(max_draft)
     ps = _prob_rows(p, where + ": p")
     vocab = p.shape[1]
-    _need(p.shape[0] == total + b, f"{where}: p must have {total + b} rows (drafts + sequences)")
+    if not (p.shape[0] == total + b):
+        raise ValueError(f"{where}: p must have {total + b} rows (drafts + sequences)")
     qs = 0
     if q is not None:
         qs = _prob_rows(q, where + ": q")
-        _need(q.shape == (total, vocab), f"{where}: q must be [{total}, {vocab}]")
-    _need(drafts.dtype == cu_draft.dtype == torch.int32, f"{where}: drafts and cu_draft must be int32")
-    _need(u.dtype == u_next.dtype == torch.float32, f"{where}: u and u_next must be float32")
-    _need(drafts.dim() == 1 and u.shape == drafts.shape and u_next.dim() == 1 and cu_draft.shape == (b + 1,),
-          f"{where}: drafts and u must be [total], u_next [B], cu_draft [B + 1]")
+        if not (q.shape == (total, vocab)):
+            raise ValueError(f"{where}: q must be [{total}, {vocab}]")
+    if not (drafts.dtype == cu_draft.dtype == torch.int32):
+        raise ValueError(f"{where}: drafts and cu_draft must be int32")
+    if not (u.dtype == u_next.dtype == torch.float32):
+        raise ValueError(f"{where}: u and u_next must be float32")
+    if not (drafts.dim() == 1 and u.shape == drafts.shape and u_next.dim() == 1 and cu_draft.shape == (b + 1,)):
+        raise ValueError(f"{where}: drafts and u must be [total], u_next [B], cu_draft [B + 1]")
     dev = p.device
     if accepted is None:
         accepted = _empty(b, torch.int32, dev, stream)
     if tokens is None:
         tokens = _empty((b, max(max_draft, 0) + 1), torch.int32, dev, stream)
-    _need(accepted.dtype == tokens.dtype == torch.int32 and accepted.shape == (b,)
-          and tokens.shape == (b, max_draft + 1), f"{where}: accepted must be int32 [{b}], tokens int32 [{b}, {max_draft + 1}]")
+    if not (accepted.dtype == tokens.dtype == torch.int32 and accepted.shape == (b,) and tokens.shape == (b, max_draft + 1)):
+        raise ValueError(f"{where}: accepted must be int32 [{b}], tokens int32 [{b}, {max_draft + 1}]")
     L = lib()
     if workspace is None:
         nbytes = L.tb_verify_draft_workspace(b, vocab)
         if nbytes:
             workspace = _empty(nbytes, torch.uint8, dev, stream)
-    _same_device(dev, q, drafts, u, u_next, cu_draft, accepted, tokens, workspace)
+    _same_device(p, q, drafts, u, u_next, cu_draft, accepted, tokens, workspace)
     args = VerifyDraftArgs(p.data_ptr(), _addr(q), drafts.data_ptr(), u.data_ptr(), u_next.data_ptr(),
                            cu_draft.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), _addr(workspace),
-                           0 if workspace is None else workspace.numel() * workspace.element_size(), b, total, vocab, ps, qs, max_draft,
-                           _float_dt(p, where + ": p"), TB_F32 if q is None else _float_dt(q, where + ": q"), 0)
+                           0 if workspace is None else workspace.numel() * workspace.element_size(), b, total, vocab,
+                           ps, qs, max_draft, _float_dt(p, where + ": p"), TB_F32 if q is None else _float_dt(q, where + ": q"), 0)
     _check(L.tb_verify_draft(args, _stream(stream)), where)
     return accepted, tokens
