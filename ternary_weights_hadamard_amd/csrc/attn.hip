@@ -39,12 +39,12 @@ __device__ __forceinline__ LineParts parts_of_row(const tb_paged_attention_args&
   const int tiles = K::tiles(a, plan, seq, rt);
   Line<CHUNK, FP8> line(a, plan);
   int64_t start = line.before(a, plan, b);
-  for (int x = 0; x < rt; ++x) start += (int64_t)a.cache.heads_kv * K::tiles(a, plan, seq, x);
+  if constexpr (CHUNK) start += a.cache.heads_kv * K::tiles_before(a, plan, seq, rt);
   return line_parts(start + (int64_t)head * tiles, tiles, cut.piece(line.total));
 }
 
-// Row r in `parts`, joined by L = 16 lanes (many rows: a wave does four) or by
-// all 64 (few rows: what counts is the time of one).  Lane p of them holds the
+// Row r in `parts`, joined by L = 16 lanes (a wave does four) or by all 64
+// (rows in many parts: what counts is the time of one).  Lane p of them holds the
 // statistics of part p, of L at a time, and their groups of 16 take the parts
 // in turn, D / 16 channels a lane.
 template <int D, bool CHUNK, bool FP8, int L>
@@ -115,22 +115,22 @@ __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const
   for (int e = 0; e < DL / 4; ++e) write4(a, at * D + d0 + 4 * e, v[e], rs);
 }
 
-// `rows` rows (a multiple of 4, at most 16) of one key/value head of one sequence.
-template <int D, bool FP8>
-__global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args a, AttnPlan plan, int rows) {
+// ROWS (16, or 4 by whole waves) rows of one key/value head of one sequence.
+template <int D, bool FP8, int ROWS>
+__global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args a, AttnPlan plan) {
   const unsigned heads = (unsigned)a.cache.heads_kv;
-  const int head = blockIdx.x % heads, r0 = blockIdx.x / heads * rows;
+  const int head = blockIdx.x % heads, r0 = blockIdx.x / heads * ROWS;
   const int64_t b = blockIdx.z;
   const LineSeq chunk = LineKind<true, FP8>::sequence(a, plan, b), few = LineKind<false, FP8>::sequence(a, plan, b);
-  if (plan.chunk_line.pieces && r0 < chunk.rows) {  // rows = 16: all of one row tile
+  if (plan.chunk_line.pieces && r0 < chunk.rows) {  // all of one row tile
     const LineParts parts = parts_of_row<true, FP8>(a, plan, b, chunk, head, r0);
-    const int r = r0 + (int)(threadIdx.x >> 4);
-    if (parts.count > 1 && r < chunk.rows) join_row<D, true, FP8, 16>(a, plan, parts, chunk, head, r);
+    const int r = r0 + (int)(ROWS == 16 ? threadIdx.x >> 4 : uniform(threadIdx.x >> 6));
+    if (parts.count > 1 && r < chunk.rows) join_row<D, true, FP8, ROWS == 16 ? 16 : 64>(a, plan, parts, chunk, head, r);
   }
   if (plan.rows_line.pieces && r0 < few.rows) {
     const LineParts parts = parts_of_row<false, FP8>(a, plan, b, few, head, r0);
     if (parts.count == 1) return;  // written by its kernel
-    for (int r = r0 + uniform(threadIdx.x >> 6); r < r0 + rows && r < few.rows; r += 4)
+    for (int r = r0 + uniform(threadIdx.x >> 6); r < r0 + ROWS && r < few.rows; r += 4)
       join_row<D, false, FP8, 64>(a, plan, parts, few, head, r);
   }
 }
@@ -145,6 +145,11 @@ int64_t most_rows(const tb_paged_attention_args& a) { return a.cache.max_q * (a.
 bool has_chunk(const tb_paged_attention_args& a, const AttnPlan& p) { return most_rows(a) > p.few; }
 bool has_rows(const tb_paged_attention_args& a, const AttnPlan& p) {
   return !has_chunk(a, p) || a.cache.total_q < a.cache.B * a.cache.max_q;
+}
+
+// about the items of chunks
+int64_t chunk_items(const tb_paged_attention_args& a, const AttnPlan& p) {
+  return (a.cache.total_q * p.group / kChunkTile + a.cache.B) * a.cache.heads_kv;
 }
 
 AttnPlan plan_of(const tb_paged_attention_args& a) {
@@ -162,14 +167,19 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   p.chunk_line.least = 4;
   p.chunk_line.row_tiles = (int)((most_rows(a) + kChunkTile - 1) / kChunkTile);
   p.chunk_line.slot_rows = kChunkTile;
-  // Short items are not cut.  Nor are chunks whose items fill the GPU: one
-  // after another, the row tiles of a head find its keys and values in L2, while
-  // pieces of a line are all elsewhere (4 x 2048 tokens over 8192, 40 heads: 625
-  // us as items, 883 us as pieces; 8 x 1..9 tokens over 16384: 56 + 65 us with
-  // their positions in fixed parts, 93 us as pieces).
   if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype == TB_FP8)) p.rows_line.pieces = kPieces;
-  const int64_t items = (c.total_q * p.group / kChunkTile + c.B) * c.heads_kv;
-  if (has_chunk(a, p) && keys > p.chunk_line.least * kChunkPositions && items < kPieces) p.chunk_line.pieces = kPieces;
+  // Chunks whose items fill the GPU are not cut: one after another, the row
+  // tiles of a head find its keys and values in L2, while pieces of a line are
+  // all elsewhere (4 x 2048 tokens over 8192, 40 heads: 625 us as items, 883 us
+  // as pieces).  Nor are those of fewer items if it saves less than ten tiles,
+  // which is what a second part's start, the parts' way through memory and the
+  // join take, and pieces run two on a CU, where each takes 5/4 of its time (2 x
+  // 777 tokens of 16 heads: 18 tiles within a window of 1000 38.6 us as items,
+  // 36 + 12 as pieces; 94 tiles without one 141 and 95 + 12).
+  const int64_t seen = a.window + (kChunkTile - 1) / p.group + 1;  // by a row tile, in a window
+  const int64_t most = a.window > 0 && seen < keys ? seen : keys;
+  const int64_t tiles = (most + kChunkPositions - 1) / kChunkPositions, items = chunk_items(a, p);
+  if (has_chunk(a, p) && items < kPieces && tiles - tiles * items * 5 / (4 * kPieces) > 10) p.chunk_line.pieces = kPieces;
   return p;
 }
 
@@ -193,9 +203,12 @@ hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stre
   const hipError_t e = hipGetLastError();
   const int64_t joined = p.chunk_line.pieces ? most_rows(a) : !p.rows_line.pieces ? 0 : most_rows(a) < p.few ? most_rows(a) : p.few;
   if (e != hipSuccess || joined == 0) return e;
-  const int each = p.chunk_line.pieces ? 16 : 4;
-  hipLaunchKernelGGL((attn_join_kernel<D, FP8>), dim3((unsigned)((joined + each - 1) / each * c.heads_kv), 1, (unsigned)c.B),
-                     dim3(256), 0, stream, a, p, each);
+  // Rows of many chunk items are in few parts each, and are many.
+  const bool many = p.chunk_line.pieces && chunk_items(a, p) > kPieces / 4;
+  const int each = many ? 16 : 4;
+  const dim3 join((unsigned)((joined + each - 1) / each * c.heads_kv), 1, (unsigned)c.B);
+  if (many) hipLaunchKernelGGL((attn_join_kernel<D, FP8, 16>), join, dim3(256), 0, stream, a, p);
+  else hipLaunchKernelGGL((attn_join_kernel<D, FP8, 4>), join, dim3(256), 0, stream, a, p);
   return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@
 #pragma once
 
 #include "attn_launch.h"
+#include "wave_scan.h"
 
 namespace tb {
 
@@ -19,11 +20,6 @@ namespace tb {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(uint32_t)((uint64_t)v >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), lane);
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
@@ -58,14 +54,24 @@ struct LineKind {
     const int n = tile_span(span(a, plan, s, rt), kPositions).count;
     return n > 1 ? n : 1;
   }
-  // of all row tiles of the sequence, for one head
-  static __device__ __forceinline__ int64_t tiles(const tb_paged_attention_args& a, const AttnPlan& plan,
-                                                  const LineSeq& s) {
+  // of row tiles 0 .. count - 1, for one head; a whole wave, the same arguments in every lane
+  static __device__ __forceinline__ int64_t tiles_before(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                                         const LineSeq& s, int count) {
     int64_t n = 0;
-    for (int rt = 0; rt * kRows < s.rows; ++rt) n += tiles(a, plan, s, rt);
-    return n;
+    for (int rt = threadIdx.x & 63; rt < count; rt += 64) n += tiles(a, plan, s, rt);
+    return wave_sum(n);
   }
 };
+
+__device__ __forceinline__ LineSeq uniform_seq(const LineSeq& x, int lane) {
+  LineSeq r;
+  r.seq.row0 = of_lane(x.seq.row0, lane);
+  r.seq.n = __builtin_amdgcn_readlane(x.seq.n, lane);
+  r.seq.keys = __builtin_amdgcn_readlane(x.seq.keys, lane);
+  r.seq.first_pos = __builtin_amdgcn_readlane(x.seq.first_pos, lane);
+  r.rows = __builtin_amdgcn_readlane(x.rows, lane);
+  return r;
+}
 
 struct LineItem {
   int64_t start;  // of its first tile in the line
@@ -85,11 +91,7 @@ __device__ __forceinline__ LineItem uniform_item(const LineItem& x) {
   r.b = uniform64(x.b);
   r.rt = uniform(x.rt);
   r.head = uniform(x.head);
-  r.seq.seq.row0 = uniform64(x.seq.seq.row0);
-  r.seq.seq.n = uniform(x.seq.seq.n);
-  r.seq.seq.keys = uniform(x.seq.seq.keys);
-  r.seq.seq.first_pos = uniform(x.seq.seq.first_pos);
-  r.seq.rows = uniform(x.seq.rows);
+  r.seq = uniform_seq(x.seq, 0);
   r.span.begin = uniform(x.span.begin);
   r.span.end = uniform(x.span.end);
   r.held.first = uniform(x.held.first);
@@ -98,7 +100,8 @@ __device__ __forceinline__ LineItem uniform_item(const LineItem& x) {
 }
 
 // The line of one kind.  Whole waves use it together, with the same arguments
-// in every lane.
+// in every lane, and all lanes active: the lanes take a sequence each, and for
+// one of many row tiles a row tile each.
 template <bool CHUNK, bool FP8>
 struct Line {
   typedef LineKind<CHUNK, FP8> K;
@@ -108,58 +111,93 @@ struct Line {
 
   __device__ __forceinline__ void look(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b0) {
     const int lane = threadIdx.x & 63;
-    own.rows = 0;
-    up = 0;
+    own = LineSeq{};
+    int64_t n = 0;
     if (b0 + lane < a.cache.B) {
       own = K::sequence(a, plan, b0 + lane);
-      up = K::tiles(a, plan, own) * a.cache.heads_kv;
+      if (own.rows > 0) n = K::tiles(a, plan, own, 0);
     }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int64_t t = __shfl_up(up, m);
-      if (lane >= m) up += t;
+    if constexpr (CHUNK) {
+      for (uint64_t more = __ballot(own.rows > K::kRows); more != 0; more &= more - 1) {
+        const int l = uniform(__builtin_ctzll(more));
+        const LineSeq s = uniform_seq(own, l);
+        const int64_t t = K::tiles_before(a, plan, s, (s.rows + K::kRows - 1) / K::kRows);
+        if (lane == l) n = t;
+      }
     }
+    up = wave_prefix(n * a.cache.heads_kv);
   }
   __device__ __forceinline__ Line(const tb_paged_attention_args& a, const AttnPlan& plan) {
     total = 0;
     for (int64_t b0 = 0; b0 < a.cache.B; b0 += 64) {
       look(a, plan, b0);
-      total += lane64(up, 63);
+      total += of_lane(up, 63);
     }
   }
-  // nothing looked at yet: only find(.., true) may be called
-  __device__ __forceinline__ Line() : up(0), total(0) {}
   // The item that holds tile `at` < total.
-  __device__ __forceinline__ LineItem find(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at,
-                                           bool again = false) {
+  __device__ __forceinline__ LineItem find(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at) {
     LineItem it{};
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < a.cache.B; b0 += 64) {
-      if (again || a.cache.B > 64) look(a, plan, b0);  // else it holds them since it was made
+      if (a.cache.B > 64) look(a, plan, b0);  // else it holds them since it was made
       const uint64_t past = __ballot(before + up > at);
       if (past != 0) {
         const int l = uniform(__builtin_ctzll(past));
         it.b = b0 + l;
-        it.start = before + (l > 0 ? lane64(up, l - 1) : 0);
-        it.seq.rows = __builtin_amdgcn_readlane(own.rows, l);
-        it.seq.seq.row0 = lane64(own.seq.row0, l);
-        it.seq.seq.n = __builtin_amdgcn_readlane(own.seq.n, l);
-        it.seq.seq.keys = __builtin_amdgcn_readlane(own.seq.keys, l);
-        it.seq.seq.first_pos = __builtin_amdgcn_readlane(own.seq.first_pos, l);
+        it.start = before + (l > 0 ? of_lane(up, l - 1) : 0);
+        it.seq = uniform_seq(own, l);
         break;
       }
-      before += lane64(up, 63);
+      before += of_lane(up, 63);
     }
     const int64_t heads = a.cache.heads_kv;
-    for (it.rt = 0;; ++it.rt) {
-      it.tiles = K::tiles(a, plan, it.seq, it.rt);
-      if (at - it.start < heads * it.tiles) break;
-      it.start += heads * it.tiles;
+    if constexpr (CHUNK) {
+      for (int rt0 = 0; rt0 * K::kRows < it.seq.rows; rt0 += 64) {
+        const int rt = rt0 + (threadIdx.x & 63);
+        const int64_t n = rt * K::kRows < it.seq.rows ? heads * K::tiles(a, plan, it.seq, rt) : 0, ends = wave_prefix(n);
+        const uint64_t past = __ballot(it.start + ends > at);
+        if (past != 0) {
+          const int l = uniform(__builtin_ctzll(past));
+          it.rt = rt0 + l;
+          it.start += of_lane(ends, l) - of_lane(n, l);
+          break;
+        }
+        it.start += of_lane(ends, 63);
+      }
     }
+    set(a, plan, it);
     it.head = (int)((unsigned)(at - it.start) / (unsigned)it.tiles);  // heads * tiles of one row tile: 32 bits
     it.start += (int64_t)it.head * it.tiles;
+    return uniform_item(it);
+  }
+  // what follows from an item's sequence and row tile
+  static __device__ __forceinline__ void set(const tb_paged_attention_args& a, const AttnPlan& plan, LineItem& it) {
     it.span = K::span(a, plan, it.seq, it.rt);
     it.held = tile_span(it.span, K::kPositions);
+    it.tiles = it.held.count > 1 ? it.held.count : 1;
+  }
+  // The item behind `it`, which is not the line's last.
+  static __device__ __forceinline__ LineItem next(const tb_paged_attention_args& a, const AttnPlan& plan, LineItem it) {
+    it.start += it.tiles;
+    if (++it.head < a.cache.heads_kv) return it;
+    it.head = 0;
+    if (CHUNK && ++it.rt * K::kRows < it.seq.rows) {
+      set(a, plan, it);
+      return uniform_item(it);
+    }
+    it.rt = 0;
+    for (++it.b; it.b < a.cache.B; it.b += 64) {
+      LineSeq own{};
+      if (it.b + (threadIdx.x & 63) < a.cache.B) own = K::sequence(a, plan, it.b + (threadIdx.x & 63));
+      const uint64_t some = __ballot(own.rows > 0);
+      if (some != 0) {
+        const int l = uniform(__builtin_ctzll(some));
+        it.b += l;
+        it.seq = uniform_seq(own, l);
+        break;
+      }
+    }
+    set(a, plan, it);
     return uniform_item(it);
   }
   // Where the items of sequence b start.
@@ -167,8 +205,8 @@ struct Line {
     int64_t n = 0;
     for (int64_t b0 = 0; b0 <= b; b0 += 64) {
       if (a.cache.B > 64) look(a, plan, b0);
-      if (b - b0 < 64) return n + (b > b0 ? lane64(up, (int)(b - b0) - 1) : 0);
-      n += lane64(up, 63);
+      if (b - b0 < 64) return n + (b > b0 ? of_lane(up, (int)(b - b0) - 1) : 0);
+      n += of_lane(up, 63);
     }
     return n;
   }
@@ -213,9 +251,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     // the last rows of a sequence see the most positions: they go first
     it.rt = (it.seq.rows + K::kRows - 1) / K::kRows - 1 - (int)(block / heads % row_tiles);
     if (it.rt < 0 || it.seq.rows == 0) return;
-    it.span = K::span(a, plan, it.seq, it.rt);
-    it.held = tile_span(it.span, K::kPositions);
-    it.tiles = it.held.count > 1 ? it.held.count : 1;
+    Line<CHUNK, FP8>::set(a, plan, it);
     it = uniform_item(it);
     part(it, 0, it.tiles, (int64_t)-1);
     return;
@@ -237,8 +273,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     at = it.start + t1;
     if (at >= end) return;
     __syncthreads();  // the next part writes the LDS that this one reads
-    // looked up again: what a lane knew of the sequences was not kept in registers meanwhile
-    it = Line<CHUNK, FP8>().find(a, plan, at, true);
+    it = Line<CHUNK, FP8>::next(a, plan, it);
   }
 }
 

@@ -13,6 +13,7 @@
 // does not depend on how the sum is split.
 #include "tb_common.h"
 #include "tb_launch.h"
+#include "wave_scan.h"
 
 namespace tb {
 
@@ -76,35 +77,6 @@ __device__ __forceinline__ Row find_row(const tb_verify_draft_args& a, int64_t b
   const uint64_t lost = ~__ballot(keep);
   return row_of(a, b, lo, T, lost == 0 ? 64 : __builtin_ctzll(lost));
 }
-
-// v of the lanes that the DPP control names, 0 where it names none
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double moved(double v) {
-  const uint64_t w = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, ROWS, 0xf, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, ROWS, 0xf, false);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-// inclusive prefix over the lanes of a wave: within rows of 16, then over them
-__device__ __forceinline__ double wave_prefix(double v) {
-  v += moved<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
-  v += moved<0x112, 0xf>(v);
-  v += moved<0x114, 0xf>(v);
-  v += moved<0x118, 0xf>(v);
-  v += moved<0x142, 0xa>(v);  // lane 15 of rows 0 and 2 to the next row
-  v += moved<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
-  return v;
-}
-
-__device__ __forceinline__ double of_lane(double v, int lane) {
-  const uint64_t w = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)w, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(w >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-__device__ __forceinline__ double wave_sum(double v) { return of_lane(wave_prefix(v), 63); }
 
 // four consecutive entries; a row starts at any element, so these loads are
 // aligned to elements only

@@ -126,6 +126,8 @@ SHAPES = [
     ([(1, 900), (4, 300), (1, 5)], 8, 2, 64, 16, 100),
     ([(150, 400), (40, 40)], 4, 1, 128, 64, 37),
     ([(200, 200), (17, 250)], 2, 2, 64, 16, 5000),
+    ([(130, 1333), (1, 700), (257, 957), (0, 30), (300, 1300)], 6, 2, 128, 32, 0),   # many row tiles in one line
+    ([(150, 1400), (40, 1040)], 4, 1, 64, 64, 1037),
 ]
 
 
