@@ -36,6 +36,19 @@ __device__ __forceinline__ f32x16 mfma32(const f16x8& a, const f16x8& b, const f
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// 16 bytes of each active lane, from page + step + lane_at, to its place in the
+// 1024 bytes at `to` in LDS; `page` and `step` are the same in every lane.  As
+// a buffer load: behind global_load_lds the compiler cannot tell what a wait
+// for LDS has to wait for, and waits for all of it every time (four times in
+// 16 products, each time until the newest operand has come).
+__device__ __forceinline__ void load_lds16(const void* page, int bytes, int lane_at, int step, u32x4* to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kWord3 = 0x00020000;  // the 32-bit data format that raw loads need
+  const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(page), (short)0, bytes, kWord3);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, lane_at, step, 0, 0);
+#endif
+}
+
 // Until at most N of the wave's loads are still on their way.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -188,8 +201,13 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
   const int pos_first = uniform(s.first_pos + (int)((unsigned)w_first / (unsigned)group));
   const int pos_last = uniform(s.first_pos + (int)((unsigned)w_last / (unsigned)group));
-  // and of the workgroup
-  const int all_first = s.first_pos + j_first, all_last = s.first_pos + j_last;
+  // Tiles whose first position is in (w_low, w_high] are seen whole by all of
+  // the wave's rows, those in (all_low, all_high] by all of the workgroup's.
+  auto behind_window = [&](int last) {
+    return a.window > 0 && (int64_t)last - a.window > -1 ? (int)((int64_t)last - a.window) : -1;
+  };
+  const int w_low = behind_window(pos_last), w_high = pos_first - (kTile - 1);
+  const int all_low = behind_window(s.first_pos + j_last), all_high = s.first_pos + j_first - (kTile - 1);
 
   // scores are scaled by |scale|; its sign goes into the queries.  A scale of
   // 0 is taken as the smallest number, so that an unseen -inf stays one.
@@ -236,37 +254,64 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int v_run = FP8 ? v_ch : v_ch >> 1;
   const uint32_t k_off = ((k_row & 15) * D + k_ch * kPer) * sizeof(Elem);  // bytes, inside a run
   const int v_off = v_row * c.page + (v_ch * kPer & 15);
-  auto lookup = [&](int t) -> int {
+  // An entry as it is loaded: paged_id of it, and so the wait for it, is left
+  // for when it is needed (with the check here, a wave stood 1100 of a tile's
+  // 5700 cycles waiting for the entry and all loads before it).
+  auto lookup = [&](int t) -> int32_t {
     const int x = (first_tile + t) * kTile + 16 * v_run;
-    if (t >= t_end || (x | (c.page - 1)) < span.begin || x >= span.end) return -1;
-    return paged_page(table, c.table_width, c.n_pages, x >> shift);
+    int32_t entry = -1;
+    if (t < t_end && (x | (c.page - 1)) >= span.begin && x < span.end) entry = paged_entry(table, c.table_width, x >> shift);
+    return entry;
   };
   auto holder = [&](int g) { return FP8 ? g : 2 * g ^ 4 * (wave & 1); };  // bf16: row v_row of lanes 0..7 is 8 wave
   auto run_page = [&](int pages, int g) { return __builtin_amdgcn_readlane(pages, holder(g)); };
   u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
+  const int page_bytes = c.page * D * (int)sizeof(Elem);
+  const int page_runs = c.page / 16;  // runs in a page
+  const bool one_page = c.page >= kTile;  // of a tile
+  auto page_of = [&](const Elem* cache, int page) { return cache + (page < 0 ? 0 : page) * page_step; };
   auto stage_k = [&](int t, int pages, u32x4* to) {
     const int x0 = (first_tile + t) * kTile;
+    if (!FP8 && one_page) {
+      const Elem* page = page_of(kc, run_page(pages, 0));
+      const int at = (x0 & (c.page - 1)) * D * (int)sizeof(Elem) + (int)k_off + (uniform(k_row) & ~15) * D * (int)sizeof(Elem);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        load_lds16(page, page_bytes, at, i * kStep * D * (int)sizeof(Elem), &to[i * 64 * kWaves + wave * 64]);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int run = (i * kStep + uniform(k_row)) >> 4, page = run_page(pages, run);
-      const Elem* kp = kc + (page < 0 ? 0 : page) * page_step + ((x0 + 16 * run) & (c.page - 1)) * D;
-      // a uniform address and a 32-bit offset of the lane
-      const char* from = reinterpret_cast<const char*>(kp) + k_off;
-      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(from);
-      else
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
-                                         (__attribute__((address_space(3))) uint32_t*)&to[i * 64 * kWaves + wave * 64], 16, 0, 0);
+      const int run = (i * kStep + uniform(k_row)) >> 4;
+      const Elem* page = page_of(kc, run_page(pages, run));
+      const int at = ((x0 + 16 * run) & (c.page - 1)) * D * (int)sizeof(Elem);
+      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(page) + at + k_off);
+      else load_lds16(page, page_bytes, (int)k_off, at, &to[i * 64 * kWaves + wave * 64]);
     }
   };
   auto stage_v = [&](int t, int pages, u32x4* to) {
     const int x0 = (first_tile + t) * kTile;
-    const Elem* vp = vc + (pages < 0 ? 0 : pages) * page_step + ((x0 + 16 * v_run) & (c.page - 1)) + v_off;
+    const int at = (x0 + 16 * v_run) & (c.page - 1);
+    if constexpr (FP8) {
+      const Elem* vp = page_of(vc, pages) + at + v_off;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if constexpr (FP8) vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
-      else
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(vp + i * vStep * c.page),
-                                         (__attribute__((address_space(3))) uint32_t*)&to[i * 64 * kWaves + wave * 64], 16, 0, 0);
+      for (int i = 0; i < kLoads; ++i) vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
+      return;
+    }
+    // A load is of one page: with several in a tile, of the lanes whose run lies in it.
+    const int lane_at = (v_off + at) * (int)sizeof(Elem), step = vStep * c.page * (int)sizeof(Elem);
+    if (one_page) {
+      const Elem* page = page_of(vc, run_page(pages, 0));
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_lds16(page, page_bytes, lane_at, i * step, &to[i * 64 * kWaves + wave * 64]);
+      return;
+    }
+#pragma unroll 1
+    for (int g = 0; g < kTile / 16; g += page_runs) {
+      if (v_run < g || v_run >= g + page_runs) continue;
+      const Elem* page = page_of(vc, run_page(pages, g));
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_lds16(page, page_bytes, lane_at, i * step, &to[i * 64 * kWaves + wave * 64]);
     }
   };
   // 8-bit: the staged registers into LDS
@@ -303,6 +348,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   float top = 0.f;  // of the lane's newest scores
 
   auto runs_of = [&](int pages) -> uint32_t {  // which of a tile's runs exist
+    if (one_page) return run_page(pages, 0) < 0 ? 0u : 0xfu;
     uint32_t there = 0xfu;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
@@ -316,7 +362,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   // at most 2^8).
   auto settle = [&](f32x16& x, int t, int u, uint32_t there) {
     const int x0 = (first_tile + t) * kTile;
-    if (!(there == 0xfu && x0 + kTile - 1 <= pos_first && (a.window <= 0 || x0 > (int64_t)pos_last - a.window))) {
+    if (!(there == 0xfu && x0 <= w_high && x0 > w_low)) {
       const int64_t rel = (int64_t)x0 + 32 * u + 8 * half;
       const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 31 ? 31 : pos - rel) : -1;
       const int lo = (int)(low - rel < -1 ? -1 : low - rel > 31 ? 31 : low - rel);
@@ -397,7 +443,8 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 #pragma unroll
   for (int i = 0; i < kRows * D / 16 / (64 * kWaves); ++i) sm.marks[i * 64 * kWaves + tid] = 0u;  // a barrier follows
   const bool idle = r0 + wave * 32 >= nrows;  // the wave has no row: it only loads
-  int p0 = lookup(t_begin), p1 = lookup(t_begin + 1), p2 = lookup(t_begin + 2);
+  const int32_t e0 = lookup(t_begin), e1 = lookup(t_begin + 1), e2 = lookup(t_begin + 2);
+  int p0 = paged_id(e0, c.n_pages), p1 = paged_id(e1, c.n_pages), p2 = paged_id(e2, c.n_pages);
   if (t_begin < t_end) {
     stage_k(t_begin, p0, sm.buffer[0]);
     stage_v(t_begin, p0, sm.buffer[2]);
@@ -431,11 +478,11 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     if (!FP8 && t + 1 < t_end) wait_loads<kLoads>();
     else wait_loads<0>();
     __syncthreads();
+    const int32_t e3 = lookup(t + 3);
     if (t + 1 < t_end) stage_v(t + 1, p1, v_next);
-    const int p3 = lookup(t + 3);
     const int x0 = (first_tile + t) * kTile;
     const uint32_t there = runs_of(p0);
-    if (!(there == 0xfu && x0 + kTile - 1 <= all_first && (a.window <= 0 || x0 > (int64_t)all_last - a.window)))
+    if (!(there == 0xfu && x0 <= all_high && x0 > all_low))
       take_nonfinite_tile<D, FP8, kRows>(v_lds, sm.marks, marked, x0, there, span.begin, span.end, s.first_pos, group, r0,
                                          nrows, a.window);
     if (!idle) {
@@ -444,6 +491,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     }
     wait_loads<FP8 ? 0 : kLoads>();  // K of t + 1 has come; V of t + 1, issued after it, may be on its way
     __syncthreads();
+    const int p3 = paged_id(e3, c.n_pages);
     if (t + 2 < t_end) stage_k(t + 2, p2, k_lds);
     if (!idle) {
       beside(sc[1], sc[0], k_next, 0, v_lds, 1);  // past the last tile: scores of what lies in k_next, not used

@@ -37,11 +37,16 @@ TB_HOST_DEVICE PagedSeq paged_seq(const int32_t* cu_q, const int32_t* kv_len, in
   return s;
 }
 
-// The page of entry `i` of a sequence's table row, or -1 if there is none.
+// The page of entry `i` of a sequence's table row, or -1 if there is none; in
+// two steps where the entry is used long after it was asked for.
+TB_HOST_DEVICE int32_t paged_entry(const int32_t* row, int64_t width, int64_t i) {
+  int32_t id = -1;
+  if (i >= 0 && i < width) id = row[i];
+  return id;
+}
+TB_HOST_DEVICE int paged_id(int32_t entry, int64_t n_pages) { return entry >= 0 && entry < n_pages ? entry : -1; }
 TB_HOST_DEVICE int paged_page(const int32_t* row, int64_t width, int64_t n_pages, int64_t i) {
-  if (i < 0 || i >= width) return -1;
-  const int32_t id = row[i];
-  return id >= 0 && id < n_pages ? id : -1;
+  return paged_id(paged_entry(row, width, i), n_pages);
 }
 
 // The positions that some of the tokens j0 .. j1 (inclusive, j1 < n) see: [begin, end).
