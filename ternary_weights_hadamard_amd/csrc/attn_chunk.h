@@ -22,6 +22,8 @@
 // ahead; two workgroups of four waves share a CU.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_rows.h"
 
 namespace tb {
@@ -167,6 +169,19 @@ __device__ __forceinline__ f32x4 marked_sum(const uint32_t* marks, int row, int 
   return r;
 }
 
+// Row r of an item: its token in the sequence, and its query head.
+struct LaneRow {
+  bool live;
+  int tok, hq;
+};
+__device__ __forceinline__ LaneRow lane_row(int r, int nrows, int group, int head) {
+  LaneRow x;
+  x.live = r < nrows;
+  x.tok = x.live ? (int)((unsigned)r / (unsigned)group) : 0;
+  x.hq = head * group + (x.live ? r - x.tok * group : 0);
+  return x;
+}
+
 // Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
 // it), or a part of it into the workspace's slot.
 template <int D, bool FP8>
@@ -190,22 +205,20 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int i32 = lane & 31, half = lane >> 5;
 
-  // the lane's row, and its wave's first and last
-  const int r = r0 + wave * 32 + i32;
-  const bool row_live = r < nrows;
-  const int tok = row_live ? (int)((unsigned)r / (unsigned)group) : 0;
-  const int hq = head * group + (row_live ? r - tok * group : 0);
-  const int pos = s.first_pos + tok;
-  const int64_t low = a.window > 0 ? (int64_t)pos - a.window : -1;
+  // the positions (low, pos] that the lane's row sees, and its wave's first and last row
+  const LaneRow row = lane_row(r0 + wave * 32 + i32, nrows, group, head);
+  const bool row_live = row.live;
+  const int pos = s.first_pos + row.tok;
+  auto behind_window = [&](int last) {
+    return a.window > 0 && (int64_t)last - a.window > -1 ? (int)((int64_t)last - a.window) : -1;
+  };
+  const int low = behind_window(pos);
   const int w_first = r0 + wave * 32 < nrows ? r0 + wave * 32 : nrows - 1;
   const int w_last = w_first + 31 < nrows ? w_first + 31 : nrows - 1;
   const int pos_first = uniform(s.first_pos + (int)((unsigned)w_first / (unsigned)group));
   const int pos_last = uniform(s.first_pos + (int)((unsigned)w_last / (unsigned)group));
   // Tiles whose first position is in (w_low, w_high] are seen whole by all of
   // the wave's rows, those in (all_low, all_high] by all of the workgroup's.
-  auto behind_window = [&](int last) {
-    return a.window > 0 && (int64_t)last - a.window > -1 ? (int)((int64_t)last - a.window) : -1;
-  };
   const int w_low = behind_window(pos_last), w_high = pos_first - (kTile - 1);
   const int all_low = behind_window(s.first_pos + j_last), all_high = s.first_pos + j_first - (kTile - 1);
 
@@ -217,7 +230,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   bf16x8 q[KK];
   {
     const uint16_t* qp =
-        static_cast<const uint16_t*>(a.q) + (s.row0 + tok) * a.q_stride + (int64_t)hq * D + 8 * half;
+        static_cast<const uint16_t*>(a.q) + (s.row0 + row.tok) * a.q_stride + (int64_t)row.hq * D + 8 * half;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       u32x4 w = {0u, 0u, 0u, 0u};
@@ -267,19 +280,11 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   auto run_page = [&](int pages, int g) { return __builtin_amdgcn_readlane(pages, holder(g)); };
   u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
   const int page_bytes = c.page * D * (int)sizeof(Elem);
-  const int page_runs = c.page / 16;  // runs in a page
-  const bool one_page = c.page >= kTile;  // of a tile
+  const int page_runs = c.page < kTile ? c.page / 16 : kTile / 16;  // runs of a tile that share a page
+  const bool one_page = c.page >= kTile;                            // all of a tile's do
   auto page_of = [&](const Elem* cache, int page) { return cache + (page < 0 ? 0 : page) * page_step; };
   auto stage_k = [&](int t, int pages, u32x4* to) {
     const int x0 = (first_tile + t) * kTile;
-    if (!FP8 && one_page) {
-      const Elem* page = page_of(kc, run_page(pages, 0));
-      const int at = (x0 & (c.page - 1)) * D * (int)sizeof(Elem) + (int)k_off + (uniform(k_row) & ~15) * D * (int)sizeof(Elem);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_lds16(page, page_bytes, at, i * kStep * D * (int)sizeof(Elem), &to[i * 64 * kWaves + wave * 64]);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int run = (i * kStep + uniform(k_row)) >> 4;
@@ -300,12 +305,6 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     }
     // A load is of one page: with several in a tile, of the lanes whose run lies in it.
     const int lane_at = (v_off + at) * (int)sizeof(Elem), step = vStep * c.page * (int)sizeof(Elem);
-    if (one_page) {
-      const Elem* page = page_of(vc, run_page(pages, 0));
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load_lds16(page, page_bytes, lane_at, i * step, &to[i * 64 * kWaves + wave * 64]);
-      return;
-    }
 #pragma unroll 1
     for (int g = 0; g < kTile / 16; g += page_runs) {
       if (v_run < g || v_run >= g + page_runs) continue;
@@ -313,6 +312,26 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) load_lds16(page, page_bytes, lane_at, i * step, &to[i * 64 * kWaves + wave * 64]);
     }
+  };
+  // The same for a tile within one page, one load at a time: `page` and `at` are
+  // found once a tile.
+  struct Loads {
+    const Elem* page;
+    int at;  // of the lane
+  };
+  auto loads_k = [&](int t, int pages) {
+    const int slot = (((first_tile + t) * kTile) & (c.page - 1)) + (uniform(k_row) & ~15);
+    return Loads{page_of(kc, run_page(pages, 0)), (int)k_off + slot * D * (int)sizeof(Elem)};
+  };
+  auto loads_v = [&](int t, int pages) {
+    const int slot = ((first_tile + t) * kTile + 16 * v_run) & (c.page - 1);
+    return Loads{page_of(vc, run_page(pages, 0)), (v_off + slot) * (int)sizeof(Elem)};
+  };
+  auto load_k = [&](const Loads& x, int i, u32x4* to) {
+    load_lds16(x.page, page_bytes, x.at, i * kStep * D * (int)sizeof(Elem), &to[i * 64 * kWaves + wave * 64]);
+  };
+  auto load_v = [&](const Loads& x, int i, u32x4* to) {
+    load_lds16(x.page, page_bytes, x.at, i * vStep * c.page * (int)sizeof(Elem), &to[i * 64 * kWaves + wave * 64]);
   };
   // 8-bit: the staged registers into LDS
   auto widen_k = [&](u32x4* to) {
@@ -363,9 +382,9 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   auto settle = [&](f32x16& x, int t, int u, uint32_t there) {
     const int x0 = (first_tile + t) * kTile;
     if (!(there == 0xfu && x0 <= w_high && x0 > w_low)) {
-      const int64_t rel = (int64_t)x0 + 32 * u + 8 * half;
-      const int hi = row_live ? (int)(pos - rel < -1 ? -1 : pos - rel > 31 ? 31 : pos - rel) : -1;
-      const int lo = (int)(low - rel < -1 ? -1 : low - rel > 31 ? 31 : low - rel);
+      const int rel = x0 + 32 * u + 8 * half;  // positions have 30 bits
+      const int hi = row_live ? (pos - rel < -1 ? -1 : pos - rel > 31 ? 31 : pos - rel) : -1;
+      const int lo = low - rel < -1 ? -1 : low - rel > 31 ? 31 : low - rel;
       top = -__builtin_inff();
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -393,7 +412,9 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 
   // Scores `now` become weights and their values' sums (part uv of v_lds),
   // beside the products of the scores `next` (part uk of the keys in k_lds).
-  auto beside = [&](f32x16& now, f32x16& next, const u32x4* k_lds, int uk, const u32x4* v_lds, int uv) {
+  // issue(i) is load i of a later tile: one every four products, as all at once
+  // they stand in line.
+  auto beside = [&](f32x16& now, f32x16& next, const u32x4* k_lds, int uk, const u32x4* v_lds, int uv, auto issue) {
     static_assert(2 * DT == KK, "as many products of values as of keys");
     constexpr int kProducts = 2 * KK, kAhead = 4;
     constexpr int kScores = 16 / KK;  // scores turned beside a product of keys
@@ -413,6 +434,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
 #pragma unroll
     for (int i = 0; i < kProducts; ++i) {
       if (i + kAhead < kProducts) load(i + kAhead);
+      if (i % 4 == 1) issue(i / 4);
       if (i < KK) {
         next = mfma32(__builtin_bit_cast(bf16x8, operand[i]), q[i], next);
 #pragma unroll
@@ -473,29 +495,46 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   // are arrays of their own, and which is which is known when this is compiled:
   // the compiler then knows that reading the one does not wait for the loads
   // into the other.
-  auto step = [&](int t, u32x4* k_lds, u32x4* k_next, u32x4* v_lds, u32x4* v_next) {
+  auto step = [&](auto one, int t, u32x4* k_lds, u32x4* k_next, u32x4* v_lds, u32x4* v_next) {
+    constexpr bool kOne = decltype(one)::value;  // bf16, in tiles within a page: loads go out beside the products
+    static_assert(FP8 || 4 * kLoads == 2 * KK, "a load for four products");
     // V of t has come: what was issued after it (K of t + 1) may still be on its way
     if (!FP8 && t + 1 < t_end) wait_loads<kLoads>();
     else wait_loads<0>();
     __syncthreads();
     const int32_t e3 = lookup(t + 3);
-    if (t + 1 < t_end) stage_v(t + 1, p1, v_next);
+    Loads ahead{};
+    if constexpr (kOne) ahead = loads_v(t + 1, p1);
+    else if (t + 1 < t_end) stage_v(t + 1, p1, v_next);
+    auto ahead_v = [&](int i) {
+      if constexpr (kOne) load_v(ahead, i, v_next);
+    };
     const int x0 = (first_tile + t) * kTile;
     const uint32_t there = runs_of(p0);
     if (!(there == 0xfu && x0 <= all_high && x0 > all_low))
       take_nonfinite_tile<D, FP8, kRows>(v_lds, sm.marks, marked, x0, there, span.begin, span.end, s.first_pos, group, r0,
                                          nrows, a.window);
     if (!idle) {
-      beside(sc[0], sc[1], k_lds, 1, v_lds, 0);
+      beside(sc[0], sc[1], k_lds, 1, v_lds, 0, ahead_v);
       settle(sc[1], t, 1, there);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) ahead_v(i);
     }
     wait_loads<FP8 ? 0 : kLoads>();  // K of t + 1 has come; V of t + 1, issued after it, may be on its way
     __syncthreads();
     const int p3 = paged_id(e3, c.n_pages);
-    if (t + 2 < t_end) stage_k(t + 2, p2, k_lds);
+    if constexpr (kOne) ahead = loads_k(t + 2, p2);
+    else if (t + 2 < t_end) stage_k(t + 2, p2, k_lds);
+    auto ahead_k = [&](int i) {
+      if constexpr (kOne) load_k(ahead, i, k_lds);
+    };
     if (!idle) {
-      beside(sc[1], sc[0], k_next, 0, v_lds, 1);  // past the last tile: scores of what lies in k_next, not used
+      beside(sc[1], sc[0], k_next, 0, v_lds, 1, ahead_k);  // past the last tile: scores of what lies in k_next, not used
       if (t + 1 < t_end) settle(sc[0], t + 1, 0, runs_of(p1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) ahead_k(i);
     }
     widen_v(v_next);
     if (t + 2 < t_end) widen_k(k_lds);
@@ -503,9 +542,17 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     p1 = p2;
     p2 = p3;
   };
-  for (int t = t_begin; t < t_end; t += 2) {
-    step(t, sm.buffer[0], sm.buffer[1], sm.buffer[2], sm.buffer[3]);
-    if (t + 1 < t_end) step(t + 1, sm.buffer[1], sm.buffer[0], sm.buffer[3], sm.buffer[2]);
+  auto all = [&](auto one) {
+    for (int t = t_begin; t < t_end; t += 2) {
+      step(one, t, sm.buffer[0], sm.buffer[1], sm.buffer[2], sm.buffer[3]);
+      if (t + 1 < t_end) step(one, t + 1, sm.buffer[1], sm.buffer[0], sm.buffer[3], sm.buffer[2]);
+    }
+  };
+  if (!FP8 && one_page) {
+    all(std::true_type());
+    wait_loads<0>();  // past the last tile its loads were of the pool's first page, for nobody
+  } else {
+    all(std::false_type());
   }
 
   // the row's sum, and its output: register 4 j + e of tile dt is channel 32 dt + 8 j + 4 half + e
@@ -514,35 +561,40 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     swap_halves(l, a0, a1);
     l = a0 + a1;
   }
-  if (!row_live) return;
+  // found again: kept through the loop, it would cost registers that the loop has not
+  int thread = threadIdx.x;
+  hold(thread);
+  const int r = r0 + (thread >> 6) * 32 + (thread & 31), c0 = 4 * (thread >> 5 & 1);
+  const LaneRow out = lane_row(r, nrows, group, head);
+  if (!out.live) return;
   if (marked) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x4 x = marked_sum<D>(sm.marks, r - r0, dt, 8 * j + 4 * half);
+        const f32x4 x = marked_sum<D>(sm.marks, r - r0, dt, 8 * j + c0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[dt][4 * j + e] += x[e];
       }
   }
-  const int64_t at = (s.row0 + tok) * a.heads_q + hq;
+  const int64_t at = (s.row0 + out.tok) * a.heads_q + out.hq;
   if (slot >= 0) {
     const int64_t pr = slot * kRows + (r - r0);
-    if (half == 0) plan.chunk_line.stats[pr] = float2{m, l};
+    if (c0 == 0) plan.chunk_line.stats[pr] = float2{m, l};
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(plan.chunk_line.values + pr * D + 32 * dt + 8 * j + 4 * half) =
+        *reinterpret_cast<f32x4*>(plan.chunk_line.values + pr * D + 32 * dt + 8 * j + c0) =
             f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
     return;
   }
-  const RowScale rs = row_scale(a, head, at, half == 0, m, l);
+  const RowScale rs = row_scale(a, head, at, c0 == 0, m, l);
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      write4(a, at * D + 32 * dt + 8 * j + 4 * half,
+      write4(a, at * D + 32 * dt + 8 * j + c0,
              f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]}, rs);
 }
 
