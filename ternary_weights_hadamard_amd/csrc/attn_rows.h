@@ -82,19 +82,23 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   const int krow = 8 * NB * (i16 >> 2) + (i16 & 3);
   const int v0 = 8 * NB * q4;
 
-  // The page of position x, or -1 (none, or nobody sees it; its table entry is not read then).
-  auto page_of = [&](int x) -> int {
-    if ((x | (page - 1)) < span.begin || x >= span.end) return -1;
-    return paged_page(table, c.table_width, c.n_pages, x >> shift);
+  // The table's entry for position x, -1 if nobody sees its page (it is not read
+  // then).  paged_id of it, and so the wait for it, is left for when its tile is
+  // loaded.
+  auto entry_of = [&](int x) -> int32_t {
+    int32_t entry = -1;
+    if ((x | (page - 1)) >= span.begin && x < span.end) entry = paged_entry(table, c.table_width, x >> shift);
+    return entry;
   };
   struct Pages {
-    int k, v;  // of the lane's keys and values
+    int32_t k, v;  // of the lane's keys and values
   };
   auto lookup = [&](int t) -> Pages {
     if (t >= t_end) return Pages{-1, -1};
     const int x0 = (first_tile + t) * T;
-    return Pages{page_of(x0 + krow), page_of(x0 + v0)};
+    return Pages{entry_of(x0 + krow), entry_of(x0 + v0)};
   };
+  auto checked = [&](const Pages& p) { return Pages{paged_id(p.k, c.n_pages), paged_id(p.v, c.n_pages)}; };
   struct Tile {
     u32x4 k[S][KL], v[DT];
     int page;  // of the values
@@ -121,7 +125,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
 
   int t = t0 + wave;
   Tile ta;
-  const Pages pa = lookup(t);
+  const Pages first = lookup(t);
   Pages ahead = lookup(t + kAttnWaves);
 
   // the lane's row
@@ -145,6 +149,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   }
   const float scale2 = a.scale * kLog2e * (FP8 && c.k_scale ? c.k_scale[head] : 1.f);
 
+  const Pages pa = checked(first);
   load_keys(ta, t, pa);
   load_values(ta, t, pa);
 
@@ -156,9 +161,9 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   // Tile t, held in `x`, which is loaded again for the tile after the next.
   auto step = [&](Tile& x, int t) {
     const int x0 = (first_tile + t) * T, pv = x.page;
-    // looked up before that tile's loads: loads return in order, and the next
-    // step waits for this one's answer only
-    const Pages now = ahead;
+    // asked for before that tile's loads: loads return in order, and the next
+    // step waits for this answer only
+    const Pages now = checked(ahead);
     ahead = lookup(t + 2 * kAttnWaves);
     f32x4 sc[S];
 #pragma unroll
