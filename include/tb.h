@@ -545,7 +545,7 @@ TB_API tb_status tb_ternary_gemm_rotated(const uint16_t* x, int64_t M, const uin
  *           rows_per_gate >= 1 (1: a gate for each row; rows: one for all)
  *   z       [rows][C] in z_dtype, or NULL: TB_F32, TB_BF16 or TB_ACT8 (the
  *           rounded bf16 result as the operand of tb_ternary_gemv)
- *   C a positive multiple of 128, at most TB_NORM_MAX_C; rows >= 0; alpha
+ *   C a positive multiple of 128, at most TB_NORM_MAX_C; 0 <= rows <= 2^35; alpha
  *   finite, eps finite and > 0 (else TB_ERR_VALUE).
  * Every output overlaps no other argument, h == resid excepted.
  */

@@ -46,7 +46,9 @@ __device__ __forceinline__ LineParts parts_of_row(const tb_paged_attention_args&
 // Row r in `parts`, joined by L = 16 lanes (a wave does four) or by all 64
 // (rows in many parts: what counts is the time of one).  Lane p of them holds the
 // statistics of part p, of L at a time, and their groups of 16 take the parts
-// in turn, D / 16 channels a lane.
+// in turn, D / 16 channels a lane.  Bound by latency: the line again, a row's
+// statistics and its first parts (16 rows of 40 heads 6.2 us; 8 x 45 rows of 8
+// key/value heads in 8 parts each 8.2 us by whole waves, 14.5 us by 16 lanes).
 template <int D, bool CHUNK, bool FP8, int L>
 __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const AttnPlan& plan, const LineParts& parts,
                                          const LineSeq& seq, int head, int r) {
@@ -170,8 +172,8 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype == TB_FP8)) p.rows_line.pieces = kPieces;
   // Chunks whose items fill the GPU are not cut: one after another, the row
   // tiles of a head find its keys and values in L2, while pieces of a line are
-  // all elsewhere (4 x 2048 tokens over 8192, 40 heads: 625 us as items, 883 us
-  // as pieces).  Nor are those of fewer items if it saves less than ten tiles,
+  // all elsewhere (4 x 2048 tokens over 8192, 40 heads, an earlier form of the
+  // kernel: 625 us as items, 883 us as pieces).  Nor are those of fewer items if it saves less than ten tiles,
   // which is what a second part's start, the parts' way through memory and the
   // join take, and pieces run two on a CU, where each takes 5/4 of its time (2 x
   // 777 tokens of 16 heads: 18 tiles within a window of 1000 38.6 us as items,
@@ -201,7 +203,8 @@ hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stre
   else if (!rows) hipLaunchKernelGGL((attn_kernel<D, FP8, false, true>), grid, block, 0, stream, a, p);
   else hipLaunchKernelGGL((attn_kernel<D, FP8, true, true>), grid, block, 0, stream, a, p);
   const hipError_t e = hipGetLastError();
-  const int64_t joined = p.chunk_line.pieces ? most_rows(a) : !p.rows_line.pieces ? 0 : most_rows(a) < p.few ? most_rows(a) : p.few;
+  const int64_t few_rows = !p.rows_line.pieces ? 0 : most_rows(a) < p.few ? most_rows(a) : p.few;
+  const int64_t joined = p.chunk_line.pieces ? most_rows(a) : few_rows;
   if (e != hipSuccess || joined == 0) return e;
   // Rows of many chunk items are in few parts each, and are many.
   const bool many = p.chunk_line.pieces && chunk_items(a, p) > kPieces / 4;

@@ -8,18 +8,21 @@
 // forms of each 16 positions are, as they are, its operand of O' = V' P'.
 // Weights never leave their lane.
 //
-// What bounds it: the matrix unit, if the vector work of turning scores into
-// weights runs beside it: for 32 positions and 32 rows of 128 channels the
-// products take 512 cycles, the weights about 300.  Two waves on a SIMD do not
-// overlap the two by themselves (as two phases a tile, the matrix unit was busy
-// 35 % of the time and the vector unit 41 %, one after the other: a wave waits
-// for its operands from LDS, for its products or for the other wave).  So the
-// instruction stream interleaves them: beside each product of the next 32
-// positions' scores two of these scores become weights, and beside the products
-// of these positions' values the maximum of the next scores is taken.  The
-// decision to rescale is what is left outside.  Tiles of 64 positions of K and
-// V are double buffered in LDS by the global-to-LDS path, each loaded one tile
-// ahead; two workgroups of four waves share a CU.
+// What bounds it: a wave's own stream.  For 32 positions and 32 rows of 128
+// channels the products take 512 cycles of the matrix unit and the weights
+// about 450 of the vector unit, and two waves on a SIMD do not overlap the two
+// by themselves (as two phases a tile, the matrix unit was busy 35 % of the time
+// and the vector unit 41 %, one after the other).  So the instruction stream
+// interleaves them: beside each product of the next 32 positions' scores two of
+// these scores become weights, and beside the products of these positions'
+// values the maximum of the next scores is taken; the loads of later tiles go
+// out between them.  Of a tile's 4600 cycles a wave spends 2000 there, 700 in
+// deciding to rescale, and the rest waiting for the other waves and looking
+// pages up.  Tiles of 64 positions of K and V are double buffered in LDS by the
+// memory-to-LDS path, each loaded one tile ahead; two workgroups of four waves
+// share a CU.  4 x up to 2048 tokens over 2048..8192, 40 heads, 8
+// key/value heads: 479 GFLOP in 553 us, 866 TFLOP/s (a large library product: 1255); 2 x
+// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 37.9 us.
 #pragma once
 
 #include <type_traits>

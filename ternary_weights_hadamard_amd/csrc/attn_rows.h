@@ -12,9 +12,13 @@
 // The running maximum and sum of each row are kept in log2 units.
 //
 // What bounds it: the cache's bytes.  Every K and V byte is loaded once,
-// straight into operand registers (no LDS, no barrier in the loop), and two
-// tiles of a wave are in flight: each half of a tile's registers is loaded
-// again, for the tile after the next, as soon as its product is formed.
+// straight into operand registers (no LDS, no barrier in the loop), and each
+// half of a tile's registers is loaded again, for the wave's next tile, as soon
+// as its product is formed.  A token of each of 16 sequences of 2048..8192, 8
+// key/value heads: 357 MB in 69.9 us, 5.1 TB/s; of 4 sequences of 16384..65536
+// in e4m3: 330 MB in 63.6 us, 5.2 TB/s (a plain copy moves 5.1 TB/s).  One
+// sequence of 1000 with 40 key/value heads: 10.3 us, of which 2 are to find the
+// piece, 3 to the first tile, and 5 the launch and the joins of the waves.
 //
 // The four waves of a workgroup take the position tiles of a part in turn and
 // join through LDS.

@@ -299,7 +299,8 @@ hipError_t launch(const tb_block_norm_args& a, hipStream_t stream) {
   const int64_t lanes = (a.C / 8 + NP - 1) / NP;
   // a workgroup per row; the row of workgroup (x, y) is y * gridDim.x + x
   const int64_t cap = 1 << 20;
-  const dim3 grid((unsigned)(a.rows < cap ? a.rows : cap), (unsigned)((a.rows + cap - 1) / cap)), block((unsigned)((lanes + 63) / 64 * 64));
+  const dim3 grid((unsigned)(a.rows < cap ? a.rows : cap), (unsigned)((a.rows + cap - 1) / cap));
+  const dim3 block((unsigned)((lanes + 63) / 64 * 64));
   const bool yb = a.y_dtype == TB_BF16, hb = a.h_dtype == TB_BF16;
 #define TB_NORM(Y, H)                                                                                   \
   do {                                                                                                  \

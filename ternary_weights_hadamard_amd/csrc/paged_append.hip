@@ -7,7 +7,9 @@
 // conversion to the cache's type puts them side by side, and from LDS each d's
 // run of positions is written in 16-byte pieces where all of a piece is new.
 //
-// Bound by HBM for a chunk, by the chain lengths - page - store for a step.
+// Bound by the chain lengths - entry - load - convert - store, of which a chunk
+// has one round (4 x 128..2048 tokens of 8 heads to e4m3, 24.5 MB: 12.9 us, 1.9
+// TB/s) and a step little else (16 tokens of 8 heads: 5.8 us).
 #include "paged.h"
 #include "tb_common.h"
 #include "tb_launch.h"
@@ -28,8 +30,8 @@ __device__ __forceinline__ uint32_t fp8_pair(float a, float b) {
 
 // x / scale, correctly rounded, for a scale whose reciprocal and products stay
 // far from the ends of fp32: the rounded quotient by the reciprocal, corrected
-// by its remainder once (exact but for quotients that e4m3 rounds to 0).  3 operations in place of the 10 of
-// the general division, which was half of the kernel's time.  Quotients past
+// by its remainder once (exact but for quotients that e4m3 rounds to 0).  3 operations in place of about 10 of
+// the general division.  Quotients past
 // 512 are cut there before the correction, so that none of it overflows; NaN
 // and infinities come through by the remainder.
 struct Quotient {
