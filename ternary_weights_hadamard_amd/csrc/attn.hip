@@ -142,11 +142,13 @@ constexpr int kPieces = 512;  // two workgroups for each of 256 CUs
 // rows of the largest sequence
 int64_t most_rows(const tb_paged_attention_args& a) { return a.cache.max_q * (a.heads_q / a.cache.heads_kv); }
 
-// Whether sequences of either kind may be there: with max_q tokens each, only
-// those of its kind are.
+// Whether sequences may have more rows than `few`, and whether any may go to the
+// kernel for few rows.  Token arrays of exactly B * max_q rows are most likely
+// those of B sequences of max_q tokens; as the lengths are not known here, the
+// chunk kernel, launched alone, then takes the short ones too (few is 0).
 bool has_chunk(const tb_paged_attention_args& a, const AttnPlan& p) { return most_rows(a) > p.few; }
 bool has_rows(const tb_paged_attention_args& a, const AttnPlan& p) {
-  return !has_chunk(a, p) || a.cache.total_q < a.cache.B * a.cache.max_q;
+  return !has_chunk(a, p) || a.cache.total_q != a.cache.B * a.cache.max_q;
 }
 
 // about the items of chunks
@@ -158,6 +160,7 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   const tb_paged_cache& c = a.cache;
   AttnPlan p{};
   p.few = kRowsTile;
+  if (!has_rows(a, p)) p.few = 0;
   p.capacity = c.n_pages > 0 ? c.table_width * c.page : 0;
   p.group = a.heads_q / c.heads_kv;
   p.shift = __builtin_ctz(c.page);

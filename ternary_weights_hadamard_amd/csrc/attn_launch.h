@@ -25,7 +25,7 @@ struct AttnLine {
 };
 
 struct AttnPlan {
-  int64_t few;       // most rows of the first kind
+  int64_t few;       // most rows of the first kind (0: all sequences are of the second)
   int64_t capacity;  // positions that the table has room for
   int group;         // query heads of a key/value head
   int shift;         // log2 of a page's positions
