@@ -22,7 +22,7 @@
 // memory-to-LDS path, each loaded one tile ahead; two workgroups of four waves
 // share a CU.  4 x up to 2048 tokens over 2048..8192, 40 heads, 8
 // key/value heads: 479 GFLOP in 553 us, 866 TFLOP/s (a large library product: 1255); 2 x
-// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 37.9 us.
+// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 38.5 us.
 #pragma once
 
 #include <type_traits>
@@ -61,18 +61,25 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
+// Weights are relative to weight_reference<kRoom> of a maximum that may lag
+// behind the row's by 2^kSlack, so they are at most 2^(kRoom + kSlack).  For
+// fp16 the two share its range: more slack is less room for small weights, less
+// is more rescaling (2 x 777 tokens of the last line above: 37.9 us with a slack
+// of 8, 38.5 with 4, 39.5 with 2).
 template <bool FP8>
 struct ChunkOps;
 template <>
 struct ChunkOps<false> {
   typedef uint16_t Elem;
   typedef bf16x8 V8;
+  static constexpr int kRoom = 0, kSlack = 8;
   static __device__ __forceinline__ __bf16 narrow(float x) { return (__bf16)x; }
 };
 template <>
 struct ChunkOps<true> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
   typedef uint8_t Elem;
   typedef f16x8 V8;
+  static constexpr int kRoom = 11, kSlack = 4;  // full precision down to 2^-25 of the largest weight
   static __device__ __forceinline__ _Float16 narrow(float x) { return (_Float16)x; }
 };
 
@@ -191,8 +198,9 @@ template <int D, bool FP8>
 __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
                                                 const LineItem& it, int t_begin, int t_stop, int64_t slot,
                                                 const AttnShared& sm) {
-  typedef typename ChunkOps<FP8>::Elem Elem;
-  typedef typename ChunkOps<FP8>::V8 V8;
+  typedef ChunkOps<FP8> O;
+  typedef typename O::Elem Elem;
+  typedef typename O::V8 V8;
   constexpr int KK = D / 16;   // steps of a score tile
   constexpr int DT = D / 32;   // 32-channel tiles of O'
   constexpr int kWaves = kAttnWaves, kRows = kChunkTile;
@@ -360,7 +368,8 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   // lane's score registers 0..7 are then positions 8 half + 0..7, 8..15 are 16 more
   const int key = 16 * (i32 >> 4) + 8 * ((i32 >> 2) & 1) + 4 * ((i32 >> 3) & 1) + (i32 & 3);
 
-  float m = -__builtin_inff(), base = 0.f;  // maximum (log2 units) that the weights are relative to; the same, or 0
+  // maximum (log2 units), and what the weights are relative to: its reference, or 0
+  float m = -__builtin_inff(), base = 0.f;
   float l = 0.f;                            // the lane's sum
   f32x16 o[DT], sc[2];                      // scores of the first and of the second 32 positions of a tile
 #pragma unroll
@@ -379,9 +388,8 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   };
 
   // New scores (part u of tile t): what the rows do not see out, the maximum,
-  // and the values' sums rescaled if it has grown by more than 2^8.  Until then
-  // weights stay relative to the older one: nothing is rounded more (they are
-  // at most 2^8).
+  // and the values' sums rescaled if it has grown by more than 2^kSlack.  Until
+  // then weights stay relative to the older one: nothing is rounded more.
   auto settle = [&](f32x16& x, int t, int u, uint32_t there) {
     const int x0 = (first_tile + t) * kTile;
     if (!(there == 0xfu && x0 <= w_high && x0 > w_low)) {
@@ -400,11 +408,12 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     float t0, t1;
     swap_halves(top, t0, t1);
     const float row_top = fmaxf(t0, t1) * scale2;
-    if (__ballot(row_top > m + 8.f) != 0) {
+    if (__ballot(row_top > m + (float)O::kSlack) != 0) {
       const float m_new = fmaxf(m, row_top);
-      const float alpha = m == -__builtin_inff() ? 1.f : exp2_fast(m - m_new);
+      const float base_new = m_new == -__builtin_inff() ? 0.f : weight_reference<O::kRoom>(m_new);
+      const float alpha = m == -__builtin_inff() ? 1.f : exp2_fast(base - base_new);
       m = m_new;
-      base = m_new == -__builtin_inff() ? 0.f : m_new;
+      base = base_new;
       l *= alpha;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
@@ -445,7 +454,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
           const int x = i * kScores + k;
           const float p = exp2_fast(fmaf(now[x], scale2, -base));
           l += p;
-          w[x >> 3][x & 7] = ChunkOps<FP8>::narrow(p);
+          w[x >> 3][x & 7] = O::narrow(p);
         }
       } else {
         o[(i - KK) % DT] = mfma32(__builtin_bit_cast(V8, operand[i]), w[(i - KK) / DT], o[(i - KK) % DT]);
@@ -581,9 +590,10 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       }
   }
   const int64_t at = (s.row0 + out.tok) * a.heads_q + out.hq;
+  const float ref = weight_reference<O::kRoom>(m);
   if (slot >= 0) {
     const int64_t pr = slot * kRows + (r - r0);
-    if (c0 == 0) plan.chunk_line.stats[pr] = float2{m, l};
+    if (c0 == 0) plan.chunk_line.stats[pr] = float2{ref, l};
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -592,7 +602,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
             f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
     return;
   }
-  const RowScale rs = row_scale(a, head, at, c0 == 0, m, l);
+  const RowScale rs = row_scale(a, head, at, c0 == 0, ref, l);
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll

@@ -14,6 +14,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// What the weights of a row with maximum m (log2 units) are relative to.  As
+// fp16 (e4m3 caches) weights up to 1 would lose bits below 2^-14 and be 0 below
+// 2^-25, while the row's sum still counts them: beside one score 14 (in units
+// of e) above the others, whose value is small, nothing of these would be left.
+// Relative to `ROOM` less than the maximum they use all of fp16's range.  Where
+// fp32 cannot tell m from m - ROOM they stay relative to m.
+template <int ROOM>
+__device__ __forceinline__ float weight_reference(float m) {
+  return ROOM > 0 && fabsf(m) < 0x1p20f ? m - (float)ROOM : m;
+}
+
 // x in the lane's row of 16 lanes, combined with the other rows': v[lane ^ 16] and v[lane ^ 32]
 __device__ __forceinline__ float max_over_rows(float v) {
   auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -8,7 +8,7 @@ namespace tb {
 // A sequence with few rows (attn_line.h) goes to the kernel for those, the
 // others to the chunk kernel.  Parts in the workspace, for each kind:
 //   values  float  [2 pieces][rows of a row tile][D]  (not divided by the sum)
-//   stats   float2 [2 pieces][rows of a row tile]     (maximum in log2 units, sum)
+//   stats   float2 [2 pieces][rows of a row tile]     (what both are relative to, in log2 units; sum)
 struct AttnLine {
   int pieces;     // workgroups; 0: one for each item, none is in parts
   int least;      // tiles of a piece

@@ -9,7 +9,9 @@
 // are chosen so that a lane's eight weights of a 32-position block belong to
 // eight consecutive positions, which is one 16-byte load of a V page
 // ([d][position]) for bf16; for e4m3 two blocks share a load of 16 positions.
-// The running maximum and sum of each row are kept in log2 units.
+// The running maximum and sum of each row are kept in log2 units; sums and
+// values are relative to weight_reference of the maximum, and what goes to LDS
+// and to the workspace as the maximum is that reference.
 //
 // What bounds it: the cache's bytes.  Every K and V byte is loaded once,
 // straight into operand registers (no LDS, no barrier in the loop), and each
@@ -35,6 +37,7 @@ template <>
 struct RowOps<false> {
   typedef uint16_t Elem;
   static constexpr int kBlocks = 1;  // 32-position blocks per tile
+  static constexpr int kRoom = 0;    // weights are at most 2^kRoom (weight_reference)
   typedef bf16x8 V8;
 };
 
@@ -42,6 +45,7 @@ template <>
 struct RowOps<true> {
   typedef uint8_t Elem;
   static constexpr int kBlocks = 2;
+  static constexpr int kRoom = 15;  // 2^16 is past fp16's largest
   typedef f16x8 V8;
 };
 
@@ -157,7 +161,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   load_keys(ta, t, pa);
   load_values(ta, t, pa);
 
-  float m = -__builtin_inff(), l = 0.f;
+  float m = -__builtin_inff(), ref = m, l = 0.f;
   f32x4 o[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -218,10 +222,12 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[st][e]);
     const float m_new = fmaxf(m, max_over_rows(top));
-    const float base = m_new == -__builtin_inff() ? 0.f : m_new;
+    const float ref_new = weight_reference<O::kRoom>(m_new);
+    const float base = m_new == -__builtin_inff() ? 0.f : ref_new;
     // at least the smallest number: a sum may hold an infinity, and keeps it
-    const float alpha = m == -__builtin_inff() ? 1.f : fmaxf(exp2_fast(m - base), 1.17549435e-38f);
+    const float alpha = m == -__builtin_inff() ? 1.f : fmaxf(exp2_fast(ref - base), 1.17549435e-38f);
     m = m_new;
+    ref = ref_new;
     float sum = 0.f;
 #pragma unroll
     for (int st = 0; st < S; ++st)
@@ -302,7 +308,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   // the waves' sums joined: each scales its values to the common maximum
   l = sum_over_rows(l);
   if (q4 == 0) {
-    sm.max[wave * 16 + i16] = m;
+    sm.max[wave * 16 + i16] = ref;
     sm.sum[wave * 16 + i16] = l;
   }
   __syncthreads();
@@ -310,7 +316,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     float top = -__builtin_inff();
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w * 16 + i16]);
-    const float f = exp2_fast(m - (top == -__builtin_inff() ? 0.f : top));
+    const float f = exp2_fast(ref - (top == -__builtin_inff() ? 0.f : top));
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) {
       if (w != wave) continue;

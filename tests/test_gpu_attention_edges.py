@@ -61,3 +61,31 @@ def test_sequences_past_max_q_hide_none(workspace, cache):
     out[~done] = torch.from_numpy(ref).to(torch.float32).to(DEV)[~done]
     lse[~done] = torch.from_numpy(rl).to(torch.float32).to(DEV)[~done]
     c.check(out, lse, what="past max_q")
+
+
+# ---------------------------------------------------------------- a dominant score
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("n", [1, 5, 40])
+@pytest.mark.parametrize("gap", [12.0, 16.0])
+def test_small_weights_beside_a_dominant_one(gap, n, workspace, cache):
+    """One position scores `gap` above every other, and its value is 0: the output
+    is what the others' small weights make it.  The bound is relative to that."""
+    say(f"dominant {gap} {n} {workspace} {cache}")
+    kv = 8192
+    for at in (0, 5003):
+        c = Case([(n, kv)], 2, 1, 128, 64, cache, poison=False)
+        g = torch.Generator().manual_seed(n)
+        score = torch.randn(kv, generator=g)
+        score[at] = score.max() + gap
+        k_scale = 1.0 if c.k_scale is None else float(c.k_scale[0])
+        # scores are 8 times channel 0 of the keys
+        c.q.zero_()
+        c.q[:, :, 0] = 8.0
+        for x in range(0, kv, c.page):
+            i = int(c.table[0, x // c.page])
+            c.k[i, 0, :, 0] = (score[x:x + c.page] / 8 / k_scale).to(c.k.dtype).to(DEV)
+        c.v[int(c.table[0, at // c.page]), 0, :, at % c.page] = 0.0
+        out, lse = _attend_into(c, c.q, workspace, scale=1.0)
+        c.check(out, lse, scale=1.0, what=f"{gap} above, at {at}")
