@@ -1,5 +1,6 @@
 // tb_paged_attention: its kernels, how a call is cut, and its launches.
 #include "attn_chunk.h"
+#include "attn_grid.h"
 #include "tb_launch.h"
 
 namespace tb {
@@ -17,13 +18,14 @@ __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_atten
   __shared__ float stats[2][16 * kAttnWaves];
   __shared__ uint32_t marks[CHUNK ? kChunkTile * D / 16 : 1];
   const AttnShared sm{{b0, b1, b2, b3}, stats[0], stats[1], marks};
-  if (CHUNK && (!ROWS || blockIdx.x < plan.chunk_blocks)) {
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (CHUNK && (!ROWS || block < plan.chunk_blocks)) {
     if constexpr (CHUNK)
-      run_line<true, FP8>(a, plan, blockIdx.x, [&](const LineItem& it, int t0, int t1, int64_t slot) {
+      run_line<true, FP8>(a, plan, block, [&](const LineItem& it, int t0, int t1, int64_t slot) {
         attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
       });
   } else if constexpr (ROWS) {
-    run_line<false, FP8>(a, plan, blockIdx.x - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot) {
+    run_line<false, FP8>(a, plan, block - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot) {
       attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
     });
   }
@@ -140,20 +142,22 @@ __global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args 
 constexpr int kPieces = 512;  // two workgroups for each of 256 CUs
 
 // rows of the largest sequence
-int64_t most_rows(const tb_paged_attention_args& a) { return a.cache.max_q * (a.heads_q / a.cache.heads_kv); }
+int64_t most_rows(const tb_paged_attention_args& a) {
+  return most_tokens(a.cache.max_q, a.cache.total_q) * (a.heads_q / a.cache.heads_kv);
+}
 
 // Whether sequences may have more rows than `few`, and whether any may go to the
-// kernel for few rows.  Token arrays of exactly B * max_q rows are most likely
-// those of B sequences of max_q tokens; as the lengths are not known here, the
+// kernel for few rows.  Token arrays of exactly B times the most tokens are most
+// likely those of B equal sequences; as the lengths are not known here, the
 // chunk kernel, launched alone, then takes the short ones too (few is 0).
 bool has_chunk(const tb_paged_attention_args& a, const AttnPlan& p) { return most_rows(a) > p.few; }
 bool has_rows(const tb_paged_attention_args& a, const AttnPlan& p) {
-  return !has_chunk(a, p) || a.cache.total_q != a.cache.B * a.cache.max_q;
+  return !has_chunk(a, p) || a.cache.total_q != a.cache.B * most_tokens(a.cache.max_q, a.cache.total_q);
 }
 
-// about the items of chunks
+// the items of chunks, at most
 int64_t chunk_items(const tb_paged_attention_args& a, const AttnPlan& p) {
-  return (a.cache.total_q * p.group / kChunkTile + a.cache.B) * a.cache.heads_kv;
+  return most_row_tiles(a.cache.total_q, a.cache.B, p.group, p.few, kChunkTile) * a.cache.heads_kv;
 }
 
 AttnPlan plan_of(const tb_paged_attention_args& a) {
@@ -167,10 +171,8 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   int64_t keys = a.window > 0 && a.window + c.max_q < a.max_kv ? a.window + c.max_q : a.max_kv;
   if (keys > TB_MAX_POSITIONS) keys = TB_MAX_POSITIONS;
   p.rows_line.least = 8;
-  p.rows_line.row_tiles = 1;
   p.rows_line.slot_rows = kRowsTile;
   p.chunk_line.least = 4;
-  p.chunk_line.row_tiles = (int)((most_rows(a) + kChunkTile - 1) / kChunkTile);
   p.chunk_line.slot_rows = kChunkTile;
   if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype == TB_FP8)) p.rows_line.pieces = kPieces;
   // Chunks whose items fill the GPU are not cut: one after another, the row
@@ -198,10 +200,10 @@ template <int D, bool FP8>
 hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stream) {
   const tb_paged_cache& c = a.cache;
   const bool chunk = has_chunk(a, p), rows = has_rows(a, p);
-  const int64_t heads = c.B * c.heads_kv;
-  p.chunk_blocks = !chunk ? 0 : (unsigned)(p.chunk_line.pieces ? p.chunk_line.pieces : heads * p.chunk_line.row_tiles);
-  const unsigned few = !rows ? 0 : (unsigned)(p.rows_line.pieces ? p.rows_line.pieces : heads);
-  const dim3 grid(p.chunk_blocks + few), block(64 * kAttnWaves);
+  p.chunk_blocks = !chunk ? 0 : p.chunk_line.pieces ? p.chunk_line.pieces : chunk_items(a, p);
+  const int64_t few = !rows ? 0 : p.rows_line.pieces ? p.rows_line.pieces : c.B * c.heads_kv;
+  const GridXY xy = grid_of(p.chunk_blocks + few);
+  const dim3 grid(xy.x, xy.y), block(64 * kAttnWaves);
   if (!chunk) hipLaunchKernelGGL((attn_kernel<D, FP8, true, false>), grid, block, 0, stream, a, p);
   else if (!rows) hipLaunchKernelGGL((attn_kernel<D, FP8, false, true>), grid, block, 0, stream, a, p);
   else hipLaunchKernelGGL((attn_kernel<D, FP8, true, true>), grid, block, 0, stream, a, p);

@@ -12,7 +12,6 @@ namespace tb {
 struct AttnLine {
   int pieces;     // workgroups; 0: one for each item, none is in parts
   int least;      // tiles of a piece
-  int row_tiles;  // most of a sequence
   int slot_rows;  // rows of a slot
   float* values;
   float2* stats;
@@ -29,7 +28,7 @@ struct AttnPlan {
   int64_t capacity;  // positions that the table has room for
   int group;         // query heads of a key/value head
   int shift;         // log2 of a page's positions
-  unsigned chunk_blocks;  // workgroups of chunks: they come first
+  int64_t chunk_blocks;  // workgroups of chunks: they come first
   AttnLine rows_line, chunk_line;
   __host__ __device__ bool is_chunk(int64_t nrows) const { return nrows > few; }
 };

@@ -235,25 +235,74 @@ __device__ __forceinline__ LineParts line_parts(int64_t start, int tiles, int64_
   return r;
 }
 
-// What a workgroup does: all parts of its piece of the line, or, if the line is
-// not cut, its item.  part(item, t0, t1, slot) does tiles t0 .. t1 - 1 of an
-// item, all of them if slot < 0; LDS is free for it when it is called.
-template <bool CHUNK, bool FP8, typename F>
-__device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const AttnPlan& plan, unsigned block, F part) {
+// Item `at` of a line that is not cut; false if there is none.  Chunks: of the
+// items that exist, so that how far max_q is above the lengths costs nothing;
+// the last rows of a sequence see the most positions and go first.  Few rows: a
+// sequence has one for each head, and none if it is of the other kind.  Whole
+// waves, the same arguments in every lane.
+template <bool CHUNK, bool FP8>
+__device__ __forceinline__ bool uncut_item(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at,
+                                           LineItem& it) {
   typedef LineKind<CHUNK, FP8> K;
+  const int64_t heads = a.cache.heads_kv;
+  it = LineItem{};
+  int64_t t = at >> 32 == 0 ? (int64_t)((uint32_t)at / (uint32_t)heads) : at / heads;
+  it.head = (int)(at - t * heads);
+  if constexpr (CHUNK) {
+    constexpr int kAhead = 4;  // of 64 sequences, whose lengths are loaded together
+    const int lane = threadIdx.x & 63;
+    for (int64_t b0 = 0; it.seq.rows == 0; b0 += 64 * kAhead) {
+      if (b0 >= a.cache.B) return false;
+      LineSeq own[kAhead];
+      int64_t n[kAhead], sum = 0;  // row tiles
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t b = b0 + 64 * u + lane;
+        own[u] = LineSeq{};
+        if (b < a.cache.B) own[u] = K::sequence(a, plan, b);
+        n[u] = (own[u].rows + K::kRows - 1) / K::kRows;
+        sum += n[u];
+      }
+      sum = wave_sum(sum);
+      if (t >= sum) {
+        t -= sum;
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (it.seq.rows != 0) continue;
+        const int64_t up = wave_prefix(n[u]);
+        const uint64_t past = __ballot(up > t);
+        if (past == 0) {
+          t -= of_lane(up, 63);
+          continue;
+        }
+        const int l = uniform(__builtin_ctzll(past));
+        it.b = b0 + 64 * u + l;
+        it.rt = (int)(of_lane(up, l) - 1 - t);
+        it.seq = uniform_seq(own[u], l);
+      }
+    }
+  } else {
+    if (t >= a.cache.B) return false;
+    it.b = t;
+    it.seq = K::sequence(a, plan, t);
+    if (it.seq.rows == 0) return false;
+  }
+  Line<CHUNK, FP8>::set(a, plan, it);
+  it = uniform_item(it);
+  return true;
+}
+
+// What workgroup `block` does: all parts of its piece of the line, or, if the
+// line is not cut, its item.  part(item, t0, t1, slot) does tiles t0 .. t1 - 1 of
+// an item, all of them if slot < 0; LDS is free for it when it is called.
+template <bool CHUNK, bool FP8, typename F>
+__device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t block, F part) {
   const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
   if (cut.pieces == 0) {
-    LineItem it{};
-    const unsigned heads = (unsigned)a.cache.heads_kv, row_tiles = (unsigned)cut.row_tiles;
-    it.head = block % heads;
-    it.b = block / heads / row_tiles;
-    it.seq = K::sequence(a, plan, it.b);
-    // the last rows of a sequence see the most positions: they go first
-    it.rt = (it.seq.rows + K::kRows - 1) / K::kRows - 1 - (int)(block / heads % row_tiles);
-    if (it.rt < 0 || it.seq.rows == 0) return;
-    Line<CHUNK, FP8>::set(a, plan, it);
-    it = uniform_item(it);
-    part(it, 0, it.tiles, (int64_t)-1);
+    LineItem it;
+    if (uncut_item<CHUNK, FP8>(a, plan, block, it)) part(it, 0, it.tiles, (int64_t)-1);
     return;
   }
   LineItem it;
@@ -261,7 +310,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
   {
     Line<CHUNK, FP8> line(a, plan);
     const int64_t per = cut.piece(line.total);
-    at = uniform64((int64_t)block * per);
+    at = uniform64(block * per);
     end = uniform64(at + per < line.total ? at + per : line.total);
     if (at >= end) return;
     it = line.find(a, plan, at);
@@ -269,7 +318,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
   for (int nth = 0;; nth = 1) {
     const int t0 = uniform((int)(at - it.start));
     const int t1 = uniform(it.start + it.tiles < end ? it.tiles : (int)(end - it.start));
-    part(it, t0, t1, t0 == 0 && t1 == it.tiles ? (int64_t)-1 : 2 * (int64_t)block + nth);
+    part(it, t0, t1, t0 == 0 && t1 == it.tiles ? (int64_t)-1 : 2 * block + nth);
     at = it.start + t1;
     if (at >= end) return;
     __syncthreads();  // the next part writes the LDS that this one reads

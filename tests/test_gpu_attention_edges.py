@@ -89,3 +89,59 @@ def test_small_weights_beside_a_dominant_one(gap, n, workspace, cache):
         c.v[int(c.table[0, at // c.page]), 0, :, at % c.page] = 0.0
         out, lse = _attend_into(c, c.q, workspace, scale=1.0)
         c.check(out, lse, scale=1.0, what=f"{gap} above, at {at}")
+
+
+# ---------------------------------------------------------------- many sequences
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("kind", ["mixed", "chunks", "steps"])
+def test_more_sequences_than_lanes(kind, workspace, cache):
+    """More than 64 and more than 256 sequences, some without tokens, of one kind and of both."""
+    say(f"many sequences {kind} {workspace} {cache}")
+    rng = np.random.default_rng(3)
+    lens = []
+    for i in range(300 if kind == "chunks" else 130):
+        n = {"steps": 1, "chunks": int(rng.integers(9, 14)), "mixed": 1 if i % 9 else int(rng.integers(9, 150))}[kind]
+        n = 0 if i % 17 == 4 else n
+        lens.append((n, n + int(rng.integers(0, 40 if kind == "chunks" else 900))))
+    c = Case(lens, 4, 2, 64, 16, cache)
+    out, lse = _attend_into(c, c.q, workspace)
+    c.check(out, lse, what=kind)
+
+
+def _shared_pages(kv, hkv, page):
+    """Caches of as many pages as the longest sequence has: all sequences share them."""
+    pages, g = -(-kv // page), torch.Generator(device=DEV).manual_seed(5)
+    k = torch.randn((pages, hkv, page, 64), generator=g, device=DEV, dtype=torch.bfloat16)
+    v = torch.randn((pages, hkv, 64, page), generator=g, device=DEV, dtype=torch.bfloat16)
+    return k, v, torch.arange(pages, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("b,long,max_q,window", [(8192, 200, 1 << 20, 0), (256, 131072, 131072, 16), (2, 300, 1 << 21, 0)])
+def test_one_prompt_among_many_steps(b, long, max_q, window):
+    """As many workgroups as there is work for, however large B and max_q are:
+    the prompt (first or last) and the single tokens are what they are alone."""
+    hq, hkv, page = 64, 8, 64
+    say(f"one prompt of {long} among {b - 1}, max_q {max_q}")
+    k, v, pages = _shared_pages(long, hkv, page)
+    table = pages.expand(b, -1).contiguous()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    g = torch.Generator(device=DEV).manual_seed(b)
+    q = torch.randn((long + b - 1, hq, 64), generator=g, device=DEV, dtype=torch.bfloat16)
+    steps = [1 + (7 * i) % 200 for i in range(b - 1)]
+    prompt, pl = tb.tb_paged_attention(q[:long], k, v, table[:1], i32([0, long]), i32([long]), long, 250, window=window,
+                                       with_lse=True)
+    single, sl = tb.tb_paged_attention(q[long:], k, v, table[1:], i32(list(range(b))), i32(steps), 1, 250, window=window,
+                                       with_lse=True)
+    out, lse = tb.tb_paged_attention(q, k, v, table, i32([0] + list(range(long, long + b))), i32([long] + steps), max_q, 250,
+                                     window=window, with_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:long], prompt) and torch.equal(lse[:long], pl)
+    assert torch.equal(out[long:], single) and torch.equal(lse[long:], sl)
+    turned = torch.cat([q[long:], q[:long]])
+    out, lse = tb.tb_paged_attention(turned, k, v, table, i32(list(range(b)) + [long + b - 1]), i32(steps + [long]), max_q, 250,
+                                     window=window, with_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out[b - 1:], prompt) and torch.equal(lse[b - 1:], pl)
+    assert torch.equal(out[:b - 1], single) and torch.equal(lse[:b - 1], sl)
