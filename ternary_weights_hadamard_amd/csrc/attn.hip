@@ -1,6 +1,5 @@
 // tb_paged_attention: its kernels, how a call is cut, and its launches.
 #include "attn_chunk.h"
-#include "attn_grid.h"
 #include "tb_launch.h"
 
 namespace tb {

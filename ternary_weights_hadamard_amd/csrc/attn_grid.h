@@ -1,8 +1,9 @@
 // How many workgroups a tb_paged_attention call has work for, from what the
-// host knows.  Plain C++, so that the bounds are also tested on the host.
+// host knows, and which head a workgroup's work is of.  Plain C++, so that it is
+// also tested on the host.
 #pragma once
 
-#include <stdint.h>
+#include "paged.h"
 
 namespace tb {
 
@@ -27,6 +28,12 @@ inline int64_t most_tokens(int64_t max_q, int64_t total_q) { return max_q < tota
 inline int64_t most_row_tiles(int64_t total_q, int64_t B, int64_t group, int64_t few, int64_t tile) {
   const int64_t some = total_q / (few / group + 1);
   return total_q * group / tile + (B < some ? B : some);
+}
+
+// The head whose `tiles` hold place `at`, all heads' in order: heads * tiles pass
+// 32 bits (129 heads of 2^30 positions), but 64-bit divisions are long.
+TB_HOST_DEVICE int head_of(int64_t at, int tiles) {
+  return at >> 32 == 0 ? (int)((uint32_t)at / (uint32_t)tiles) : (int)(at / tiles);
 }
 
 }  // namespace tb

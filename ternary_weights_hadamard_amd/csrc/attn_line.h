@@ -11,6 +11,7 @@
 // read back to the host: every workgroup finds its piece from cu_q and kv_len.
 #pragma once
 
+#include "attn_grid.h"
 #include "attn_launch.h"
 #include "wave_scan.h"
 
@@ -166,7 +167,7 @@ struct Line {
       }
     }
     set(a, plan, it);
-    it.head = (int)((unsigned)(at - it.start) / (unsigned)it.tiles);  // heads * tiles of one row tile: 32 bits
+    it.head = head_of(at - it.start, it.tiles);
     it.start += (int64_t)it.head * it.tiles;
     return uniform_item(it);
   }

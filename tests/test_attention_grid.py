@@ -1,4 +1,4 @@
-"""The workgroups of an attention call, from its sizes (compiled for the host)."""
+"""The workgroups of an attention call and what they find, from its sizes (compiled for the host)."""
 
 import ctypes
 import os
@@ -21,6 +21,7 @@ extern "C" int64_t tokens(int64_t max_q, int64_t total_q) { return tb::most_toke
 extern "C" int64_t tiles(int64_t total_q, int64_t B, int64_t group, int64_t few, int64_t tile) {
   return tb::most_row_tiles(total_q, B, group, few, tile);
 }
+extern "C" int head(int64_t at, int tiles) { return tb::head_of(at, tiles); }
 """
 
 
@@ -38,6 +39,7 @@ def probe(tmp_path_factory):
     lib.grid.argtypes = [i64, ctypes.POINTER(i64)]
     lib.tokens.argtypes, lib.tokens.restype = [i64] * 2, i64
     lib.tiles.argtypes, lib.tiles.restype = [i64] * 5, i64
+    lib.head.argtypes = [i64, ctypes.c_int]
     return lib
 
 
@@ -76,3 +78,10 @@ def test_lengths_and_not_max_q_make_the_grid(probe):
     # 255 single tokens of 5 rows each cannot all have more than 16: at most a fourth of them
     assert probe.tiles(2303, 256, 5, 16, 128) == 2303 * 5 // 128 + 256
     assert probe.tiles(300, 256, 5, 16, 128) == 300 * 5 // 128 + 75
+
+
+def test_head_of_a_place_past_32_bits(probe):
+    for heads, tiles in ((8, 1000), (128, 1 << 25), (129, 1 << 25), (65535, (1 << 25) - 3), (65535, 1), (300, 1 << 24)):
+        for h in (0, 1, heads // 2, heads - 1):
+            for at in (h * tiles, h * tiles + tiles // 2, (h + 1) * tiles - 1):
+                assert probe.head(at, tiles) == h
