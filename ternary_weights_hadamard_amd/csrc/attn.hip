@@ -15,17 +15,18 @@ __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_atten
   static_assert(kBuffer >= kRowsTile * (D + 4) * 4, "both kinds share the buffers");
   __shared__ u32x4 b0[kBuffer / 16], b1[kBuffer / 16], b2[kBuffer / 16], b3[kBuffer / 16];
   __shared__ float stats[2][16 * kAttnWaves];
+  __shared__ int bits[kAttnWaves];
   __shared__ uint32_t marks[CHUNK ? kChunkTile * D / 16 : 1];
-  const AttnShared sm{{b0, b1, b2, b3}, stats[0], stats[1], marks};
+  const AttnShared sm{{b0, b1, b2, b3}, stats[0], stats[1], bits, marks};
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (CHUNK && (!ROWS || block < plan.chunk_blocks)) {
     if constexpr (CHUNK)
-      run_line<true, FP8>(a, plan, block, [&](const LineItem& it, int t0, int t1, int64_t slot) {
-        attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
+      run_line<true, FP8>(a, plan, block, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
+        return attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, careful, sm);
       });
   } else if constexpr (ROWS) {
-    run_line<false, FP8>(a, plan, block - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot) {
-      attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, sm);
+    run_line<false, FP8>(a, plan, block - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
+      return attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, careful, sm);
     });
   }
 }
@@ -87,12 +88,12 @@ __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const
         top = now;
         total = fmaf(total, alpha, st.y * f);
 #pragma unroll
-        for (int e = 0; e < DL / 4; ++e) v[e] *= alpha;
+        for (int e = 0; e < DL / 4; ++e) v[e] *= keep_infinity(alpha);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int p = p0 + G * u + g;
-        const float w = __shfl(f, p - c0, L);
+        const float w = keep_infinity(__shfl(f, p - c0, L));
 #pragma unroll
         for (int e = 0; e < DL / 4; ++e)
 #pragma unroll

@@ -22,7 +22,7 @@
 // memory-to-LDS path, each loaded one tile ahead; two workgroups of four waves
 // share a CU.  4 x up to 2048 tokens over 2048..8192, 40 heads, 8
 // key/value heads: 479 GFLOP in 553 us, 866 TFLOP/s (a large library product: 1255); 2 x
-// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 38.5 us.
+// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 36.7 us.
 #pragma once
 
 #include <type_traits>
@@ -64,8 +64,8 @@ __device__ __forceinline__ void wait_loads() {
 // Weights are relative to weight_reference<kRoom> of a maximum that may lag
 // behind the row's by 2^kSlack, so they are at most 2^(kRoom + kSlack).  For
 // fp16 the two share its range: more slack is less room for small weights, less
-// is more rescaling (2 x 777 tokens of the last line above: 37.9 us with a slack
-// of 8, 38.5 with 4, 39.5 with 2).
+// is more rescaling (the windowed chunk above, measured together: 37.9 us with a
+// slack of 8, 38.5 with 4, 39.5 with 2).
 template <bool FP8>
 struct ChunkOps;
 template <>
@@ -104,6 +104,19 @@ __device__ __forceinline__ void hold(T& x) {
 #endif
 }
 
+// The two low bits of x that are set in some lane of the workgroup, in every
+// lane; a barrier.  Between two calls there has to be another.  (The call for
+// it of the runtime counts lanes in three dimensions, in registers that the
+// compiler keeps through the loop over the tiles.)
+__device__ __forceinline__ int workgroup_bits(int x, int* of_wave) {
+  of_wave[threadIdx.x >> 6] = (__ballot(x & 1) != 0 ? 1 : 0) | (__ballot(x & 2) != 0 ? 2 : 0);
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWaves; ++w) all |= of_wave[w];
+  return uniform(all);
+}
+
 // Values that are not finite, in a tile that not every row sees all of (the
 // products multiply every value with every row's weight, 0 where it does not
 // see the position).  They are set to 0 in LDS.  Where some row sees one, it is
@@ -114,12 +127,13 @@ __device__ __forceinline__ void hold(T& x) {
 //   x0, there   the tile's first position, and which of its runs of 16 exist
 //   begin, end  the positions that some row sees
 template <int D, bool FP8, int ROWS>
-__device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, uint32_t* marks, bool& marked, int x0, uint32_t there,
-                                                    int begin, int end, int first_pos, int group, int r0, int nrows,
-                                                    int64_t window) {
+__device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, const AttnShared& sm, bool& marked, int x0,
+                                                    uint32_t there, int begin, int end, int first_pos, int group, int r0,
+                                                    int nrows, int64_t window) {
   constexpr int kThreads = 64 * kAttnWaves, kChunks = kTile * D / 8;
   typedef typename ChunkOps<FP8>::V8 V8;
-  const int tid = threadIdx.x;
+  int tid = threadIdx.x;
+  hold(tid);  // what follows from it is not kept for the next tile
   int bad = 0;  // 1: some value is not finite, 2: at a position that some row sees
 #pragma unroll 1
   for (int i = tid; i < kChunks; i += kThreads) {
@@ -128,8 +142,9 @@ __device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, uint32_t* mark
     const int row = i / (kTile / 8), x = x0 + (((i % (kTile / 8)) ^ ((row >> 1) & 7)) * 8);  // of the chunk: v_chunk
     bad |= x + 8 > begin && x < end ? 3 : 1;
   }
-  if (!__syncthreads_or(bad)) return;
-  if (__syncthreads_or(bad & 2)) {
+  const int any = workgroup_bits(bad, sm.bits);
+  if (any == 0) return;
+  if (any & 2) {
     marked = true;
     // a thread has one row, and a share of the channels
     const int row = tid % ROWS, share = tid / ROWS;
@@ -153,7 +168,7 @@ __device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, uint32_t* mark
         }
       }
       if (up | down) {
-        uint32_t* at = marks + (row * (D / 32) + (d >> 5)) * 2;
+        uint32_t* at = sm.marks + (row * (D / 32) + (d >> 5)) * 2;
         if (up) atomicOr(at, 1u << (d & 31));
         if (down) atomicOr(at + 1, 1u << (d & 31));
       }
@@ -193,10 +208,11 @@ __device__ __forceinline__ LaneRow lane_row(int r, int nrows, int group, int hea
 }
 
 // Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
-// it), or a part of it into the workspace's slot.
+// it), or a part of it into the workspace's slot.  True: nothing was written, it
+// is to be done again, `careful` (LDS is free for it).
 template <int D, bool FP8>
-__device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
-                                                const LineItem& it, int t_begin, int t_stop, int64_t slot,
+__device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                                const LineItem& it, int t_begin, int t_stop, int64_t slot, bool careful,
                                                 const AttnShared& sm) {
   typedef ChunkOps<FP8> O;
   typedef typename O::Elem Elem;
@@ -213,7 +229,11 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int r_last = r0 + kRows - 1 < nrows ? r0 + kRows - 1 : nrows - 1;
   const int j_first = uniform((unsigned)r0 / (unsigned)group), j_last = uniform((unsigned)r_last / (unsigned)group);
   const int first_tile = it.held.first, t_end = t_stop < it.held.count ? t_stop : it.held.count;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  // what follows from the thread is found again each time: kept for the next
+  // part, it would cost registers that the loop over the tiles has not
+  int own = threadIdx.x;
+  hold(own);
+  const int lane = own & 63, wave = uniform(own >> 6);
   const int i32 = lane & 31, half = lane >> 5;
 
   // the positions (low, pos] that the lane's row sees, and its wave's first and last row
@@ -229,9 +249,11 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   const int pos_first = uniform(s.first_pos + (int)((unsigned)w_first / (unsigned)group));
   const int pos_last = uniform(s.first_pos + (int)((unsigned)w_last / (unsigned)group));
   // Tiles whose first position is in (w_low, w_high] are seen whole by all of
-  // the wave's rows, those in (all_low, all_high] by all of the workgroup's.
+  // the wave's rows, those in (all_low, all_high] by all of the workgroup's
+  // (none if values are taken out of every tile).
   const int w_low = behind_window(pos_last), w_high = pos_first - (kTile - 1);
-  const int all_low = behind_window(s.first_pos + j_last), all_high = s.first_pos + j_first - (kTile - 1);
+  const int all_low = behind_window(s.first_pos + j_last);
+  const int all_high = careful ? -__INT_MAX__ - 1 : s.first_pos + j_first - (kTile - 1);
 
   // scores are scaled by |scale|; its sign goes into the queries.  A scale of
   // 0 is taken as the smallest number, so that an unseen -inf stays one.
@@ -524,8 +546,8 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     const int x0 = (first_tile + t) * kTile;
     const uint32_t there = runs_of(p0);
     if (!(there == 0xfu && x0 <= all_high && x0 > all_low))
-      take_nonfinite_tile<D, FP8, kRows>(v_lds, sm.marks, marked, x0, there, span.begin, span.end, s.first_pos, group, r0,
-                                         nrows, a.window);
+      take_nonfinite_tile<D, FP8, kRows>(v_lds, sm, marked, x0, there, span.begin, span.end, s.first_pos, group, r0, nrows,
+                                         a.window);
     if (!idle) {
       beside(sc[0], sc[1], k_lds, 1, v_lds, 0, ahead_v);
       settle(sc[1], t, 1, there);
@@ -578,7 +600,14 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
   hold(thread);
   const int r = r0 + (thread >> 6) * 32 + (thread & 31), c0 = 4 * (thread >> 5 & 1);
   const LaneRow out = lane_row(r, nrows, group, head);
-  if (!out.live) return;
+  if (!FP8 && !careful) {
+    bool bad = false;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) bad = bad || any_nonfinite(o[dt], 16);
+    bad = bad && out.live && fabsf(l) < __builtin_inff();  // else all of the row is NaN
+    if (workgroup_bits(bad, sm.bits)) return true;
+  }
+  if (!out.live) return false;
   if (marked) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -600,7 +629,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<f32x4*>(plan.chunk_line.values + pr * D + 32 * dt + 8 * j + c0) =
             f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
-    return;
+    return false;
   }
   const RowScale rs = row_scale(a, head, at, c0 == 0, ref, l);
 #pragma unroll
@@ -609,6 +638,7 @@ __device__ __forceinline__ void attn_chunk_part(const tb_paged_attention_args& a
     for (int j = 0; j < 4; ++j)
       write4(a, at * D + 32 * dt + 8 * j + c0,
              f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]}, rs);
+  return false;
 }
 
 }  // namespace tb

@@ -74,7 +74,11 @@ __device__ __forceinline__ f16x8 fp8_to_f16(const u32x2& w) {
 // weight, 0 where the token does not see it.  In the rare tile where both
 // occur, two products with 1 in the places of +inf (or NaN) and -inf (or NaN)
 // first count what each token sees of them, and the values then go in with
-// these elements replaced by 0.
+// these elements replaced by 0.  An infinity that all tokens see is one in each
+// sum, but its product is NaN with a weight that has rounded to 0 (or with the
+// low part of one).  Such sums are found when a part of the work is done; it is
+// then done again with the values of all tiles taken out and counted, and
+// keep_infinity joins the parts.  (e4m3 has no infinities, and NaN stays NaN.)
 template <typename V8>
 struct Nonfinite {
   V8 up, down;
@@ -97,6 +101,17 @@ __device__ __forceinline__ Nonfinite<V8> take_nonfinite(V8& v) {
 // what the counts of seen infinities and NaN add to a sum: +inf - inf is NaN
 __device__ __forceinline__ float nonfinite_sum(float up, float down) {
   return (up > 0.f ? __builtin_inff() : 0.f) + (down > 0.f ? -__builtin_inff() : 0.f);
+}
+
+// A factor of a sum that may hold an infinity: never 0.
+__device__ __forceinline__ float keep_infinity(float f) { return fmaxf(f, 1.17549435e-38f); }
+
+template <typename V>
+__device__ __forceinline__ bool any_nonfinite(const V& v, int n) {
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < n; ++e) bad = bad || !(fabsf(v[e]) < __builtin_inff());
+  return bad;
 }
 
 // any element of 8 bf16 (four words) infinite or NaN

@@ -54,6 +54,7 @@ __device__ __forceinline__ TileSpan tile_span(const PagedSpan& p, int positions)
 struct AttnShared {
   u32x4* buffer[4];
   float *max, *sum;
+  int* bits;        // of each wave, for what all waves have to know
   uint32_t* marks;  // of chunks: values that are not finite (attn_chunk.h)
 };
 

@@ -296,19 +296,28 @@ __device__ __forceinline__ bool uncut_item(const tb_paged_attention_args& a, con
 }
 
 // What workgroup `block` does: all parts of its piece of the line, or, if the
-// line is not cut, its item.  part(item, t0, t1, slot) does tiles t0 .. t1 - 1 of
-// an item, all of them if slot < 0; LDS is free for it when it is called.
+// line is not cut, its item.  part(item, t0, t1, slot, careful) does tiles t0 ..
+// t1 - 1 of an item, all of them if slot < 0; if it answers true it is to be done
+// again, carefully.  LDS is free for it when it is called, and when it answers.
 template <bool CHUNK, bool FP8, typename F>
 __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t block, F part) {
   const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
-  if (cut.pieces == 0) {
-    LineItem it;
-    if (uncut_item<CHUNK, FP8>(a, plan, block, it)) part(it, 0, it.tiles, (int64_t)-1);
-    return;
-  }
+  bool careful = false;
   LineItem it;
   int64_t at, end;
-  {
+  if (cut.pieces == 0) {
+    if (!uncut_item<CHUNK, FP8>(a, plan, block, it)) return;
+    if constexpr (CHUNK) {
+      // a copy of its own: with what the loop over a piece's parts holds, the
+      // chunk kernel runs out of scalar registers (4 x 2048 tokens 572 us for 547)
+      do {
+        careful = uniform(part(it, 0, it.tiles, (int64_t)-1, careful));
+      } while (careful);
+      return;
+    }
+    at = it.start = 0;
+    end = it.tiles;
+  } else {
     Line<CHUNK, FP8> line(a, plan);
     const int64_t per = cut.piece(line.total);
     at = uniform64(block * per);
@@ -316,10 +325,12 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     if (at >= end) return;
     it = line.find(a, plan, at);
   }
-  for (int nth = 0;; nth = 1) {
+  for (int nth = 0;;) {
     const int t0 = uniform((int)(at - it.start));
     const int t1 = uniform(it.start + it.tiles < end ? it.tiles : (int)(end - it.start));
-    part(it, t0, t1, t0 == 0 && t1 == it.tiles ? (int64_t)-1 : 2 * block + nth);
+    careful = uniform(part(it, t0, t1, t0 == 0 && t1 == it.tiles ? (int64_t)-1 : 2 * block + nth, careful));
+    if (careful) continue;
+    nth = 1;
     at = it.start + t1;
     if (at >= end) return;
     __syncthreads();  // the next part writes the LDS that this one reads

@@ -57,10 +57,12 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
 }
 
 // Tiles t0 .. t1 - 1 of an item: its output (slot < 0: they are all of it), or
-// a part of it into the workspace's slot.
+// a part of it into the workspace's slot.  True: nothing was written, it is to be
+// done again, `careful` (values that are not finite are taken out of every tile).
 template <int D, bool FP8>
-__device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a, const AttnPlan& plan,
-                                               const LineItem& it, int t0, int t1, int64_t slot, const AttnShared& sm) {
+__device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a, const AttnPlan& plan,
+                                               const LineItem& it, int t0, int t1, int64_t slot, bool careful,
+                                               const AttnShared& sm) {
   typedef RowOps<FP8> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
@@ -197,7 +199,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[st][e] *= scale2;
     // every row of the tile sees every position of it
-    const bool full = __ballot(pv < 0) == 0 && x0 + T - 1 <= s.first_pos &&
+    const bool full = !careful && __ballot(pv < 0) == 0 && x0 + T - 1 <= s.first_pos &&
                       (a.window <= 0 || x0 > (int64_t)s.first_pos + j1 - a.window);
     uint32_t seen = 0xffffffffu;  // bit 4 st + e
     if (!full) {
@@ -224,8 +226,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     const float m_new = fmaxf(m, max_over_rows(top));
     const float ref_new = weight_reference<O::kRoom>(m_new);
     const float base = m_new == -__builtin_inff() ? 0.f : ref_new;
-    // at least the smallest number: a sum may hold an infinity, and keeps it
-    const float alpha = m == -__builtin_inff() ? 1.f : fmaxf(exp2_fast(ref - base), 1.17549435e-38f);
+    const float alpha = m == -__builtin_inff() ? 1.f : keep_infinity(exp2_fast(ref - base));
     m = m_new;
     ref = ref_new;
     float sum = 0.f;
@@ -311,12 +312,28 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     sm.max[wave * 16 + i16] = ref;
     sm.sum[wave * 16 + i16] = l;
   }
+  if constexpr (!FP8) {
+    bool bad = false;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) bad = bad || any_nonfinite(o[dt], 4);
+    // a sum that is not finite makes all of the row NaN
+    sm.bits[wave] = !careful && __ballot(bad && row_live && fabsf(l) < __builtin_inff()) != 0 ? 1 : 0;
+  }
   __syncthreads();
+  if constexpr (!FP8) {
+    int any = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) any |= sm.bits[w];
+    if (uniform(any) != 0) {
+      __syncthreads();
+      return true;
+    }
+  }
   {
     float top = -__builtin_inff();
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w * 16 + i16]);
-    const float f = exp2_fast(ref - (top == -__builtin_inff() ? 0.f : top));
+    const float f = keep_infinity(exp2_fast(ref - (top == -__builtin_inff() ? 0.f : top)));
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) {
       if (w != wave) continue;
@@ -328,7 +345,7 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
   __syncthreads();
   constexpr int DL = D / 16;  // channels of a thread: 16 threads a row
   const int d0 = (threadIdx.x & 15) * DL, row = threadIdx.x >> 4;
-  if (row >= nrows) return;
+  if (row >= nrows) return false;
   float top = -__builtin_inff(), total = 0.f;
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm.max[w * 16 + row]);
@@ -348,13 +365,14 @@ __device__ __forceinline__ void attn_rows_part(const tb_paged_attention_args& a,
     if (d0 == 0) plan.rows_line.stats[pr] = float2{top, total};
 #pragma unroll
     for (int e = 0; e < DL / 4; ++e) *reinterpret_cast<f32x4*>(plan.rows_line.values + pr * D + d0 + 4 * e) = v[e];
-    return;
+    return false;
   }
   const int otok = (unsigned)row / (unsigned)group;
   const int64_t at = (s.row0 + otok) * a.heads_q + head * group + (row - otok * group);
   const RowScale rs = row_scale(a, head, at, d0 == 0, top, total);
 #pragma unroll
   for (int e = 0; e < DL / 4; ++e) write4(a, at * D + d0 + 4 * e, v[e], rs);
+  return false;
 }
 
 }  // namespace tb

@@ -145,3 +145,33 @@ def test_one_prompt_among_many_steps(b, long, max_q, window):
     torch.cuda.synchronize()
     assert torch.equal(out[b - 1:], prompt) and torch.equal(lse[b - 1:], pl)
     assert torch.equal(out[:b - 1], single) and torch.equal(lse[:b - 1], sl)
+
+
+# ---------------------------------------------------------- infinities that are seen
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("scale", [None, 3.0])
+@pytest.mark.parametrize("n,kv", [(1, 1000), (12, 1000), (150, 1000)])
+def test_infinite_values_stay_infinite(n, kv, scale, workspace):
+    """An infinity among the values of a position that a row sees is one in its
+    output, however small its weight (scores of scale 3 are hundreds apart); two of
+    different signs are NaN.  Other channels and heads are as they were."""
+    say(f"infinite {n} {kv} {scale} {workspace}")
+    c = Case([(n, kv), (n, n)], 4, 2, 128, 16, "bf16")
+    kw = {} if scale is None else dict(scale=scale)
+    first, fl = _attend_into(c, c.q, workspace, **kw)
+    for places in ([(3, 7, 1)], [(3, 7, -1), (700, 9, 1)], [(0, 7, 1), (517, 7, -1), (400, 9, 1), (401, 9, 1)]):
+        d = Case([(n, kv), (n, n)], 4, 2, 128, 16, "bf16")
+        want = {}
+        for x, ch, sign in places:
+            d.v[int(d.table[0, x // 16]), 1, ch, x % 16] = sign * float("inf")
+            want[ch] = want.get(ch, 0.0) + sign * float("inf")
+        out, lse = _attend_into(d, d.q, workspace, **kw)
+        assert torch.equal(lse, fl)
+        assert torch.equal(out[n:], first[n:]) and torch.equal(out[:n, :2], first[:n, :2])
+        for ch, w in want.items():
+            got = out[:n, 2:, ch]
+            assert (torch.isnan(got) if w != w else got == w).all(), (places, ch, w)
+        rest = torch.ones(128, dtype=torch.bool, device=DEV)
+        rest[list(want)] = False
+        assert torch.allclose(out[:n, 2:][..., rest], first[:n, 2:][..., rest], rtol=1e-5, atol=1e-6)
