@@ -655,10 +655,12 @@ TB_API tb_status tb_paged_append(const tb_paged_cache* cache, const void* k, int
  *           or NULL the positions are not split.  Calls sharing a workspace
  *           must be ordered on one stream.
  * Products of bf16 (e4m3 widened exactly) accumulate in fp32; softmax
- * statistics are fp32.  With an e4m3 cache the weights exp(s_y) enter the
- * product with the values as fp16: to 11 bits down to 2^-25 of the row's
- * largest, with fewer below, as 0 below 2^-36.  Results do not change between
- * equal calls.
+ * statistics are fp32.  The weights exp(s_y) enter the product with the values
+ * rounded.  bf16 cache: to 16 bits (as two bf16) for sequences of at most 16
+ * rows (tokens * heads_q / heads_kv), to 8 bits (as one) for longer ones, and
+ * for all of a call with total_q = B * max_q where those would be longer.  e4m3
+ * cache: as fp16, to 11 bits down to 2^-25 of the row's largest, with fewer
+ * below, as 0 below 2^-36.  Results do not change between equal calls.
  */
 typedef struct {
   tb_paged_cache cache;

@@ -69,7 +69,7 @@ __device__ __forceinline__ void wait_loads() {
 template <bool FP8>
 struct ChunkOps;
 template <>
-struct ChunkOps<false> {
+struct ChunkOps<false> {  // weights have bf16's 8 bits: as two bf16 (few rows) there would be half as many products again
   typedef uint16_t Elem;
   typedef bf16x8 V8;
   static constexpr int kRoom = 0, kSlack = 8;

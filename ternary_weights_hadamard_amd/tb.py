@@ -660,7 +660,9 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
     its cached positions, causal, the last `window` of them only if window > 0;
     the cache as in tb_paged_append, which comes first.  max_kv is the most
     positions a sequence is likely to hold (it only decides the split).  scale
-    defaults to 1 / sqrt(d).  Returns out [tokens, heads, d], and (out, lse) if
+    defaults to 1 / sqrt(d).  Softmax weights are rounded for the product with the
+    values, to 8 bits in chunks of more than 16 rows (tokens * shared heads) of a
+    bf16 cache: see include/tb.h.  Returns out [tokens, heads, d], and (out, lse) if
     `lse` (fp32 [tokens, heads]) is given or with_lse; rows that see nothing
     are 0 (lse -inf).  `workspace`: a device tensor of
     tb_paged_attention_workspace bytes, allocated here when None."""

@@ -175,3 +175,51 @@ def test_infinite_values_stay_infinite(n, kv, scale, workspace):
         rest = torch.ones(128, dtype=torch.bool, device=DEV)
         rest[list(want)] = False
         assert torch.allclose(out[:n, 2:][..., rest], first[:n, 2:][..., rest], rtol=1e-5, atol=1e-6)
+
+
+# ----------------------------------------------------------------- forms and layouts
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("lens,hq,hkv", [([(1, 3), (1, 7), (1, 40)], 4, 4), ([(2, 5), (1, 900), (3, 30)], 5, 1),
+                                         ([(1, 1500), (1, 6)], 16, 1)])
+def test_weights_of_few_rows_have_16_bits(lens, hq, hkv, workspace):
+    """A weight as two bf16 is off by half a step of the low one, 2^-8 of at most 2^-8
+    of it; scores of small queries add little (the sums of their magnitudes are
+    about 1)."""
+    e = 2.0 ** -24
+    c = Case(lens, hq, hkv, 128, 16, "bf16")
+    c.q.mul_(0.125)
+    out, lse = _attend_into(c, c.q, workspace)
+    ref, rl, mean, size = c.reference()
+    bound = (2.0 ** -16 + 2 * (128 + 4) * e * size[..., None] + (c.max_kv + 64) * e) * mean
+    err = np.abs(out.double().cpu().numpy() - ref)
+    say(f"  few rows {lens}: of the bound {np.max(err / bound):.2f}, of one of 8 bits {np.max(err / mean) * 256:.4f}")
+    assert np.all(err <= bound)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens", [[(1, 1), (1, 300)], [(1, 40), (1, 33), (1, 900)], [(2, 50), (0, 9), (1, 700), (9, 1400)]])
+def test_more_query_heads_than_a_tile_has_rows(lens, cache):
+    say(f"20 heads on one {lens} {cache}")
+    c = Case(lens, 40, 2, 64, 16, cache)
+    for workspace in (True, False):
+        out, lse = _attend_into(c, c.q, workspace)
+        c.check(out, lse, what="20 heads on one")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_table_rows_further_apart_than_their_entries(cache):
+    """The block table as some columns of a wider one, for the append and the attention."""
+    say(f"wide table {cache}")
+    lens = [(1, 70), (30, 130), (2, 2)]
+    c, d = (Case(lens, 4, 2, 128, 32, cache, poison=False) for _ in range(2))
+    wide = torch.full((3, c.table_d.shape[1] + 9), -5, dtype=torch.int32, device=DEV)
+    wide[:, 4:4 + c.table_d.shape[1]] = c.table_d
+    d.table_d = wide[:, 4:4 + c.table_d.shape[1]]
+    c.append()
+    d.append()
+    out, lse = _attend_into(c, c.q, True)
+    got, gl = _attend_into(d, d.q, True)
+    assert torch.equal(got, out) and torch.equal(gl, lse)
+    assert torch.equal(c.k.view(torch.uint8), d.k.view(torch.uint8)) and torch.equal(c.v.view(torch.uint8), d.v.view(torch.uint8))
+    d.check(got, gl, what="wide table")
