@@ -584,7 +584,7 @@ def _token_rows(t, heads, d, where):
         raise ValueError(f"{where} must be bfloat16 [tokens, {heads}, {d}] (got {t.dtype} {tuple(t.shape)})")
     if not t.is_cuda or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
         raise ValueError(f"{where}: a token's heads must be contiguous on the device")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+    return t.stride(0) if t.shape[0] > 1 else heads * d  # of one token it says nothing
 
 
 def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_scale, v_scale):

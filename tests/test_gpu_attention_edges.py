@@ -223,3 +223,19 @@ def test_table_rows_further_apart_than_their_entries(cache):
     assert torch.equal(got, out) and torch.equal(gl, lse)
     assert torch.equal(c.k.view(torch.uint8), d.k.view(torch.uint8)) and torch.equal(c.v.view(torch.uint8), d.v.view(torch.uint8))
     d.check(got, gl, what="wide table")
+
+
+def test_one_token_has_no_stride():
+    """The stride of a dimension of one says nothing: a single row of a wider or overlapping array is taken as it is."""
+    c = Case([(1, 50)], 4, 2, 64, 16, "bf16")
+    ref, rl = _attend_into(c, c.q, True)
+    for step in (1, 4 * 64 + 1, 4 * 64 - 8, 4 * 64 + 8):
+        q = c.q.contiguous().as_strided((1, 4, 64), (step, 64, 1))
+        out, lse = _attend_into(c, q, True)
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+        k, v = (x.contiguous().as_strided((1, 2, 64), (step, 64, 1)) for x in (c.new_k, c.new_v))
+        tb.tb_paged_append(k, v, c.k, c.v, c.table_d, c.cu_d, c.kv_d, c.max_q)
+        torch.cuda.synchronize()
+        i, s = int(c.table[0, 49 // 16]), 49 % 16
+        assert torch.equal(c.k[i, :, s], c.new_k[0]) and torch.equal(c.v[i, :, :, s], c.new_v[0])
+        ref, rl = _attend_into(c, c.q, True)
