@@ -605,7 +605,7 @@ def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max
         raise TypeError(f"{where}: block_table, cu_q and kv_len must be int32")
     if kv_len.dim() != 1 or cu_q.shape != (b + 1,) or block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"{where}: kv_len must be [B], cu_q [B + 1], block_table [B, entries]")
-    if not block_table.is_cuda or (block_table.numel() and block_table.stride(1) != 1):
+    if not block_table.is_cuda or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError(f"{where}: a sequence's block_table entries must be contiguous on the device")
     for sc in (k_scale, v_scale):
         if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):

@@ -239,3 +239,14 @@ def test_one_token_has_no_stride():
         i, s = int(c.table[0, 49 // 16]), 49 % 16
         assert torch.equal(c.k[i, :, s], c.new_k[0]) and torch.equal(c.v[i, :, :, s], c.new_v[0])
         ref, rl = _attend_into(c, c.q, True)
+
+
+def test_table_of_one_column_has_no_stride():
+    """Short sequences have a page each: their table is a row turned into a column."""
+    c = Case([(1, 5), (2, 16), (1, 9)], 4, 2, 64, 16, "bf16")
+    ref, rl = _attend_into(c, c.q, True)
+    c.table_d = c.table_d[:, 0].contiguous()[None].t()
+    assert c.table_d.stride() == (1, 3)
+    out, lse = _attend_into(c, c.q, True)
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+    c.append()
