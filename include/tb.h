@@ -81,8 +81,8 @@ extern "C" {
 typedef enum {
   TB_OK = 0,
   TB_ERR_NULL = 1,        /* a required pointer is NULL                         */
-  TB_ERR_SHAPE = 2,       /* N or K not a positive multiple of 128, bad batch   */
-  TB_ERR_ALIGN = 3,       /* a pointer is not 16-byte aligned                   */
+  TB_ERR_SHAPE = 2,       /* a size, count or stride outside its range          */
+  TB_ERR_ALIGN = 3,       /* a pointer is not aligned (16 bytes, or as stated)  */
   TB_ERR_DTYPE = 4,       /* unknown dtype enum value                           */
   TB_ERR_FORMAT = 5,      /* unknown format, or a plane given/missing for it    */
   TB_ERR_LAUNCH = 6,      /* the HIP runtime refused the launch                 */

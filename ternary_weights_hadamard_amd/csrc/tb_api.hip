@@ -168,8 +168,8 @@ const char* tb_status_string(int status) {
   switch (status) {
     case TB_OK: return "TB_OK";
     case TB_ERR_NULL: return "TB_ERR_NULL: a required pointer is NULL";
-    case TB_ERR_SHAPE: return "TB_ERR_SHAPE: N and K must be positive multiples of 128 and the batch in range";
-    case TB_ERR_ALIGN: return "TB_ERR_ALIGN: pointers must be 16-byte aligned";
+    case TB_ERR_SHAPE: return "TB_ERR_SHAPE: a size, count or stride is outside its range (of a product: N and K positive multiples of 128)";
+    case TB_ERR_ALIGN: return "TB_ERR_ALIGN: a pointer is not aligned (to 16 bytes, or to its elements where the call says so)";
     case TB_ERR_DTYPE: return "TB_ERR_DTYPE: unknown dtype";
     case TB_ERR_FORMAT: return "TB_ERR_FORMAT: unknown format or wrong planes for it";
     case TB_ERR_LAUNCH: return "TB_ERR_LAUNCH: the HIP runtime refused the launch";
