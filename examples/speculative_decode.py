@@ -8,7 +8,8 @@ rotated basis, and the operators between them stay in it:
   tb_block_norm       residual, norm and both rotations between two products
   tb_ternary_gemm     queries, keys and values of 128-wide heads stay rotated:
                       scores do not change, and the output projection takes
-                      rotated inputs
+                      rotated inputs (rotary positions, which this decoder does
+                      not have, would need queries and keys rotated back first)
   tb_paged_append     the new keys and values into the pages of the cache
   tb_paged_attention  the new tokens over their sequence's pages
   tb_verify_draft     which drafts are kept, and the token drawn after them

@@ -49,8 +49,8 @@ __device__ __forceinline__ LineParts parts_of_row(const tb_paged_attention_args&
 // (rows in many parts: what counts is the time of one).  Lane p of them holds the
 // statistics of part p, of L at a time, and their groups of 16 take the parts
 // in turn, D / 16 channels a lane.  Bound by latency: the line again, a row's
-// statistics and its first parts (16 rows of 40 heads 6.2 us; 8 x 45 rows of 8
-// key/value heads in 8 parts each 8.2 us by whole waves, 14.5 us by 16 lanes).
+// statistics and its first parts (16 rows of 40 heads 6.1 us; 8 x 45 rows of 8
+// key/value heads in 8 parts each 8.4 us by whole waves, 14.5 us by 16 lanes).
 template <int D, bool CHUNK, bool FP8, int L>
 __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const AttnPlan& plan, const LineParts& parts,
                                          const LineSeq& seq, int head, int r) {

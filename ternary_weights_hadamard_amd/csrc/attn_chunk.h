@@ -21,8 +21,10 @@
 // pages up.  Tiles of 64 positions of K and V are double buffered in LDS by the
 // memory-to-LDS path, each loaded one tile ahead; two workgroups of four waves
 // share a CU.  4 x up to 2048 tokens over 2048..8192, 40 heads, 8
-// key/value heads: 479 GFLOP in 553 us, 866 TFLOP/s (a large library product: 1255); 2 x
-// 777 tokens over 6000 in a window of 1000, 16 heads of 64 in e4m3: 36.7 us.
+// key/value heads: 479 GFLOP in 500 us, 958 TFLOP/s (a large library product:
+// 1255), 525 us in the first twenty calls, before the clock has risen; in e4m3
+// 540 us, in pages of 16 602 us.  2 x 777 tokens over 6000 in a window of 1000,
+// 16 heads of 64 in e4m3: 35.3 us.
 #pragma once
 
 #include <type_traits>
@@ -105,9 +107,9 @@ __device__ __forceinline__ void hold(T& x) {
 }
 
 // The two low bits of x that are set in some lane of the workgroup, in every
-// lane; a barrier.  Between two calls there has to be another.  (The call for
-// it of the runtime counts lanes in three dimensions, in registers that the
-// compiler keeps through the loop over the tiles.)
+// lane; a barrier.  Between two calls there has to be another.
+// (__syncthreads_or counts lanes in three dimensions, in registers that the
+// compiler keeps through the loop over the tiles: with it values are spilled.)
 __device__ __forceinline__ int workgroup_bits(int x, int* of_wave) {
   of_wave[threadIdx.x >> 6] = (__ballot(x & 1) != 0 ? 1 : 0) | (__ballot(x & 2) != 0 ? 2 : 0);
   __syncthreads();

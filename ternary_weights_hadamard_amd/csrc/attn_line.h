@@ -309,7 +309,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     if (!uncut_item<CHUNK, FP8>(a, plan, block, it)) return;
     if constexpr (CHUNK) {
       // a copy of its own: with what the loop over a piece's parts holds, the
-      // chunk kernel runs out of scalar registers (4 x 2048 tokens 572 us for 547)
+      // chunk kernel runs out of scalar registers (4 x 2048 tokens 5 % slower)
       do {
         careful = uniform(part(it, 0, it.tiles, (int64_t)-1, careful));
       } while (careful);

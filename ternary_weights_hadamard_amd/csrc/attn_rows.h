@@ -17,9 +17,9 @@
 // straight into operand registers (no LDS, no barrier in the loop), and each
 // half of a tile's registers is loaded again, for the wave's next tile, as soon
 // as its product is formed.  A token of each of 16 sequences of 2048..8192, 8
-// key/value heads: 357 MB in 69.9 us, 5.1 TB/s; of 4 sequences of 16384..65536
-// in e4m3: 330 MB in 63.6 us, 5.2 TB/s (a plain copy moves 5.1 TB/s).  One
-// sequence of 1000 with 40 key/value heads: 10.3 us, of which 2 are to find the
+// key/value heads: 357 MB in 70.4 us, 5.1 TB/s; of 4 sequences of 16384..65536
+// in e4m3: 330 MB in 63.2 us, 5.2 TB/s (a plain copy moves 5.1 TB/s).  One
+// sequence of 1000 with 40 key/value heads: 10.4 us, of which 2 are to find the
 // piece, 3 to the first tile, and 5 the launch and the joins of the waves.
 //
 // The four waves of a workgroup take the position tiles of a part in turn and
