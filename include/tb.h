@@ -92,8 +92,8 @@ typedef enum {
   TB_ERR_VALUE = 10       /* a scalar argument (scale, eps) outside its range   */
 } tb_status;
 
-/* TB_FP8 (OCP e4m3) is a dtype of the paged cache only. */
-typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_ACT8 = 2, TB_FP8 = 3 } tb_dtype;
+/* TB_FP8 (OCP e4m3) and TB_INT4 are dtypes of the paged cache only. */
+typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_ACT8 = 2, TB_FP8 = 3, TB_INT4 = 4 } tb_dtype;
 /* Quantiser rules and storage formats.  TB_FMT_DENSE_MINERR stores the dense
  * format; only the threshold and scale rule differ (tb_quantize_pack).
  * TB_FMT_DENSE_RESID stores two dense planes with their 128-groups
@@ -583,7 +583,25 @@ TB_API tb_status tb_block_norm(const tb_block_norm_args* args, void* stream);
  *   v_cache  [n_pages][heads_kv][head_dim][page]  (positions along the fast
  *            axis: the operand order of the product with the weights)
  * in cache_dtype: TB_BF16, or TB_FP8 (OCP e4m3) standing for code *
- * k_scale[head] (v_scale[head]; fp32 [heads_kv], NULL: 1).
+ * k_scale[head] (v_scale[head]; fp32 [heads_kv], NULL: 1), or TB_INT4.
+ * TB_INT4: codes 0 .. 15, one scale and one offset (fp16) for the head_dim
+ * channels of a position and head; a code stands for
+ *   value = fp16(scale * (64 + code) + offset)           (rounded once)
+ * so the offset is 64 steps below the least value.  (A code in the high half
+ * of a byte, below the byte 0x54, is the fp16 number 64 + code: it becomes a
+ * value by one multiply-add.)  A byte holds two channels of one position: byte
+ * 4 g + i of its head_dim / 2 bytes has channel 8 g + i in its low and channel
+ * 8 g + i + 4 in its high four bits.
+ *   k_cache  uint8 [n_pages][heads_kv][page][head_dim / 2]
+ *   v_cache  uint8 [n_pages][heads_kv][head_dim / 2][page]
+ *   k_scale  fp16  [n_pages][heads_kv][page][2]     (scale, offset)
+ *   v_scale  fp16  [n_pages][heads_kv][2][page]     (the scales, then the offsets)
+ * all four required, the scales aligned to 16 bytes.  Written positions have
+ *   lo, hi  the least and the largest channel, each first limited to +-4096
+ *   scale = fp16((hi - lo) / 15),  offset = fp16(lo - 64 scale),
+ *   code = round((x - offset) / scale) - 64, at least 0 and at most 15
+ * (ties to even; 0 if scale is 0), from channels that are exact to 64 bits
+ * but for their own rounding; a NaN among them makes all of them NaN (scale and offset NaN).
  * Sequence b of B holds kv_len[b] positions, its new tokens among them; the
  * page of position x is block_table[b * table_stride + x / page], of
  * table_width entries.  Its new tokens are rows cu_q[b] .. cu_q[b + 1] - 1 of
@@ -603,8 +621,8 @@ TB_API tb_status tb_block_norm(const tb_block_norm_args* args, void* stream);
 typedef struct {
   const void* k_cache;
   const void* v_cache;
-  const float* k_scale;
-  const float* v_scale;
+  const void* k_scale;
+  const void* v_scale;
   const int32_t* block_table;
   const int32_t* cu_q;
   const int32_t* kv_len;
@@ -626,8 +644,8 @@ typedef struct {
  * [total_q][heads_kv][head_dim], k_stride and v_stride elements between
  * tokens (a slice of a fused projection's output; multiples of 8, at least
  * heads_kv * head_dim).  TB_FP8: the nearest e4m3 value (ties to even) of
- * x / scale, at most 448 in magnitude; NaN stays NaN.  One launch; positions
- * other than the new tokens' are left as they are.
+ * x / scale, at most 448 in magnitude; NaN stays NaN.  TB_INT4: as above.  One
+ * launch; positions other than the new tokens' are left as they are.
  */
 TB_API tb_status tb_paged_append(const tb_paged_cache* cache, const void* k, int64_t k_stride, const void* v,
                           int64_t v_stride, void* stream);
@@ -659,8 +677,13 @@ TB_API tb_status tb_paged_append(const tb_paged_cache* cache, const void* k, int
  * rounded.  bf16 cache: to 16 bits (as two bf16) for sequences of at most 16
  * rows (tokens * heads_q / heads_kv), to 8 bits (as one) for longer ones, and
  * for all of a call with total_q = B * max_q where those would be longer.  e4m3
- * cache: as fp16, to 11 bits down to 2^-25 of the row's largest, with fewer
- * below, as 0 below 2^-36.  Results do not change between equal calls.
+ * cache, and 4-bit cache: as fp16, to 11 bits down to 2^-25 of the row's
+ * largest, with fewer below, as 0 below 2^-36.  4-bit cache: queries are
+ * multiplied as fp16 too, in units of a power of two that the row's largest
+ * gives: exactly, but for elements below 2^-24 of it, which are rounded to
+ * multiples of 2^-34 of it; an infinite value (from a scale or offset that
+ * tb_paged_append does not write) may be NaN in the outputs that see it.
+ * Results do not change between equal calls.
  */
 typedef struct {
   tb_paged_cache cache;
@@ -684,6 +707,91 @@ typedef struct {
 TB_API size_t tb_paged_attention_workspace(const tb_paged_attention_args* args);
 
 TB_API tb_status tb_paged_attention(const tb_paged_attention_args* args, void* stream);
+
+/*
+ * Rotary positions on the way into the cache: new tokens' queries and keys are
+ * rotated by their positions, queries come out, keys and values go into the
+ * cache as tb_paged_append writes them.  One launch.  For a head x of D
+ * channels of a token at position t:
+ *   x = H x                          if turn_in  (q and k)
+ *   (x_a, x_b) = factor * (x_a cos(w_i) - x_b sin(w_i), x_a sin(w_i) + x_b cos(w_i)),
+ *        w_i = t * inv_freq[i],  i < rotary_dim / 2,  (a, b) = (i, i + rotary_dim / 2), or
+ *        (2 i, 2 i + 1) if neighbours; channels from rotary_dim on stay as they are
+ *   x = H x                          if turn_out (q and k)
+ *   v = H v                          if turn_v
+ * H is the orthonormal 128-point Walsh-Hadamard transform: products of rotated
+ * weights give heads in its basis (turn_in takes them back), scores and the
+ * output projection of rotated weights take them in it (turn_out, turn_v), and
+ * it spreads a large channel over all of them, which is what few bits need.
+ *   q       bf16 [total_q][heads_q][D], q_stride elements between tokens, or
+ *           NULL (no queries: heads_q and q_out are not used)
+ *   k, v    as for tb_paged_append
+ *   q_out   bf16 [total_q][heads_q][D], contiguous; rows of no sequence, and past
+ *           a sequence's max_q, are left as they are
+ *   inv_freq  fp32 [rotary_dim / 2], radians a position; not read if rotary_dim is 0
+ *   rotary_dim  0 (no positions) or a multiple of 16, at most D
+ *   factor  multiplies cosine and sine (long contexts); finite (TB_ERR_VALUE)
+ *   turn_in, turn_out, turn_v only with head_dim 128 (else TB_ERR_SHAPE)
+ * Angles are formed and reduced in 64 bits.  Queries, and the keys of a bf16
+ * cache, are computed in fp32, with cosine and sine correct to fp32's step at
+ * 1; keys and values of the other caches in 64 bits, so that their codes are
+ * those of the formula but for ties that 64 bits do not tell.  A token at a
+ * negative position is rotated by it all the same (its key has no place).
+ */
+typedef struct {
+  tb_paged_cache cache;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const float* inv_freq;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int heads_q;
+  int rotary_dim;
+  int neighbours;
+  int turn_in;
+  int turn_out;
+  int turn_v;
+  float factor;
+  int reserved;  /* must be 0 */
+} tb_paged_rotary_args;
+
+TB_API tb_status tb_paged_append_rotary(const tb_paged_rotary_args* args, void* stream);
+
+/*
+ * Rotary frequencies, radians a position: inv_freq[i], i < rotary_dim / 2 (a
+ * HOST array), for positions up to `scale` times those a model was trained
+ * for, and the factor that goes with them (*factor, may be NULL).
+ *   f_i = base^(-2 i / rotary_dim)
+ *   TB_ROPE_PLAIN   f_i                                        factor 1
+ *   TB_ROPE_LINEAR  f_i / scale                                factor 1
+ *   TB_ROPE_NTK     f_i for base * scale^(R / (R - 2))         factor 1
+ *   TB_ROPE_YARN    f_i (1 - r_i) + f_i / scale * r_i,
+ *                   r_i = min(max((i - lo) / max(hi - lo, 0.001), 0), 1),
+ *                   lo = max(floor(c(fast)), 0), hi = min(ceil(c(slow)), R - 1),
+ *                   c(n) = R ln(trained / (2 pi n)) / (2 ln base);
+ *                   factor 0.1 ln(scale) + 1
+ * In 64 bits, rounded once.  rotary_dim as above, not 0 (NTK: at least 4);
+ * base > 1, scale >= 1, trained > 0, fast and slow > 0 (read by TB_ROPE_YARN
+ * only), all finite (else TB_ERR_VALUE).  Host-only.
+ */
+typedef enum { TB_ROPE_PLAIN = 0, TB_ROPE_LINEAR = 1, TB_ROPE_NTK = 2, TB_ROPE_YARN = 3 } tb_rope_scaling;
+
+TB_API tb_status tb_rotary_frequencies(int rotary_dim, double base, int scaling, double scale, double trained,
+                                double fast, double slow, float* inv_freq, float* factor);
+
+/*
+ * Read the cache back: rows cu_q[b] .. of k_out and v_out (out_dtype TB_F32 or
+ * TB_BF16, [total_q][heads_kv][head_dim], contiguous; either may be NULL) are
+ * the values that sequence b's last positions stand for, as tb_paged_append
+ * would write them (cu_q counting positions: kv_len of them for whole
+ * sequences).  For a sequence that leaves the pool, or goes to a cache of
+ * another type.  Rows whose position does not exist, rows of no sequence and
+ * past max_q are left as they are.  One launch.
+ */
+TB_API tb_status tb_paged_read(const tb_paged_cache* cache, void* k_out, void* v_out, int out_dtype, void* stream);
 
 /*
  * Verification of drafted tokens (speculative decoding) from given random
@@ -742,6 +850,91 @@ typedef struct {
 TB_API size_t tb_verify_draft_workspace(int64_t B, int64_t vocab);
 
 TB_API tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream);
+
+/*
+ * The probabilities of tokens from logits: what tb_verify_draft takes as p (and,
+ * without drafts, a sampler).  Sequence b has T = cu_draft[b + 1] - cu_draft[b]
+ * drafted tokens and T + 1 rows of logits, from row cu_draft[b] + b on; row j is
+ * what follows its first j drafts.  With params[b] = (temperature, repeats,
+ * presence, frequency) and c(v) the times that v is among the generated tokens
+ * of its history and its first j drafts:
+ *   x = logit + bias(v)
+ *   x = x > 0 ? x / repeats : x * repeats      if v is in the history or the j drafts
+ *   x = x - (frequency * c(v) + presence)      if c(v) > 0
+ *   x = -inf                                   if the row's mask does not allow v
+ *   p(v) = exp(x / temperature) / sum_w exp(x_w / temperature)
+ * A temperature that is not above 0 takes the largest x: p is 1 at the first
+ * of them and 0 elsewhere (NaN are passed over).  A row of which nothing is
+ * left (every x -inf) is all 0.  What the mask does not allow does not reach
+ * the row, NaN and infinities included; otherwise they do what they do in the formula.
+ * In fp32, p rounded once.
+ *   logits  [total + B][vocab] in logits_dtype (TB_F32 or TB_BF16),
+ *           logits_stride >= vocab elements between rows
+ *   p       [total + B][vocab] in p_dtype (TB_F32 or TB_BF16), p_stride; rows of
+ *           no sequence, and past a sequence's max_draft drafts, are left as they are
+ *   params  fp32 [B][4], 16-byte aligned
+ *   drafts  int32 [total] (NULL only if total is 0); cu_draft int32 [B + 1], or
+ *           NULL if total is 0 (no drafts: a row for each sequence); max_draft at
+ *           least every T, at most TB_MAX_DRAFT
+ *   history  int32 [total_history], or NULL (none): tokens cu_history[b] ..
+ *           cu_history[b + 1] - 1 are sequence b's; the first prompt_len[b] of
+ *           them (int32 [B]; NULL: 0) are its prompt's, which count as
+ *           repeated, not as generated.  At most 2^20 - 64 generated tokens of
+ *           a sequence are counted, the last ones
+ *   bias_ids int32, bias_values fp32 [total_bias], cu_bias int32 [B + 1], or
+ *           all NULL (bias 0): sequence b's biased tokens; of an id that is
+ *           there more than once the last one counts.  At most TB_MAX_BIAS of a
+ *           sequence are looked at, the first ones
+ *   mask    uint32 [n_masks][mask_stride >= ceil(vocab / 32)], or NULL (all is
+ *           allowed): bit v % 32 of word v / 32 allows token v; mask_row int32
+ *           [total + B] says which mask each row has, one outside [0, n_masks)
+ *           none (all is allowed); NULL: row r has mask r, and n_masks is total + B
+ *   workspace  tb_token_probs_workspace(args) bytes, 16-byte aligned (none up to
+ *           a vocabulary of 2^15: may be NULL).  Calls sharing a workspace must
+ *           be ordered on one stream.
+ * cu_draft, cu_history and cu_bias are read on the device: clamped to their
+ * arrays and to rise; ids outside [0, vocab) are passed over.  Arrays need only
+ * their elements' alignment but where more is said.
+ */
+#define TB_MAX_BIAS 2047
+
+typedef struct {
+  const void* logits;
+  void* p;
+  const float* params;
+  const int32_t* drafts;
+  const int32_t* cu_draft;
+  const int32_t* history;
+  const int32_t* cu_history;
+  const int32_t* prompt_len;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const int32_t* cu_bias;
+  const uint32_t* mask;
+  const int32_t* mask_row;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t B;
+  int64_t total;
+  int64_t vocab;
+  int64_t logits_stride;
+  int64_t p_stride;
+  int64_t total_history;
+  int64_t total_bias;
+  int64_t n_masks;
+  int64_t mask_stride;
+  int max_draft;
+  int logits_dtype;
+  int p_dtype;
+  int reserved;  /* must be 0 */
+} tb_token_probs_args;
+
+/* Workspace bytes of tb_token_probs for these arguments (of the pointers only
+ * whether there is a mask is looked at).  Host-only; 0 when none is used, and
+ * for invalid sizes. */
+TB_API size_t tb_token_probs_workspace(const tb_token_probs_args* args);
+
+TB_API tb_status tb_token_probs(const tb_token_probs_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -125,3 +125,81 @@ def verify_draft(p, q, drafts, u, u_next, cu, max_draft):
             past = np.nonzero((edge > u_next[b] * edge[-1]) & (w > 0))[0]
             tokens[b, m] = past[0] if len(past) else np.nonzero(w)[0][-1]
     return accepted, tokens
+
+
+def codes4(x):
+    """Rows [.., d] in 4 bits: (bytes [.., d / 2], scale, offset as float16 [..])."""
+    bad = np.isnan(x).any(-1)
+    x = np.clip(np.where(np.isnan(x), 0.0, x), -4096.0, 4096.0)
+    lo, hi = x.min(-1), x.max(-1)
+    scale = ((hi - lo) / 15).astype(np.float16)
+    s = scale.astype(np.float64)
+    offset = (lo - 64 * s).astype(np.float16)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        n = np.clip(np.rint((x - offset.astype(np.float64)[..., None]) / s[..., None]) - 64, 0, 15)
+    n = np.where((s == 0)[..., None] | bad[..., None], 0, n).astype(np.uint8)
+    out = np.zeros(x.shape[:-1] + (x.shape[-1] // 2,), np.uint8)
+    for c in range(x.shape[-1]):
+        out[..., 4 * (c // 8) + c % 4] |= n[..., c] << (4 if c % 8 >= 4 else 0)
+    nan = np.float16("nan")
+    return out, np.where(bad, nan, scale), np.where(bad, nan, offset)
+
+
+def values4(codes, scale, offset):
+    """What bytes [.., d / 2] of a position stand for, in float64 [.., d]."""
+    out = np.zeros(codes.shape[:-1] + (2 * codes.shape[-1],))
+    for c in range(out.shape[-1]):
+        byte = codes[..., 4 * (c // 8) + c % 4]
+        n = byte >> 4 if c % 8 >= 4 else byte & 15
+        with np.errstate(over="ignore", invalid="ignore"):
+            out[..., c] = (scale.astype(np.float64) * (64 + n.astype(np.float64)) + offset.astype(np.float64)).astype(np.float16)
+    return out
+
+
+def rotary(x, pos, inv_freq, factor, neighbours):
+    """Heads x [tokens, heads, d] rotated by their positions [tokens]; inv_freq
+    float64 [rotary_dim / 2]."""
+    half = len(inv_freq)
+    y = x.copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if neighbours else (i, i + half)
+        w = pos.astype(np.float64) * inv_freq[i]
+        c, s = factor * np.cos(w)[:, None], factor * np.sin(w)[:, None]
+        y[..., a], y[..., b] = x[..., a] * c - x[..., b] * s, x[..., a] * s + x[..., b] * c
+    return y
+
+
+def token_probs(logits, params, drafts, cu_draft, max_draft, history, cu_history, prompt_len, bias, allowed):
+    """Rows of float64 logits as probabilities (None: a row of no sequence).
+    history [b] and bias [b] are lists (tokens; (id, value) pairs), prompt_len [b];
+    allowed [row] is a set of bools [vocab], or None."""
+    vocab = logits.shape[1]
+    out = [None] * logits.shape[0]
+    for b in range(len(params)):
+        lo, n = int(cu_draft[b]), int(cu_draft[b + 1]) - int(cu_draft[b])
+        t, repeats, presence, frequency = (float(x) for x in params[b])
+        told, made = history[b][:prompt_len[b]], history[b][prompt_len[b]:]
+        for j in range(min(n, max_draft) + 1):
+            row = lo + b + j
+            x = logits[row].copy()
+            for i, v in dict((i, v) for i, v in bias[b] if 0 <= i < vocab).items():
+                x[i] += v
+            after = [i for i in list(made) + [int(d) for d in drafts[lo:lo + j]] if 0 <= i < vocab]
+            for i in set(after) | set(i for i in told if 0 <= i < vocab):
+                x[i] = x[i] / repeats if x[i] > 0 else x[i] * repeats
+            for i in set(after):
+                x[i] -= frequency * after.count(i) + presence
+            if allowed[row] is not None:
+                x = np.where(allowed[row], x, -np.inf)
+            p = np.zeros(vocab)
+            if t > 0:
+                if not (np.isneginf(x)).all():
+                    with np.errstate(invalid="ignore"):
+                        e = np.exp((x - x.max()) / t) if not np.isnan(x).any() else np.full(vocab, np.nan)
+                    p = e / e.sum()
+            else:
+                y = np.where(np.isnan(x), -np.inf, x)
+                if y.max() > -np.inf:
+                    p[int(np.argmax(y))] = 1.0
+            out[row] = p
+    return out

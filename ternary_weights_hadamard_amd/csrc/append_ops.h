@@ -1,0 +1,94 @@
+// What writes the paged cache's codes: bf16 pairs taken apart, e4m3 and 4-bit
+// roundings.
+#pragma once
+
+#include "tb_common.h"
+
+namespace tb {
+
+// nearest e4m3 of x (ties to even), at most 448 in magnitude; NaN stays NaN
+__device__ __forceinline__ uint32_t fp8_pair(float a, float b) {
+  a = a > 448.f ? 448.f : a < -448.f ? -448.f : a;
+  b = b > 448.f ? 448.f : b < -448.f ? -448.f : b;
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;
+}
+
+// x / scale, correctly rounded, for a scale whose reciprocal and products stay
+// far from the ends of fp32: the rounded quotient by the reciprocal, corrected
+// by its remainder once (exact but for quotients that e4m3 rounds to 0).  3 operations in place of about 10 of
+// the general division.  Quotients past
+// 512 are cut there before the correction, so that none of it overflows; NaN
+// and infinities come through by the remainder.
+struct Quotient {
+  float scale, inverse;
+  bool plain;
+  __device__ explicit Quotient(float s) : scale(s), inverse(1.f / s) { plain = s >= 0x1p-60f && s <= 0x1p60f; }
+  __device__ float operator()(float x) const {
+    if (!plain) return x / scale;
+    const float q = __builtin_amdgcn_fmed3f(x * inverse, -512.f, 512.f);
+    return __builtin_fmaf(-__builtin_fmaf(q, scale, -x), inverse, q);  // signs so that -0 stays -0
+  }
+};
+
+// channels 2w and 2w + 1 of a row of bf16
+__device__ __forceinline__ float channel(const u32x4& w, int d) {
+  return d & 1 ? __uint_as_float(w[d >> 1] & 0xffff0000u) : bf16_to_f32(w[d >> 1] & 0xffffu);
+}
+
+// The scale and offset of a position's channels in 4 bits (include/tb.h,
+// TB_INT4), and its codes: a group of LANES = D / 8 consecutive lanes holds a
+// position, 8 channels a lane.  In 64 bits: the scale rounds a quotient of 24
+// or more bits to 11, and a code a quotient by it, so that with 32 bits some of
+// 65536 rows get another scale, and with it other values in every channel.
+struct Codes4 {
+  uint32_t word;   // byte i: channels i (low) and i + 4 of the lane's eight
+  uint32_t scale;  // fp16 bits: scale, and offset above it
+};
+constexpr double kLimit4 = 4096.0;
+
+template <int LANES>
+__device__ __forceinline__ Codes4 codes4(double (&x)[8]) {
+  bool nan = false;
+  double lo = kLimit4, hi = -kLimit4;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    nan = nan || x[e] != x[e];
+    x[e] = x[e] > kLimit4 ? kLimit4 : x[e] < -kLimit4 ? -kLimit4 : x[e];
+    lo = x[e] < lo ? x[e] : lo;
+    hi = x[e] > hi ? x[e] : hi;
+  }
+  auto join = [&](double l, double h) {
+    lo = l < lo ? l : lo;
+    hi = h > hi ? h : hi;
+  };
+  join(xor_lane<1>(lo), xor_lane<1>(hi));
+  join(xor_lane<2>(lo), xor_lane<2>(hi));
+  join(xor_lane<4>(lo), xor_lane<4>(hi));
+  if constexpr (LANES == 16) join(xor_lane<8>(lo), xor_lane<8>(hi));
+  const int lane = threadIdx.x & 63;
+  const uint64_t group = ((uint64_t)1 << LANES) - 1;
+  Codes4 r{0u, 0x7e007e00u};
+  if ((__ballot(nan) >> (lane & ~(LANES - 1)) & group) != 0) return r;
+  const _Float16 sh = (_Float16)((hi - lo) / 15.0);
+  const double s = (double)sh;
+  const _Float16 oh = (_Float16)(lo - 64.0 * s);
+  const double o = (double)oh, inverse = 1.0 / s;
+  r.scale = (uint32_t)__builtin_bit_cast(uint16_t, sh) | (uint32_t)__builtin_bit_cast(uint16_t, oh) << 16;
+  if (!(s > 0.0)) return r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double t = x[e] - o;
+    double n = __builtin_rint(t * inverse);
+    // the product is a step of 2^-53 off at most: what it may get wrong is a
+    // quotient next to, or at, the middle between two codes
+    const double twice = 2.0 * __builtin_fma(-n, s, t);
+    const bool odd = ((int)n & 1) != 0;
+    if (twice > s || (twice == s && odd)) n += 1.0;
+    else if (twice < -s || (twice == -s && odd)) n -= 1.0;
+    const int code = (int)n - 64;
+    r.word |= (uint32_t)(code < 0 ? 0 : code > 15 ? 15 : code) << (8 * (e & 3) + (e & 4));
+  }
+  return r;
+}
+
+}  // namespace tb

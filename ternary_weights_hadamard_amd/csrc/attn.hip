@@ -9,7 +9,7 @@ namespace {
 // The first plan.chunk_blocks workgroups are for chunks, the others for few
 // rows.  Batches of one kind launch its kernel alone; both kinds together use
 // no more registers or LDS than the chunks do.
-template <int D, bool FP8, bool ROWS, bool CHUNK>
+template <int D, int C, bool ROWS, bool CHUNK>
 __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_attention_args a, AttnPlan plan) {
   constexpr int kBuffer = CHUNK ? kChunkPositions * D * 2 : kRowsTile * (D + 4) * 4;  // bytes
   static_assert(kBuffer >= kRowsTile * (D + 4) * 4, "both kinds share the buffers");
@@ -21,25 +21,25 @@ __global__ void __launch_bounds__(64 * kAttnWaves, 2) attn_kernel(tb_paged_atten
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (CHUNK && (!ROWS || block < plan.chunk_blocks)) {
     if constexpr (CHUNK)
-      run_line<true, FP8>(a, plan, block, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
-        return attn_chunk_part<D, FP8>(a, plan, it, t0, t1, slot, careful, sm);
+      run_line<true, C>(a, plan, block, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
+        return attn_chunk_part<D, C>(a, plan, it, t0, t1, slot, careful, sm);
       });
   } else if constexpr (ROWS) {
-    run_line<false, FP8>(a, plan, block - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
-      return attn_rows_part<D, FP8>(a, plan, it, t0, t1, slot, careful, sm);
+    run_line<false, C>(a, plan, block - plan.chunk_blocks, [&](const LineItem& it, int t0, int t1, int64_t slot, bool careful) {
+      return attn_rows_part<D, C>(a, plan, it, t0, t1, slot, careful, sm);
     });
   }
 }
 
 // The parts of row r's item: of a sequence of the kind, one head.
-template <bool CHUNK, bool FP8>
+template <bool CHUNK, int C>
 __device__ __forceinline__ LineParts parts_of_row(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b,
                                                   const LineSeq& seq, int head, int r) {
-  typedef LineKind<CHUNK, FP8> K;
+  typedef LineKind<CHUNK, C> K;
   const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
   const int rt = (unsigned)r / (unsigned)K::kRows;
   const int tiles = K::tiles(a, plan, seq, rt);
-  Line<CHUNK, FP8> line(a, plan);
+  Line<CHUNK, C> line(a, plan);
   int64_t start = line.before(a, plan, b);
   if constexpr (CHUNK) start += a.cache.heads_kv * K::tiles_before(a, plan, seq, rt);
   return line_parts(start + (int64_t)head * tiles, tiles, cut.piece(line.total));
@@ -51,10 +51,10 @@ __device__ __forceinline__ LineParts parts_of_row(const tb_paged_attention_args&
 // in turn, D / 16 channels a lane.  Bound by latency: the line again, a row's
 // statistics and its first parts (16 rows of 40 heads 6.1 us; 8 x 45 rows of 8
 // key/value heads in 8 parts each 8.4 us by whole waves, 14.5 us by 16 lanes).
-template <int D, bool CHUNK, bool FP8, int L>
+template <int D, bool CHUNK, int C, int L>
 __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const AttnPlan& plan, const LineParts& parts,
                                          const LineSeq& seq, int head, int r) {
-  constexpr int kRows = LineKind<CHUNK, FP8>::kRows, G = L / 16;
+  constexpr int kRows = LineKind<CHUNK, C>::kRows, G = L / 16;
   constexpr int DL = D / 16, kBatch = 4;  // parts whose loads a lane has in flight
   const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
   const int lane = threadIdx.x & (L - 1), g = lane >> 4, d0 = (lane & 15) * DL;
@@ -120,22 +120,22 @@ __device__ __forceinline__ void join_row(const tb_paged_attention_args& a, const
 }
 
 // ROWS (16, or 4 by whole waves) rows of one key/value head of one sequence.
-template <int D, bool FP8, int ROWS>
+template <int D, int C, int ROWS>
 __global__ void __launch_bounds__(256) attn_join_kernel(tb_paged_attention_args a, AttnPlan plan) {
   const unsigned heads = (unsigned)a.cache.heads_kv;
   const int head = blockIdx.x % heads, r0 = blockIdx.x / heads * ROWS;
   const int64_t b = blockIdx.z;
-  const LineSeq chunk = LineKind<true, FP8>::sequence(a, plan, b), few = LineKind<false, FP8>::sequence(a, plan, b);
+  const LineSeq chunk = LineKind<true, C>::sequence(a, plan, b), few = LineKind<false, C>::sequence(a, plan, b);
   if (plan.chunk_line.pieces && r0 < chunk.rows) {  // all of one row tile
-    const LineParts parts = parts_of_row<true, FP8>(a, plan, b, chunk, head, r0);
+    const LineParts parts = parts_of_row<true, C>(a, plan, b, chunk, head, r0);
     const int r = r0 + (int)(ROWS == 16 ? threadIdx.x >> 4 : uniform(threadIdx.x >> 6));
-    if (parts.count > 1 && r < chunk.rows) join_row<D, true, FP8, ROWS == 16 ? 16 : 64>(a, plan, parts, chunk, head, r);
+    if (parts.count > 1 && r < chunk.rows) join_row<D, true, C, ROWS == 16 ? 16 : 64>(a, plan, parts, chunk, head, r);
   }
   if (plan.rows_line.pieces && r0 < few.rows) {
-    const LineParts parts = parts_of_row<false, FP8>(a, plan, b, few, head, r0);
+    const LineParts parts = parts_of_row<false, C>(a, plan, b, few, head, r0);
     if (parts.count == 1) return;  // written by its kernel
     for (int r = r0 + uniform(threadIdx.x >> 6); r < r0 + ROWS && r < few.rows; r += 4)
-      join_row<D, false, FP8, 64>(a, plan, parts, few, head, r);
+      join_row<D, false, C, 64>(a, plan, parts, few, head, r);
   }
 }
 
@@ -174,7 +174,7 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   p.rows_line.slot_rows = kRowsTile;
   p.chunk_line.least = 4;
   p.chunk_line.slot_rows = kChunkTile;
-  if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype == TB_FP8)) p.rows_line.pieces = kPieces;
+  if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype)) p.rows_line.pieces = kPieces;
   // Chunks whose items fill the GPU are not cut: one after another, the row
   // tiles of a head find its keys and values in L2, while pieces of a line are
   // all elsewhere (4 x 2048 tokens over 8192, 40 heads, an earlier form of the
@@ -196,7 +196,7 @@ size_t value_bytes(const tb_paged_attention_args& a, const AttnLine& l) {
 }
 size_t stat_bytes(const AttnLine& l) { return 2 * (size_t)l.pieces * (size_t)l.slot_rows * sizeof(float2); }
 
-template <int D, bool FP8>
+template <int D, int C>
 hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stream) {
   const tb_paged_cache& c = a.cache;
   const bool chunk = has_chunk(a, p), rows = has_rows(a, p);
@@ -204,9 +204,9 @@ hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stre
   const int64_t few = !rows ? 0 : p.rows_line.pieces ? p.rows_line.pieces : c.B * c.heads_kv;
   const GridXY xy = grid_of(p.chunk_blocks + few);
   const dim3 grid(xy.x, xy.y), block(64 * kAttnWaves);
-  if (!chunk) hipLaunchKernelGGL((attn_kernel<D, FP8, true, false>), grid, block, 0, stream, a, p);
-  else if (!rows) hipLaunchKernelGGL((attn_kernel<D, FP8, false, true>), grid, block, 0, stream, a, p);
-  else hipLaunchKernelGGL((attn_kernel<D, FP8, true, true>), grid, block, 0, stream, a, p);
+  if (!chunk) hipLaunchKernelGGL((attn_kernel<D, C, true, false>), grid, block, 0, stream, a, p);
+  else if (!rows) hipLaunchKernelGGL((attn_kernel<D, C, false, true>), grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL((attn_kernel<D, C, true, true>), grid, block, 0, stream, a, p);
   const hipError_t e = hipGetLastError();
   const int64_t few_rows = !p.rows_line.pieces ? 0 : most_rows(a) < p.few ? most_rows(a) : p.few;
   const int64_t joined = p.chunk_line.pieces ? most_rows(a) : few_rows;
@@ -215,8 +215,8 @@ hipError_t launch(const tb_paged_attention_args& a, AttnPlan p, hipStream_t stre
   const bool many = p.chunk_line.pieces && chunk_items(a, p) > kPieces / 4;
   const int each = many ? 16 : 4;
   const dim3 join((unsigned)((joined + each - 1) / each * c.heads_kv), 1, (unsigned)c.B);
-  if (many) hipLaunchKernelGGL((attn_join_kernel<D, FP8, 16>), join, dim3(256), 0, stream, a, p);
-  else hipLaunchKernelGGL((attn_join_kernel<D, FP8, 4>), join, dim3(256), 0, stream, a, p);
+  if (many) hipLaunchKernelGGL((attn_join_kernel<D, C, 16>), join, dim3(256), 0, stream, a, p);
+  else hipLaunchKernelGGL((attn_join_kernel<D, C, 4>), join, dim3(256), 0, stream, a, p);
   return hipGetLastError();
 }
 
@@ -237,9 +237,12 @@ hipError_t launch_paged_attention(const tb_paged_attention_args& a, bool split, 
     l->stats = reinterpret_cast<float2*>(w);
     w += stat_bytes(*l);
   }
-  const bool f8 = a.cache.cache_dtype == TB_FP8;
-  if (a.cache.head_dim == 64) return f8 ? launch<64, true>(a, p, stream) : launch<64, false>(a, p, stream);
-  return f8 ? launch<128, true>(a, p, stream) : launch<128, false>(a, p, stream);
+  const bool wide = a.cache.head_dim == 128;
+  switch (a.cache.cache_dtype) {
+    case TB_FP8: return wide ? launch<128, TB_FP8>(a, p, stream) : launch<64, TB_FP8>(a, p, stream);
+    case TB_INT4: return wide ? launch<128, TB_INT4>(a, p, stream) : launch<64, TB_INT4>(a, p, stream);
+    default: return wide ? launch<128, TB_BF16>(a, p, stream) : launch<64, TB_BF16>(a, p, stream);
+  }
 }
 
 }  // namespace tb

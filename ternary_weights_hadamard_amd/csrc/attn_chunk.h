@@ -68,21 +68,27 @@ __device__ __forceinline__ void wait_loads() {
 // fp16 the two share its range: more slack is less room for small weights, less
 // is more rescaling (the windowed chunk above, measured together: 37.9 us with a
 // slack of 8, 38.5 with 4, 39.5 with 2).
-template <bool FP8>
+template <int C>
 struct ChunkOps;
 template <>
-struct ChunkOps<false> {  // weights have bf16's 8 bits: as two bf16 (few rows) there would be half as many products again
+struct ChunkOps<TB_BF16> {  // weights have bf16's 8 bits: as two bf16 (few rows) there would be half as many products again
   typedef uint16_t Elem;
   typedef bf16x8 V8;
+  typedef bf16x8 Q8;
   static constexpr int kRoom = 0, kSlack = 8;
   static __device__ __forceinline__ __bf16 narrow(float x) { return (__bf16)x; }
 };
 template <>
-struct ChunkOps<true> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
+struct ChunkOps<TB_FP8> {  // e4m3 values are widened to fp16 in LDS, and weights have its 11 bits
   typedef uint8_t Elem;
   typedef f16x8 V8;
+  typedef bf16x8 Q8;
   static constexpr int kRoom = 11, kSlack = 4;  // full precision down to 2^-25 of the largest weight
   static __device__ __forceinline__ _Float16 narrow(float x) { return (_Float16)x; }
+};
+template <>
+struct ChunkOps<TB_INT4> : ChunkOps<TB_FP8> {  // keys are fp16 in LDS too, and so are queries (QueryUnit)
+  typedef f16x8 Q8;
 };
 
 // 16-byte chunks of the two tiles in LDS.  Row r of K (a position) has D / 8 of
@@ -128,19 +134,19 @@ __device__ __forceinline__ int workgroup_bits(int x, int* of_wave) {
 // in v_lds and a barrier behind them.
 //   x0, there   the tile's first position, and which of its runs of 16 exist
 //   begin, end  the positions that some row sees
-template <int D, bool FP8, int ROWS>
+template <int D, int C, int ROWS>
 __device__ __forceinline__ void take_nonfinite_tile(u32x4* v_lds, const AttnShared& sm, bool& marked, int x0,
                                                     uint32_t there, int begin, int end, int first_pos, int group, int r0,
                                                     int nrows, int64_t window) {
   constexpr int kThreads = 64 * kAttnWaves, kChunks = kTile * D / 8;
-  typedef typename ChunkOps<FP8>::V8 V8;
+  typedef typename ChunkOps<C>::V8 V8;
   int tid = threadIdx.x;
   hold(tid);  // what follows from it is not kept for the next tile
   int bad = 0;  // 1: some value is not finite, 2: at a position that some row sees
 #pragma unroll 1
   for (int i = tid; i < kChunks; i += kThreads) {
     const u32x4 w = v_lds[i];
-    if (!(FP8 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w))) continue;
+    if (!(C != TB_BF16 ? any_nonfinite_f16(w) : any_nonfinite_bf16(w))) continue;
     const int row = i / (kTile / 8), x = x0 + (((i % (kTile / 8)) ^ ((row >> 1) & 7)) * 8);  // of the chunk: v_chunk
     bad |= x + 8 > begin && x < end ? 3 : 1;
   }
@@ -212,13 +218,15 @@ __device__ __forceinline__ LaneRow lane_row(int r, int nrows, int group, int hea
 // Tiles t_begin .. t_stop - 1 of an item: its output (slot < 0: they are all of
 // it), or a part of it into the workspace's slot.  True: nothing was written, it
 // is to be done again, `careful` (LDS is free for it).
-template <int D, bool FP8>
+template <int D, int C>
 __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a, const AttnPlan& plan,
                                                 const LineItem& it, int t_begin, int t_stop, int64_t slot, bool careful,
                                                 const AttnShared& sm) {
-  typedef ChunkOps<FP8> O;
+  typedef ChunkOps<C> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
+  typedef typename O::Q8 Q8;
+  constexpr bool INT4 = C == TB_INT4, FP8 = C != TB_BF16;  // FP8: through registers, widened on the way
   constexpr int KK = D / 16;   // steps of a score tile
   constexpr int DT = D / 32;   // 32-channel tiles of O'
   constexpr int kWaves = kAttnWaves, kRows = kChunkTile;
@@ -259,26 +267,42 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
 
   // scores are scaled by |scale|; its sign goes into the queries.  A scale of
   // 0 is taken as the smallest number, so that an unseen -inf stays one.
-  float scale2 = a.scale * kLog2e * (FP8 && c.k_scale ? c.k_scale[head] : 1.f);
+  float scale2 = a.scale * kLog2e * (C == TB_FP8 ? head_scale(c.k_scale, head) : 1.f);
   const uint32_t flip = scale2 < 0.f ? 0x80008000u : 0u;
-  scale2 = fmaxf(fabsf(scale2), 1.17549435e-38f);
-  bf16x8 q[KK];
+  scale2 = fabsf(scale2);
+  Q8 q[KK];
   {
     const uint16_t* qp =
         static_cast<const uint16_t*>(a.q) + (s.row0 + row.tok) * a.q_stride + (int64_t)row.hq * D + 8 * half;
+    u32x4 qw[KK];
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       u32x4 w = {0u, 0u, 0u, 0u};
       if (row_live) w = *reinterpret_cast<const u32x4*>(qp + 16 * kk);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] ^= flip;
-      q[kk] = __builtin_bit_cast(bf16x8, w);
+      qw[kk] = w;
+    }
+    if constexpr (INT4) {
+      float largest = 0.f, l0, l1;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) largest = QueryUnit::largest(qw[kk], largest);
+      swap_halves(largest, l0, l1);
+      const QueryUnit unit(fmaxf(l0, l1));
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) q[kk] = unit(qw[kk]);
+      scale2 = __builtin_amdgcn_ldexpf(scale2, -unit.shift);
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) q[kk] = __builtin_bit_cast(Q8, qw[kk]);
     }
   }
+  scale2 = fmaxf(scale2, 1.17549435e-38f);
 
   const int32_t* table = c.block_table + it.b * c.table_stride;
   const int shift = plan.shift;
-  const int64_t page_elems = (int64_t)c.page * D, page_step = (int64_t)c.heads_kv * page_elems;
+  constexpr int kRow = INT4 ? D / 2 : D;  // elements of a position
+  const int64_t page_elems = (int64_t)c.page * kRow, page_step = (int64_t)c.heads_kv * page_elems;
   const Elem* kc = static_cast<const Elem*>(c.k_cache) + head * page_elems;
   const Elem* vc = static_cast<const Elem*>(c.v_cache) + head * page_elems;
 
@@ -291,16 +315,19 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
   // run's page (-1: none, or nobody sees it; its entry is not read then), and
   // holder(g) is a lane that thereby holds run g's.  What a wave loads of K with one
   // instruction lies in one run.
-  constexpr int kPer = FP8 ? 16 : 8;                               // positions (or channels) of a 16-byte load
-  constexpr int kLoads = kTile * D / kPer / (64 * kWaves);         // loads of a lane, for K and for V
-  constexpr int kStep = FP8 ? 64 * kWaves / (D / 16) : 64 * kWaves / (D / 8);        // rows of K between them
+  // 4 bits: one load a lane, of D / 8 bytes: a quarter of a key's row, and 16
+  // positions (8 with 64 channels) of two channels.
+  constexpr int kPer = INT4 ? D / 8 : FP8 ? 16 : 8;                // positions (or elements of a key) of a load
+  constexpr int kLoads = kTile * kRow / kPer / (64 * kWaves);      // loads of a lane, for K and for V
+  constexpr int kKeys = kRow / kPer;                               // lanes of a key's row
+  constexpr int kStep = 64 * kWaves / kKeys;                       // rows of K between them
   constexpr int vStep = 64 * kWaves / (kTile / kPer);              // rows of V between them
   const int tid = wave * 64 + lane;
-  const int k_row = tid / (D / kPer), v_row = tid / (kTile / kPer);  // of the first load
-  const int k_ch = FP8 ? tid % (D / 16) : (tid % (D / 8)) ^ (k_row & (D / 8 - 1));
-  const int v_ch = FP8 ? tid % 4 : (tid % 8) ^ ((v_row >> 1) & 7);
-  const int v_run = FP8 ? v_ch : v_ch >> 1;
-  const uint32_t k_off = ((k_row & 15) * D + k_ch * kPer) * sizeof(Elem);  // bytes, inside a run
+  const int k_row = tid / kKeys, v_row = tid / (kTile / kPer);     // of the first load
+  const int k_ch = FP8 ? tid % kKeys : (tid % (D / 8)) ^ (k_row & (D / 8 - 1));
+  const int v_ch = FP8 ? tid % (kTile / kPer) : (tid % 8) ^ ((v_row >> 1) & 7);
+  const int v_run = kPer == 16 ? v_ch : v_ch >> 1;
+  const uint32_t k_off = ((k_row & 15) * kRow + k_ch * kPer) * sizeof(Elem);  // bytes, inside a run
   const int v_off = v_row * c.page + (v_ch * kPer & 15);
   // An entry as it is loaded: paged_id of it, and so the wait for it, is left
   // for when it is needed (with the check here, a wave stood 1100 of a tile's
@@ -311,21 +338,29 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
     if (t < t_end && (x | (c.page - 1)) >= span.begin && x < span.end) entry = paged_entry(table, c.table_width, x >> shift);
     return entry;
   };
-  auto holder = [&](int g) { return FP8 ? g : 2 * g ^ 4 * (wave & 1); };  // bf16: row v_row of lanes 0..7 is 8 wave
+  auto holder = [&](int g) { return INT4 && kPer == 8 ? 2 * g : FP8 ? g : 2 * g ^ 4 * (wave & 1); };  // bf16: row v_row of lanes 0..7 is 8 wave
   auto run_page = [&](int pages, int g) { return __builtin_amdgcn_readlane(pages, holder(g)); };
-  u32x4 kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
+  typedef __attribute__((ext_vector_type(INT4 ? D / 32 : 4))) uint32_t Load;
+  Load kr[FP8 ? kLoads : 1], vr[FP8 ? kLoads : 1];
+  uint32_t k_so;                                          // 4 bits: scale and offset of the key,
+  u32x4 v_scale[INT4 ? kPer / 8 : 1], v_offset[INT4 ? kPer / 8 : 1];  // and of the positions
   const int page_bytes = c.page * D * (int)sizeof(Elem);
   const int page_runs = c.page < kTile ? c.page / 16 : kTile / 16;  // runs of a tile that share a page
   const bool one_page = c.page >= kTile;                            // all of a tile's do
   auto page_of = [&](const Elem* cache, int page) { return cache + (page < 0 ? 0 : page) * page_step; };
   auto stage_k = [&](int t, int pages, u32x4* to) {
     const int x0 = (first_tile + t) * kTile;
+    if constexpr (INT4) {
+      const int run = uniform(k_row) >> 4, page = run_page(pages, run);
+      k_so = (static_cast<const uint32_t*>(c.k_scale) +
+              ((page < 0 ? 0 : page) * (int64_t)c.heads_kv + head) * c.page)[((x0 + 16 * run) & (c.page - 1)) + (k_row & 15)];
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int run = (i * kStep + uniform(k_row)) >> 4;
       const Elem* page = page_of(kc, run_page(pages, run));
-      const int at = ((x0 + 16 * run) & (c.page - 1)) * D * (int)sizeof(Elem);
-      if constexpr (FP8) kr[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(page) + at + k_off);
+      const int at = ((x0 + 16 * run) & (c.page - 1)) * kRow * (int)sizeof(Elem);
+      if constexpr (FP8) kr[i] = *reinterpret_cast<const Load*>(reinterpret_cast<const char*>(page) + at + k_off);
       else load_lds16(page, page_bytes, (int)k_off, at, &to[i * 64 * kWaves + wave * 64]);
     }
   };
@@ -335,7 +370,16 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
     if constexpr (FP8) {
       const Elem* vp = page_of(vc, pages) + at + v_off;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) vr[i] = *reinterpret_cast<const u32x4*>(vp + i * vStep * c.page);
+      for (int i = 0; i < kLoads; ++i) vr[i] = *reinterpret_cast<const Load*>(vp + i * vStep * c.page);
+      if constexpr (INT4) {
+        const uint16_t* so = static_cast<const uint16_t*>(c.v_scale) +
+                             ((pages < 0 ? 0 : pages) * (int64_t)c.heads_kv + head) * 2 * c.page + at + (v_ch * kPer & 15);
+#pragma unroll
+        for (int i = 0; i < kPer / 8; ++i) {
+          v_scale[i] = *reinterpret_cast<const u32x4*>(so + 8 * i);
+          v_offset[i] = *reinterpret_cast<const u32x4*>(so + c.page + 8 * i);
+        }
+      }
       return;
     }
     // A load is of one page: with several in a tile, of the lanes whose run lies in it.
@@ -368,9 +412,13 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
   auto load_v = [&](const Loads& x, int i, u32x4* to) {
     load_lds16(x.page, page_bytes, x.at, i * vStep * c.page * (int)sizeof(Elem), &to[i * 64 * kWaves + wave * 64]);
   };
-  // 8-bit: the staged registers into LDS
+  // 8-bit and 4-bit: the staged registers into LDS
   auto widen_k = [&](u32x4* to) {
-    if constexpr (FP8) {
+    if constexpr (INT4) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        to[k_chunk<D>(k_row, D / 32 * k_ch + i)] = __builtin_bit_cast(u32x4, channels4(kr[0][i], k_so));
+    } else if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         to[k_chunk<D>(i * kStep + k_row, 2 * k_ch)] = __builtin_bit_cast(u32x4, fp8_to_bf16(u32x2{kr[i][0], kr[i][1]}));
@@ -379,7 +427,16 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
     }
   };
   auto widen_v = [&](u32x4* to) {
-    if constexpr (FP8) {
+    if constexpr (INT4) {
+      const int ch = 8 * (v_row >> 2) + (v_row & 3);  // of the low codes; 4 more: of the high
+#pragma unroll
+      for (int i = 0; i < kPer / 8; ++i) {
+        const Nibbles a0 = nibbles(vr[0][2 * i]), a1 = nibbles(vr[0][2 * i + 1]);
+        to[v_chunk(ch, kPer / 8 * v_ch + i)] = __builtin_bit_cast(u32x4, positions4(a0.low, a1.low, v_scale[i], v_offset[i]));
+        to[v_chunk(ch + 4, kPer / 8 * v_ch + i)] =
+            __builtin_bit_cast(u32x4, positions4(a0.high, a1.high, v_scale[i], v_offset[i]));
+      }
+    } else if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         to[v_chunk(i * vStep + v_row, 2 * v_ch)] = __builtin_bit_cast(u32x4, fp8_to_f16(u32x2{vr[i][0], vr[i][1]}));
@@ -472,7 +529,7 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
       if (i + kAhead < kProducts) load(i + kAhead);
       if (i % 4 == 1) issue(i / 4);
       if (i < KK) {
-        next = mfma32(__builtin_bit_cast(bf16x8, operand[i]), q[i], next);
+        next = mfma32(__builtin_bit_cast(Q8, operand[i]), q[i], next);
 #pragma unroll
         for (int k = 0; k < kScores; ++k) {
           const int x = i * kScores + k;
@@ -519,7 +576,7 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
       for (int x = 0; x < 16; ++x) sc[0][x] = sc[1][x] = 0.f;
 #pragma unroll
       for (int i = 0; i < KK; ++i)
-        sc[0] = mfma32(__builtin_bit_cast(bf16x8, sm.buffer[0][k_chunk<D>(key, 2 * i + half)]), q[i], sc[0]);
+        sc[0] = mfma32(__builtin_bit_cast(Q8, sm.buffer[0][k_chunk<D>(key, 2 * i + half)]), q[i], sc[0]);
       top = sc[0][0];
 #pragma unroll
       for (int x = 1; x < 16; ++x) top = fmaxf(top, sc[0][x]);
@@ -548,7 +605,7 @@ __device__ __forceinline__ bool attn_chunk_part(const tb_paged_attention_args& a
     const int x0 = (first_tile + t) * kTile;
     const uint32_t there = runs_of(p0);
     if (!(there == 0xfu && x0 <= all_high && x0 > all_low))
-      take_nonfinite_tile<D, FP8, kRows>(v_lds, sm, marked, x0, there, span.begin, span.end, s.first_pos, group, r0, nrows,
+      take_nonfinite_tile<D, C, kRows>(v_lds, sm, marked, x0, there, span.begin, span.end, s.first_pos, group, r0, nrows,
                                          a.window);
     if (!idle) {
       beside(sc[0], sc[1], k_lds, 1, v_lds, 0, ahead_v);

@@ -37,7 +37,7 @@ constexpr int kAttnWaves = 4;    // waves of a workgroup
 constexpr int kRowsTile = 16;    // rows of a row tile: few rows,
 constexpr int kChunkTile = 128;  // and chunks
 // positions of a tile: few rows (the cache's type), and chunks
-__host__ __device__ constexpr int rows_positions(bool fp8) { return fp8 ? 64 : 32; }
+__host__ __device__ constexpr int rows_positions(int cache) { return cache == TB_BF16 ? 32 : 64; }
 constexpr int kChunkPositions = 64;
 
 // The tiles that hold a span's positions: first .. first + count - 1.
@@ -66,7 +66,7 @@ struct RowScale {
 __device__ __forceinline__ RowScale row_scale(const tb_paged_attention_args& a, int head, int64_t at, bool first,
                                               float top, float total) {
   const tb_paged_cache& c = a.cache;
-  const float vs = c.cache_dtype == TB_FP8 && c.v_scale ? c.v_scale[head] : 1.f;
+  const float vs = c.cache_dtype == TB_FP8 ? head_scale(c.v_scale, head) : 1.f;
   if (a.lse && first) a.lse[at] = total == 0.f ? -__builtin_inff() : (top + log2f(total)) * kLn2;
   return RowScale{total == 0.f ? 0.f : vs / total};
 }

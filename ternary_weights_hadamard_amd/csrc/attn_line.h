@@ -30,10 +30,10 @@ struct LineSeq {
   int rows;  // 0: it is of the other kind
 };
 
-template <bool CHUNK, bool FP8>
+template <bool CHUNK, int C>
 struct LineKind {
   static constexpr int kRows = CHUNK ? kChunkTile : kRowsTile;
-  static constexpr int kPositions = CHUNK ? kChunkPositions : rows_positions(FP8);
+  static constexpr int kPositions = CHUNK ? kChunkPositions : rows_positions(C);
 
   static __device__ __forceinline__ LineSeq sequence(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t b) {
     const tb_paged_cache& c = a.cache;
@@ -103,9 +103,9 @@ __device__ __forceinline__ LineItem uniform_item(const LineItem& x) {
 // The line of one kind.  Whole waves use it together, with the same arguments
 // in every lane, and all lanes active: the lanes take a sequence each, and for
 // one of many row tiles a row tile each.
-template <bool CHUNK, bool FP8>
+template <bool CHUNK, int C>
 struct Line {
-  typedef LineKind<CHUNK, FP8> K;
+  typedef LineKind<CHUNK, C> K;
   LineSeq own;    // of sequence b0 + lane, of the last 64 looked at
   int64_t up;     // tiles of the sequences b0 .. b0 + lane
   int64_t total;  // tiles of the line
@@ -241,10 +241,10 @@ __device__ __forceinline__ LineParts line_parts(int64_t start, int tiles, int64_
 // the last rows of a sequence see the most positions and go first.  Few rows: a
 // sequence has one for each head, and none if it is of the other kind.  Whole
 // waves, the same arguments in every lane.
-template <bool CHUNK, bool FP8>
+template <bool CHUNK, int C>
 __device__ __forceinline__ bool uncut_item(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t at,
                                            LineItem& it) {
-  typedef LineKind<CHUNK, FP8> K;
+  typedef LineKind<CHUNK, C> K;
   const int64_t heads = a.cache.heads_kv;
   it = LineItem{};
   int64_t t = at >> 32 == 0 ? (int64_t)((uint32_t)at / (uint32_t)heads) : at / heads;
@@ -290,7 +290,7 @@ __device__ __forceinline__ bool uncut_item(const tb_paged_attention_args& a, con
     it.seq = K::sequence(a, plan, t);
     if (it.seq.rows == 0) return false;
   }
-  Line<CHUNK, FP8>::set(a, plan, it);
+  Line<CHUNK, C>::set(a, plan, it);
   it = uniform_item(it);
   return true;
 }
@@ -299,14 +299,14 @@ __device__ __forceinline__ bool uncut_item(const tb_paged_attention_args& a, con
 // line is not cut, its item.  part(item, t0, t1, slot, careful) does tiles t0 ..
 // t1 - 1 of an item, all of them if slot < 0; if it answers true it is to be done
 // again, carefully.  LDS is free for it when it is called, and when it answers.
-template <bool CHUNK, bool FP8, typename F>
+template <bool CHUNK, int C, typename F>
 __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const AttnPlan& plan, int64_t block, F part) {
   const AttnLine& cut = CHUNK ? plan.chunk_line : plan.rows_line;
   bool careful = false;
   LineItem it;
   int64_t at, end;
   if (cut.pieces == 0) {
-    if (!uncut_item<CHUNK, FP8>(a, plan, block, it)) return;
+    if (!uncut_item<CHUNK, C>(a, plan, block, it)) return;
     if constexpr (CHUNK) {
       // a copy of its own: with what the loop over a piece's parts holds, the
       // chunk kernel runs out of scalar registers (4 x 2048 tokens 5 % slower)
@@ -318,7 +318,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     at = it.start = 0;
     end = it.tiles;
   } else {
-    Line<CHUNK, FP8> line(a, plan);
+    Line<CHUNK, C> line(a, plan);
     const int64_t per = cut.piece(line.total);
     at = uniform64(block * per);
     end = uniform64(at + per < line.total ? at + per : line.total);
@@ -334,7 +334,7 @@ __device__ __forceinline__ void run_line(const tb_paged_attention_args& a, const
     at = it.start + t1;
     if (at >= end) return;
     __syncthreads();  // the next part writes the LDS that this one reads
-    it = Line<CHUNK, FP8>::next(a, plan, it);
+    it = Line<CHUNK, C>::next(a, plan, it);
   }
 }
 

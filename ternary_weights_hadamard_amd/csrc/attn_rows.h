@@ -27,27 +27,96 @@
 #pragma once
 
 #include "attn_line.h"
+#include "cache4.h"
 
 namespace tb {
 
-template <bool FP8>
+template <int C>
 struct RowOps;
 
 template <>
-struct RowOps<false> {
+struct RowOps<TB_BF16> {
   typedef uint16_t Elem;
   static constexpr int kBlocks = 1;  // 32-position blocks per tile
   static constexpr int kRoom = 0;    // weights are at most 2^kRoom (weight_reference)
-  typedef bf16x8 V8;
+  typedef bf16x8 V8;                 // eight values, and eight channels of a query, in their product
+  typedef bf16x8 Q8;
 };
 
 template <>
-struct RowOps<true> {
+struct RowOps<TB_FP8> {
   typedef uint8_t Elem;
   static constexpr int kBlocks = 2;
   static constexpr int kRoom = 15;  // 2^16 is past fp16's largest
   typedef f16x8 V8;
+  typedef bf16x8 Q8;
 };
+
+template <>
+struct RowOps<TB_INT4> {
+  typedef uint8_t Elem;  // two codes
+  static constexpr int kBlocks = 2;
+  static constexpr int kRoom = 15;
+  typedef f16x8 V8;
+  typedef f16x8 Q8;
+};
+
+// A tile as a lane loads it.
+template <int D, int C>
+struct RowsTile {
+  static constexpr int NB = RowOps<C>::kBlocks, KL = D / 32 / NB;  // 16-byte loads of a key row
+  u32x4 k[2 * NB][KL], v[D / 16];
+  int page;  // of the values
+};
+template <int D>
+struct RowsTile<D, TB_INT4> {
+  typedef __attribute__((ext_vector_type(D / 32))) uint32_t Key;  // a quarter of a row's codes
+  Key k[4];
+  uint32_t k_so[4];            // scale, and offset above it, of each key
+  u32x4 v[D / 32];             // 16 positions of two channels: both of a byte
+  u32x4 v_scale[2], v_offset[2];
+  int page;
+};
+
+// Queries as fp16, in units of a power of two of the row: its largest channel
+// becomes 2^9 to 2^10, so that every channel down to 2^-24 of it is exact, and
+// one with an infinity or a NaN stays as it is.  `largest`: of the row's
+// magnitudes.  What scores are multiplied with is 2^-shift of what it was.
+struct QueryUnit {
+  int shift;
+  __device__ __forceinline__ explicit QueryUnit(float largest) {
+    shift = largest > 0.f && largest < __builtin_inff() ? 10 - __builtin_amdgcn_frexp_expf(largest) : 0;
+  }
+  __device__ __forceinline__ f16x8 operator()(const u32x4& w) const {
+    f16x8 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[2 * e] = (_Float16)__builtin_amdgcn_ldexpf(__uint_as_float(w[e] << 16), shift);
+      r[2 * e + 1] = (_Float16)__builtin_amdgcn_ldexpf(__uint_as_float(w[e] & 0xffff0000u), shift);
+    }
+    return r;
+  }
+  static __device__ __forceinline__ float largest(const u32x4& w, float m) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m = fmaxf(m, fabsf(__uint_as_float(w[e] << 16)));
+      m = fmaxf(m, fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+    }
+    return m;
+  }
+};
+
+// Any of 8 positions whose values may be infinite or NaN: its scale is 2^8 or
+// more, or its offset 2^15 (79 scales and an offset below these are below
+// 53000), or one of them is not finite.
+__device__ __forceinline__ bool any_large4(const u32x4& scales, const u32x4& offsets) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad = bad || (scales[i] & 0x7c00u) >= 0x5c00u || (scales[i] & 0x7c000000u) >= 0x5c000000u ||
+          (offsets[i] & 0x7c00u) >= 0x7800u || (offsets[i] & 0x7c000000u) >= 0x78000000u;
+  return bad;
+}
 
 __device__ __forceinline__ f32x4 mfma16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -59,17 +128,18 @@ __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f3
 // Tiles t0 .. t1 - 1 of an item: its output (slot < 0: they are all of it), or
 // a part of it into the workspace's slot.  True: nothing was written, it is to be
 // done again, `careful` (values that are not finite are taken out of every tile).
-template <int D, bool FP8>
+template <int D, int C>
 __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a, const AttnPlan& plan,
                                                const LineItem& it, int t0, int t1, int64_t slot, bool careful,
                                                const AttnShared& sm) {
-  typedef RowOps<FP8> O;
+  typedef RowOps<C> O;
   typedef typename O::Elem Elem;
   typedef typename O::V8 V8;
+  constexpr bool FP8 = C == TB_FP8, INT4 = C == TB_INT4;
   constexpr int NB = O::kBlocks;          // 32-position blocks of a tile
-  constexpr int T = rows_positions(FP8);  // positions of a tile
+  constexpr int T = rows_positions(C);    // positions of a tile
   constexpr int S = 2 * NB;               // 16-row score tiles of a tile
-  constexpr int KL = D / 32 / NB;         // 16-byte loads of a key row per lane
+  constexpr int KL = D / 32 / NB;         // 16-byte loads of a key row per lane (4 bits: half of one is the least)
   constexpr int DT = D / 16;              // 16-row tiles of O'
 
   const tb_paged_cache& c = a.cache;
@@ -83,9 +153,13 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
 
   const int32_t* table = c.block_table + it.b * c.table_stride;
   const int shift = plan.shift, page = c.page;
-  const int64_t page_step = (int64_t)c.heads_kv * page * D;
-  const Elem* kc = static_cast<const Elem*>(c.k_cache) + (int64_t)head * page * D;
-  const Elem* vc = static_cast<const Elem*>(c.v_cache) + (int64_t)head * page * D;
+  constexpr int kRow = INT4 ? D / 2 : D;  // elements of a position
+  const int64_t page_step = (int64_t)c.heads_kv * page * kRow;
+  const Elem* kc = static_cast<const Elem*>(c.k_cache) + (int64_t)head * page * kRow;
+  const Elem* vc = static_cast<const Elem*>(c.v_cache) + (int64_t)head * page * kRow;
+  // 4 bits: a position's scale and offset, 4 bytes in both
+  const uint32_t* k_so = static_cast<const uint32_t*>(c.k_scale) + (int64_t)head * page;
+  const uint32_t* v_so = static_cast<const uint32_t*>(c.v_scale) + (int64_t)head * page;
 
   // positions of the lane inside a tile: its key row (of score tile t, u):
   // krow + 8 t + 4 u, and its values: v0 .. v0 + 8 NB - 1
@@ -109,28 +183,41 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
     return Pages{entry_of(x0 + krow), entry_of(x0 + v0)};
   };
   auto checked = [&](const Pages& p) { return Pages{paged_id(p.k, c.n_pages), paged_id(p.v, c.n_pages)}; };
-  struct Tile {
-    u32x4 k[S][KL], v[DT];
-    int page;  // of the values
-  };
-  const int k_off = (krow & 15) * D + (16 / (int)sizeof(Elem)) * q4, v_off = i16 * page + (v0 & 15);
+  typedef RowsTile<D, C> Tile;
+  const int k_off = (krow & 15) * kRow + (INT4 ? D / 8 : 16 / (int)sizeof(Elem)) * q4, v_off = i16 * page + (v0 & 15);
   auto load_keys = [&](Tile& x, int t, const Pages& pg) {
     if (t >= t_end) return;
     const int slot = ((first_tile + t) * T + (krow & ~15)) & (page - 1);
-    const Elem* p = kc + (pg.k < 0 ? 0 : pg.k) * page_step + slot * D + k_off;
+    const Elem* p = kc + (pg.k < 0 ? 0 : pg.k) * page_step + slot * kRow + k_off;
+    if constexpr (INT4) {
+      const uint32_t* so = k_so + (pg.k < 0 ? 0 : pg.k) * ((int64_t)c.heads_kv * page) + slot + (krow & 15);
 #pragma unroll
-    for (int st = 0; st < S; ++st)
+      for (int st = 0; st < S; ++st) x.k_so[st] = so[4 * st];
 #pragma unroll
-      for (int kk = 0; kk < KL; ++kk)
-        x.k[st][kk] = *reinterpret_cast<const u32x4*>(p + (8 * (st >> 1) + 4 * (st & 1)) * D + 32 * NB * kk);
+      for (int st = 0; st < S; ++st) x.k[st] = *reinterpret_cast<const typename Tile::Key*>(p + 4 * st * kRow);
+    } else {
+#pragma unroll
+      for (int st = 0; st < S; ++st)
+#pragma unroll
+        for (int kk = 0; kk < KL; ++kk)
+          x.k[st][kk] = *reinterpret_cast<const u32x4*>(p + (8 * (st >> 1) + 4 * (st & 1)) * D + 32 * NB * kk);
+    }
   };
   auto load_values = [&](Tile& x, int t, const Pages& pg) {
     x.page = pg.v;
     if (t >= t_end) return;
     const int slot = ((first_tile + t) * T + (v0 & ~15)) & (page - 1);
     const Elem* p = vc + (pg.v < 0 ? 0 : pg.v) * page_step + slot + v_off;
+    if constexpr (INT4) {
+      const uint16_t* so = reinterpret_cast<const uint16_t*>(v_so + (pg.v < 0 ? 0 : pg.v) * ((int64_t)c.heads_kv * page)) + slot;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) x.v[dt] = *reinterpret_cast<const u32x4*>(p + 16 * dt * page);
+      for (int nb = 0; nb < NB; ++nb) {
+        x.v_scale[nb] = *reinterpret_cast<const u32x4*>(so + 8 * nb);
+        x.v_offset[nb] = *reinterpret_cast<const u32x4*>(so + page + 8 * nb);
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < (INT4 ? DT / 2 : DT); ++dt) x.v[dt] = *reinterpret_cast<const u32x4*>(p + 16 * dt * page);
   };
 
   int t = t0 + wave;
@@ -145,19 +232,31 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
   const int hq = head * group + (row_live ? r - tok * group : 0);
   const int pos = s.first_pos + tok;                                 // sees positions <= pos ..
   const int64_t low = a.window > 0 ? (int64_t)pos - a.window : -1;   // .. and > low
-  bf16x8 q[D / 32];
+  float scale2 = a.scale * kLog2e * (FP8 ? head_scale(c.k_scale, head) : 1.f);
+  typename O::Q8 q[D / 32];
   {
+    u32x4 qw[D / 32];
     const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (s.row0 + tok) * a.q_stride + (int64_t)hq * D;
 #pragma unroll
     for (int kk = 0; kk < D / 32; ++kk) {
       // the d that lane group q4 of this step multiplies, as the key loads give them
-      const int d = FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk % 2) : 32 * kk + 8 * q4;
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if (row_live) w = *reinterpret_cast<const u32x4*>(qp + d);
-      q[kk] = __builtin_bit_cast(bf16x8, w);
+      const int d = INT4 ? D / 4 * q4 + 8 * kk : FP8 ? 64 * (kk / 2) + 16 * q4 + 8 * (kk % 2) : 32 * kk + 8 * q4;
+      qw[kk] = u32x4{0u, 0u, 0u, 0u};
+      if (row_live) qw[kk] = *reinterpret_cast<const u32x4*>(qp + d);
+    }
+    if constexpr (INT4) {
+      float largest = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) largest = QueryUnit::largest(qw[kk], largest);
+      const QueryUnit unit(max_over_rows(largest));
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) q[kk] = unit(qw[kk]);
+      scale2 = __builtin_amdgcn_ldexpf(scale2, -unit.shift);
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) q[kk] = __builtin_bit_cast(bf16x8, qw[kk]);
     }
   }
-  const float scale2 = a.scale * kLog2e * (FP8 && c.k_scale ? c.k_scale[head] : 1.f);
 
   const Pages pa = checked(first);
   load_keys(ta, t, pa);
@@ -167,6 +266,21 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
   f32x4 o[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Values of 32-position block nb for the 16-row tile dt of O': 4 bits, row m
+  // of tiles 2 i and 2 i + 1 is both channels of the bytes of row 16 i + m.
+  auto value_of = [&](const Tile& x, int dt, int nb) -> V8 {
+    if constexpr (INT4) {
+      const u32x4& w = x.v[dt >> 1];
+      const Nibbles a0 = nibbles(w[2 * nb]), a1 = nibbles(w[2 * nb + 1]);
+      return dt & 1 ? positions4(a0.high, a1.high, x.v_scale[nb], x.v_offset[nb])
+                    : positions4(a0.low, a1.low, x.v_scale[nb], x.v_offset[nb]);
+    } else if constexpr (FP8) {
+      return fp8_to_f16(u32x2{x.v[dt][2 * nb], x.v[dt][2 * nb + 1]});
+    } else {
+      return __builtin_bit_cast(bf16x8, x.v[dt]);
+    }
+  };
 
   // Tile t, held in `x`, which is loaded again for the tile after the next.
   auto step = [&](Tile& x, int t) {
@@ -179,9 +293,15 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
     for (int st = 0; st < S; ++st) {
       sc[st] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (INT4) {
 #pragma unroll
-      for (int kk = 0; kk < KL; ++kk) {
-        if constexpr (FP8) {
+        for (int kk = 0; kk < D / 32; ++kk) sc[st] = mfma16(channels4(x.k[st][kk], x.k_so[st]), q[kk], sc[st]);
+        continue;
+      }
+#pragma unroll
+      for (int kk = 0; kk < (INT4 ? 0 : KL); ++kk) {
+        if constexpr (INT4) {
+        } else if constexpr (FP8) {
           const u32x4 w = x.k[st][kk];
           sc[st] = mfma16(fp8_to_bf16(u32x2{w[0], w[1]}), q[2 * kk], sc[st]);
           sc[st] = mfma16(fp8_to_bf16(u32x2{w[2], w[3]}), q[2 * kk + 1], sc[st]);
@@ -243,11 +363,17 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
       for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
     }
 
+    bool dropped = false;  // 4 bits: values that are not finite are replaced on their way
     if (!full) {
       bool bad = false;
+      if constexpr (INT4) {
+        bad = any_large4(x.v_scale[0], x.v_offset[0]) || any_large4(x.v_scale[1], x.v_offset[1]);
+      } else {
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) bad = bad || (FP8 ? any_nonfinite_fp8(x.v[dt]) : any_nonfinite_bf16(x.v[dt]));
+        for (int dt = 0; dt < DT; ++dt) bad = bad || (FP8 ? any_nonfinite_fp8(x.v[dt]) : any_nonfinite_bf16(x.v[dt]));
+      }
       if (__ballot(bad) != 0) {
+        dropped = INT4;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
           f32x4 up = {0.f, 0.f, 0.f, 0.f}, down = up;
@@ -256,12 +382,11 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
             V8 v, see;
 #pragma unroll
             for (int e = 0; e < 8; ++e) see[e] = (seen >> (8 * nb + e)) & 1u ? 1.f : 0.f;
-            if constexpr (FP8) v = fp8_to_f16(u32x2{x.v[dt][2 * nb], x.v[dt][2 * nb + 1]});
-            else v = __builtin_bit_cast(bf16x8, x.v[dt]);
+            v = value_of(x, dt, nb);
             const Nonfinite<V8> nf = take_nonfinite(v);
             up = mfma16(nf.up, see, up);
             down = mfma16(nf.down, see, down);
-            if constexpr (!FP8) x.v[dt] = __builtin_bit_cast(u32x4, v);
+            if constexpr (C == TB_BF16) x.v[dt] = __builtin_bit_cast(u32x4, v);
           }
           if constexpr (FP8) x.v[dt] = drop_nonfinite_fp8(x.v[dt]);
 #pragma unroll
@@ -273,14 +398,14 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       // Weights are rounded to 11 bits (fp16: every e4m3 value is exact in
-      // it) or, for bf16 values, given as the sum of two bf16 numbers (16
+      // it, and a 4-bit code stands for an fp16 number) or, for bf16 values, given as the sum of two bf16 numbers (16
       // bits): the matrix unit has room, and one bf16 would add an error as
       // large as the output's own rounding.
       V8 w, low_w;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float p = sc[2 * nb + (e >> 2)][e & 3];
-        if constexpr (FP8) {
+        if constexpr (C != TB_BF16) {
           w[e] = (_Float16)p;
         } else {
           w[e] = (__bf16)p;
@@ -289,13 +414,10 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
       }
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        if constexpr (FP8) {
-          o[dt] = mfma16(fp8_to_f16(u32x2{x.v[dt][2 * nb], x.v[dt][2 * nb + 1]}), w, o[dt]);
-        } else {
-          const bf16x8 v = __builtin_bit_cast(bf16x8, x.v[dt]);
-          o[dt] = mfma16(v, w, o[dt]);
-          o[dt] = mfma16(v, low_w, o[dt]);
-        }
+        V8 v = value_of(x, dt, nb);
+        if (INT4 && dropped) take_nonfinite(v);
+        o[dt] = mfma16(v, w, o[dt]);
+        if constexpr (C == TB_BF16) o[dt] = mfma16(v, low_w, o[dt]);
       }
     }
     load_values(x, t + kAttnWaves, now);
@@ -305,14 +427,14 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
     t += kAttnWaves;
   }
 
-  constexpr int kRow = D + 4;  // floats of a row in LDS
+  constexpr int kOutRow = D + 4;  // floats of a row in LDS
   // the waves' sums joined: each scales its values to the common maximum
   l = sum_over_rows(l);
   if (q4 == 0) {
     sm.max[wave * 16 + i16] = ref;
     sm.sum[wave * 16 + i16] = l;
   }
-  if constexpr (!FP8) {
+  if constexpr (C == TB_BF16) {
     bool bad = false;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) bad = bad || any_nonfinite(o[dt], 4);
@@ -320,7 +442,7 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
     sm.bits[wave] = !careful && __ballot(bad && row_live && fabsf(l) < __builtin_inff()) != 0 ? 1 : 0;
   }
   __syncthreads();
-  if constexpr (!FP8) {
+  if constexpr (C == TB_BF16) {
     int any = 0;
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) any |= sm.bits[w];
@@ -337,9 +459,9 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) {
       if (w != wave) continue;
-      f32x4* to = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(sm.buffer[w]) + i16 * kRow + 4 * q4);
+      f32x4* to = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(sm.buffer[w]) + i16 * kOutRow + (INT4 ? 8 : 4) * q4);
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) to[4 * dt] = o[dt] * f;
+      for (int dt = 0; dt < DT; ++dt) to[INT4 ? 8 * (dt >> 1) + (dt & 1) : 4 * dt] = o[dt] * f;
     }
   }
   __syncthreads();
@@ -358,7 +480,7 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
     total = fmaf(sm.sum[w * 16 + row], exp2_fast(sm.max[w * 16 + row] - base), total);
 #pragma unroll
     for (int e = 0; e < DL / 4; ++e)
-      v[e] += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(sm.buffer[w]) + row * kRow + d0 + 4 * e);
+      v[e] += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(sm.buffer[w]) + row * kOutRow + d0 + 4 * e);
   }
   if (slot >= 0) {
     const int64_t pr = slot * kRowsTile + row;

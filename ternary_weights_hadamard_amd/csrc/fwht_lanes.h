@@ -27,13 +27,23 @@ __device__ __forceinline__ void fwht_lane_round(float (&v)[8], int sub) {
   }
 }
 
-__device__ __forceinline__ void fwht128_lanes(float (&v)[8], int sub) {
+template <int MASK>
+__device__ __forceinline__ void fwht_lane_round(double (&v)[8], int sub) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double p = xor_lane<MASK>(v[e]);
+    v[e] = (sub & MASK) != 0 ? p - v[e] : p + v[e];
+  }
+}
+
+template <typename F>
+__device__ __forceinline__ void fwht128_lanes(F (&v)[8], int sub) {
 #pragma unroll
   for (int h = 1; h < 8; h <<= 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if ((e & h) == 0) {
-        const float a = v[e], c = v[e + h];
+        const F a = v[e], c = v[e + h];
         v[e] = a + c;
         v[e + h] = a - c;
       }

@@ -49,6 +49,11 @@ TB_HOST_DEVICE int paged_page(const int32_t* row, int64_t width, int64_t n_pages
   return paged_id(paged_entry(row, width, i), n_pages);
 }
 
+// What an e4m3 code of a head is multiplied with.
+TB_HOST_DEVICE float head_scale(const void* scales, int head) {
+  return scales ? static_cast<const float*>(scales)[head] : 1.f;
+}
+
 // The positions that some of the tokens j0 .. j1 (inclusive, j1 < n) see: [begin, end).
 struct PagedSpan {
   int begin, end;

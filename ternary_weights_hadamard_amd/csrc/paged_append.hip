@@ -10,8 +10,8 @@
 // Bound by the chain lengths - entry - load - convert - store, of which a chunk
 // has one round (4 x 128..2048 tokens of 8 heads to e4m3, 24.5 MB: 12.9 us, 1.9
 // TB/s) and a step little else (16 tokens of 8 heads: 5.8 us).
+#include "append_ops.h"
 #include "paged.h"
-#include "tb_common.h"
 #include "tb_launch.h"
 
 namespace tb {
@@ -20,35 +20,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;  // positions per workgroup
-
-// nearest e4m3 of x (ties to even), at most 448 in magnitude; NaN stays NaN
-__device__ __forceinline__ uint32_t fp8_pair(float a, float b) {
-  a = a > 448.f ? 448.f : a < -448.f ? -448.f : a;
-  b = b > 448.f ? 448.f : b < -448.f ? -448.f : b;
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xffffu;
-}
-
-// x / scale, correctly rounded, for a scale whose reciprocal and products stay
-// far from the ends of fp32: the rounded quotient by the reciprocal, corrected
-// by its remainder once (exact but for quotients that e4m3 rounds to 0).  3 operations in place of about 10 of
-// the general division.  Quotients past
-// 512 are cut there before the correction, so that none of it overflows; NaN
-// and infinities come through by the remainder.
-struct Quotient {
-  float scale, inverse;
-  bool plain;
-  __device__ explicit Quotient(float s) : scale(s), inverse(1.f / s) { plain = s >= 0x1p-60f && s <= 0x1p60f; }
-  __device__ float operator()(float x) const {
-    if (!plain) return x / scale;
-    const float q = __builtin_amdgcn_fmed3f(x * inverse, -512.f, 512.f);
-    return __builtin_fmaf(-__builtin_fmaf(q, scale, -x), inverse, q);  // signs so that -0 stays -0
-  }
-};
-
-// channels 2w and 2w + 1 of a row of bf16
-__device__ __forceinline__ float channel(const u32x4& w, int d) {
-  return d & 1 ? __uint_as_float(w[d >> 1] & 0xffff0000u) : bf16_to_f32(w[d >> 1] & 0xffffu);
-}
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) append_kernel(tb_paged_cache c, const uint16_t* __restrict__ k,
@@ -78,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(tb_paged_cache c, cons
   const int hi = end - tile0 < kTile ? (int)(end - tile0) : kTile;
   const int32_t* row = c.block_table + b * c.table_stride;
   const int shift = __builtin_ctz(c.page);
-  const Quotient ks(FP8 && c.k_scale ? c.k_scale[head] : 1.f), vs(FP8 && c.v_scale ? c.v_scale[head] : 1.f);
+  const Quotient ks(FP8 ? head_scale(c.k_scale, head) : 1.f), vs(FP8 ? head_scale(c.v_scale, head) : 1.f);
 
 #pragma unroll
   for (int i = threadIdx.x; i < kTile / kWord * (D / 8); i += kThreads) {

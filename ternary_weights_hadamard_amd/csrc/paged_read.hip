@@ -1,0 +1,162 @@
+// The paged cache's values, read back (include/tb.h, tb_paged_read).
+//
+// A workgroup takes 64 positions of one head.  Keys are rows as they are; values
+// lie by channel, so their codes go through LDS, whose rows are one word longer
+// than their positions: a wave's lanes, which read a column each, fall on
+// different banks.  Bound by HBM: the codes in, the values out.
+#include "cache4.h"
+#include "paged.h"
+#include "tb_launch.h"
+
+namespace tb {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;
+
+__device__ __forceinline__ float fp8_value(uint32_t w, int e) {
+  switch (e) {
+    case 0: return __builtin_amdgcn_cvt_f32_fp8((int)w, 0);
+    case 1: return __builtin_amdgcn_cvt_f32_fp8((int)w, 1);
+    case 2: return __builtin_amdgcn_cvt_f32_fp8((int)w, 2);
+    default: return __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
+  }
+}
+
+// eight channels from 8 g on to out[row][head][..]
+__device__ __forceinline__ void write8(void* out, int dtype, int64_t at, const float (&x)[8]) {
+  if (dtype == TB_F32) {
+    f32x4* to = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at);
+    to[0] = f32x4{x[0], x[1], x[2], x[3]};
+    to[1] = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(x[2 * i]) | f32_to_bf16_rne(x[2 * i + 1]) << 16;
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) = w;
+  }
+}
+
+template <int D, int C>
+__global__ void __launch_bounds__(kThreads) read_kernel(tb_paged_cache c, void* k_out, void* v_out, int dtype) {
+  constexpr int kRows = C == TB_INT4 ? D / 2 : D;           // of a page of V
+  constexpr int kElem = C == TB_BF16 ? 2 : 1;               // bytes
+  constexpr int kStride = kTile * kElem + 4;                // bytes of a row in LDS
+  constexpr int kPiece = 16 / kElem, kPieces = kTile / kPiece;
+  constexpr int G = D / 8;
+  __shared__ uint32_t tile[kRows * kStride / 4];
+
+  const int64_t b = blockIdx.z;
+  const int head = blockIdx.y;
+  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, c.table_width * c.page);
+  const int n = s.n < c.max_q ? s.n : (int)c.max_q;
+  const int begin = s.first_pos > 0 ? s.first_pos : 0;
+  const int64_t top = (int64_t)s.first_pos + n;
+  const int end = top < s.keys ? (int)(top < 0 ? 0 : top) : s.keys;
+  const int64_t tile0 = (int64_t)(begin / kTile + (int64_t)blockIdx.x) * kTile;
+  if (tile0 >= end) return;
+  const int lo = begin > tile0 ? begin - (int)tile0 : 0;
+  const int hi = end - tile0 < kTile ? (int)(end - tile0) : kTile;
+  const int32_t* row = c.block_table + b * c.table_stride;
+  const int shift = __builtin_ctz(c.page), mask = c.page - 1;
+  // first element of head's page, in positions
+  auto page_at = [&](int x) -> int64_t {
+    const int page = paged_page(row, c.table_width, c.n_pages, (tile0 + x) >> shift);
+    return page < 0 ? -1 : ((int64_t)page * c.heads_kv + head) * c.page;
+  };
+  const float ks = C == TB_FP8 ? head_scale(c.k_scale, head) : 1.f, vs = C == TB_FP8 ? head_scale(c.v_scale, head) : 1.f;
+  const uint8_t* kc = static_cast<const uint8_t*>(c.k_cache);
+  const uint8_t* vc = static_cast<const uint8_t*>(c.v_cache);
+
+  if (v_out) {
+#pragma unroll
+    for (int i = threadIdx.x; i < kRows * kPieces; i += kThreads) {
+      const int r = i / kPieces, x = i % kPieces * kPiece;
+      if (x + kPiece <= lo || x >= hi) continue;
+      const int64_t at = page_at(x);
+      if (at < 0) continue;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(vc + (at * kRows + (int64_t)r * c.page + ((tile0 + x) & mask)) * kElem);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[(r * kStride + x * kElem) / 4 + e] = w[e];
+    }
+  }
+  if (k_out) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTile * G; i += kThreads) {
+      const int x = i / G, g = i % G;
+      if (x < lo || x >= hi) continue;
+      const int64_t page = page_at(x);
+      if (page < 0) continue;
+      const int64_t at = page + ((tile0 + x) & mask);
+      float f[8];
+      if constexpr (C == TB_BF16) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(kc + (at * D + 8 * g) * 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+      } else if constexpr (C == TB_FP8) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(kc + at * D + 8 * g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fp8_value(w[e >> 2], e & 3) * ks;
+      } else {
+        const f16x8 v = channels4(*reinterpret_cast<const uint32_t*>(kc + at * (D / 2) + 4 * g),
+                                  static_cast<const uint32_t*>(c.k_scale)[at]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+      }
+      write8(k_out, dtype, ((s.row0 + (tile0 + x - s.first_pos)) * c.heads_kv + head) * D + 8 * g, f);
+    }
+  }
+  if (!v_out) return;
+  __syncthreads();
+  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(tile);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kTile * G; i += kThreads) {
+    const int x = i / G, g = i % G;
+    if (x < lo || x >= hi) continue;
+    const int64_t page = page_at(x);
+    if (page < 0) continue;
+    float f[8];
+    if constexpr (C == TB_INT4) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w |= (uint32_t)bytes[(4 * g + e) * kStride + x] << (8 * e);
+      const uint16_t* so = static_cast<const uint16_t*>(c.v_scale) + page * 2 + ((tile0 + x) & mask);
+      const f16x8 v = channels4(w, so[0] | (uint32_t)so[c.page] << 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* at = bytes + (8 * g + e) * kStride + x * kElem;
+        if constexpr (C == TB_BF16) f[e] = bf16_to_f32(*reinterpret_cast<const uint16_t*>(at));
+        else f[e] = fp8_value(*at, 0) * vs;
+      }
+    }
+    write8(v_out, dtype, ((s.row0 + (tile0 + x - s.first_pos)) * c.heads_kv + head) * D + 8 * g, f);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_paged_read(const tb_paged_cache& c, void* k_out, void* v_out, int out_dtype, hipStream_t stream) {
+  // positions that do not start on a tile reach into one more
+  const dim3 grid((unsigned)((c.max_q + kTile - 1) / kTile + 1), (unsigned)c.heads_kv, (unsigned)c.B), block(kThreads);
+  const bool wide = c.head_dim == 128;
+  switch (c.cache_dtype) {
+    case TB_BF16:
+      if (wide) hipLaunchKernelGGL((read_kernel<128, TB_BF16>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+      else hipLaunchKernelGGL((read_kernel<64, TB_BF16>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+      break;
+    case TB_FP8:
+      if (wide) hipLaunchKernelGGL((read_kernel<128, TB_FP8>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+      else hipLaunchKernelGGL((read_kernel<64, TB_FP8>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+      break;
+    default:
+      if (wide) hipLaunchKernelGGL((read_kernel<128, TB_INT4>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+      else hipLaunchKernelGGL((read_kernel<64, TB_INT4>), grid, block, 0, stream, c, k_out, v_out, out_dtype);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace tb

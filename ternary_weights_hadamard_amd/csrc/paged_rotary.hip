@@ -1,0 +1,447 @@
+// Rotary positions on the way into the paged cache, and the 4-bit cache's
+// append (include/tb.h, tb_paged_append_rotary, tb_paged_append).
+//
+// A group of D / 8 lanes holds one head of one token, 8 channels a lane, so that
+// the 128-point transforms and the 4-bit statistics are exchanges between lanes
+// and a pair of channels is in one lane or in two of the group.  The workgroups
+// of a sequence are of three kinds, side by side in one launch:
+//   queries   kTokens tokens of some heads; a group keeps its token, so a lane's
+//             cosines and sines are found once
+//   keys      the same, of all heads
+//   values    64 positions of one head, turned in LDS: pages hold [d][position]
+// With few tokens a sequence (at most kFew) a group has one head, and values are
+// stored as they come, a code at a time: no turn through LDS, no barrier.
+#include "append_ops.h"
+#include "fwht_lanes.h"
+#include "paged.h"
+#include "tb_launch.h"
+
+namespace tb {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;      // positions of a workgroup of values
+constexpr int kTokens = 16;    // tokens of a workgroup of queries or keys, for chunks
+constexpr int kFew = 16;       // tokens a sequence up to which each group has one head
+constexpr int kRatio = kTile / kTokens;
+
+// cosine and sine of x
+struct Angle {
+  double c, s;
+};
+
+// Of position * f radians.  The turns are formed to 2^-104 of their size and
+// reduced to an eighth; there the Taylor series to x^15 and x^16 are off by less
+// than 2^-53.
+__device__ __forceinline__ Angle angle_of(double position, float f) {
+  constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double p = position * (double)f;  // 31 + 24 bits: exact below 2^29
+  const double turns = p * kHigh;
+  const double r = (turns - __builtin_rint(turns)) + __builtin_fma(p, kLow, __builtin_fma(p, kHigh, -turns));
+  const double quarter = __builtin_rint(4.0 * r);
+  const double x = __builtin_fma(-0.25, quarter, r) * kTwoPi, y = x * x;
+  double s = -1.0 / 1307674368000.0, c = 1.0 / 20922789888000.0;
+  s = __builtin_fma(s, y, 1.0 / 6227020800.0);
+  s = __builtin_fma(s, y, -1.0 / 39916800.0);
+  s = __builtin_fma(s, y, 1.0 / 362880.0);
+  s = __builtin_fma(s, y, -1.0 / 5040.0);
+  s = __builtin_fma(s, y, 1.0 / 120.0);
+  s = __builtin_fma(s, y, -1.0 / 6.0);
+  s = __builtin_fma(s * y, x, x);
+  c = __builtin_fma(c, y, -1.0 / 87178291200.0);
+  c = __builtin_fma(c, y, 1.0 / 479001600.0);
+  c = __builtin_fma(c, y, -1.0 / 3628800.0);
+  c = __builtin_fma(c, y, 1.0 / 40320.0);
+  c = __builtin_fma(c, y, -1.0 / 720.0);
+  c = __builtin_fma(c, y, 1.0 / 24.0);
+  c = __builtin_fma(c, y, -0.5);
+  c = __builtin_fma(c, y, 1.0);
+  const int q = (int)quarter & 3;
+  Angle a{q & 1 ? s : c, q & 1 ? c : s};
+  if (q == 1 || q == 2) a.c = -a.c;
+  if (q >= 2) a.s = -a.s;
+  return a;
+}
+
+__device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
+
+// A lane's eight channels, rotated by a position: x -> x c + (its partner) s.
+template <typename F, int D>
+struct Rotation {
+  F c[8], s[8];
+  bool live;  // the lane's channels are among the first rotary_dim
+  int from;   // lane of the partners (neighbours: its own)
+
+  __device__ __forceinline__ Rotation(const tb_paged_rotary_args& a, int sub, int64_t position) {
+    const int d0 = 8 * sub, half = a.rotary_dim / 2;
+    live = d0 < a.rotary_dim;
+    const bool second = !a.neighbours && d0 >= half;
+    from = !live || a.neighbours ? 0 : second ? -half / 8 : half / 8;
+    if (!live) return;
+    if (a.neighbours) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const Angle x = angle_of((double)position, a.inv_freq[(d0 + e) / 2]);
+        c[e] = c[e + 1] = (F)(x.c * (double)a.factor);
+        s[e + 1] = (F)(x.s * (double)a.factor);
+        s[e] = -s[e + 1];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Angle x = angle_of((double)position, a.inv_freq[d0 - (second ? half : 0) + e]);
+        c[e] = (F)(x.c * (double)a.factor);
+        s[e] = (F)((second ? x.s : -x.s) * (double)a.factor);
+      }
+    }
+  }
+  // all lanes of the group together
+  __device__ __forceinline__ void operator()(const tb_paged_rotary_args& a, F (&x)[8]) const {
+    if (a.rotary_dim == 0) return;
+    F other[8];
+    if (a.neighbours) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = x[e ^ 1];
+    } else {
+      const int lane = (threadIdx.x & 63) + from;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = __shfl(x[e], lane);
+    }
+    if (!live) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fused(x[e], c[e], other[e] * s[e]);
+  }
+};
+
+template <typename F>
+__device__ __forceinline__ void turn(F (&x)[8], int sub) {
+  fwht128_lanes(x, sub);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= (F)0x1.6a09e667f3bcdp-4;
+}
+
+template <typename F>
+__device__ __forceinline__ void unpack(const u32x4& w, F (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = (F)channel(w, e);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return f32_to_bf16_rne(a) | f32_to_bf16_rne(b) << 16;
+}
+
+// What a cache's codes are made from, and how: 8 channels a lane.
+template <int C>
+struct Made {
+  typedef double F;
+  typedef uint8_t Elem;
+};
+template <>
+struct Made<TB_BF16> {
+  typedef float F;
+  typedef uint16_t Elem;
+};
+
+struct Place {
+  int page, slot;  // page < 0: there is none
+};
+__device__ __forceinline__ Place place_of(const tb_paged_cache& c, int64_t b, const PagedSeq& s, int pos) {
+  Place p{-1, 0};
+  if (pos < 0 || pos >= s.keys) return p;
+  p.page = paged_page(c.block_table + b * c.table_stride, c.table_width, c.n_pages, pos / c.page);
+  p.slot = pos & (c.page - 1);
+  return p;
+}
+
+// 8 channels, from d0 = 8 * sub on, as the codes of the cache: words of bf16, or
+// of e4m3, or one of 4-bit codes; its scale and offset for those.
+template <int C, int D>
+struct Codes {
+  uint32_t w[C == TB_BF16 ? 4 : C == TB_FP8 ? 2 : 1];
+  uint32_t scale;
+  __device__ __forceinline__ Codes(typename Made<C>::F (&x)[8], double inverse) {
+    if constexpr (C == TB_BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+    } else if constexpr (C == TB_FP8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[i] = fp8_pair((float)(x[4 * i] * inverse), (float)(x[4 * i + 1] * inverse)) |
+               fp8_pair((float)(x[4 * i + 2] * inverse), (float)(x[4 * i + 3] * inverse)) << 16;
+    } else {
+      const Codes4 r = codes4<D / 8>(x);
+      w[0] = r.word;
+      scale = r.scale;
+    }
+  }
+};
+
+// one head's page of K: bytes, and the words of its scales
+template <int C, int D>
+__device__ __forceinline__ void store_key(const tb_paged_cache& c, const Place& at, int head, int sub, const Codes<C, D>& k) {
+  if (at.page < 0) return;
+  const int64_t row = ((int64_t)at.page * c.heads_kv + head) * c.page + at.slot;
+  if constexpr (C == TB_BF16) {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(const_cast<void*>(c.k_cache)) + row * D + 8 * sub) =
+        u32x4{k.w[0], k.w[1], k.w[2], k.w[3]};
+  } else if constexpr (C == TB_FP8) {
+    *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(const_cast<void*>(c.k_cache)) + row * D + 8 * sub) =
+        u32x2{k.w[0], k.w[1]};
+  } else {
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(const_cast<void*>(c.k_cache)) + row * (D / 2) + 4 * sub) = k.w[0];
+    if (sub == 0) static_cast<uint32_t*>(const_cast<void*>(c.k_scale))[row] = k.scale;
+  }
+}
+
+__device__ __forceinline__ void store_scale(const tb_paged_cache& c, const Place& at, int head, uint32_t scale) {
+  uint16_t* to = static_cast<uint16_t*>(const_cast<void*>(c.v_scale)) + ((int64_t)at.page * c.heads_kv + head) * 2 * c.page + at.slot;
+  to[0] = (uint16_t)scale;
+  to[c.page] = (uint16_t)(scale >> 16);
+}
+
+// one position's values, a code at a time
+template <int C, int D>
+__device__ __forceinline__ void store_value(const tb_paged_cache& c, const Place& at, int head, int sub, const Codes<C, D>& v) {
+  if (at.page < 0) return;
+  typedef typename Made<C>::Elem Elem;
+  constexpr int kRows = C == TB_INT4 ? D / 2 : D, kMine = kRows / (D / 8), kPer = 4 / sizeof(Elem);
+  Elem* to = static_cast<Elem*>(const_cast<void*>(c.v_cache)) +
+             (((int64_t)at.page * c.heads_kv + head) * kRows + sub * kMine) * c.page + at.slot;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) to[i * c.page] = (Elem)(v.w[i / kPer] >> (32 / kPer * (i % kPer)));
+  if (C == TB_INT4 && sub == 0) store_scale(c, at, head, v.scale);
+}
+
+struct Cut {
+  int tokens;       // of a workgroup of queries or keys
+  int q_heads;      // of a workgroup of queries, and
+  int q_groups;     // how many of these there are for a token tile
+  int kv_groups;    // workgroups of keys (few tokens: of keys and values)
+  int kv_heads;     // heads of one
+};
+
+// Queries: group g has token g % tokens of the tile and every (groups / tokens)-th head.
+template <int D>
+__device__ __forceinline__ void run_queries(const tb_paged_rotary_args& a, const Cut& cut, const PagedSeq& s, int n,
+                                            int tile, int part) {
+  constexpr int kLanes = D / 8, kAhead = 4;
+  const int group = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+  const int tok = tile * cut.tokens + group % cut.tokens, step = kThreads / kLanes / cut.tokens;
+  int h = part * cut.q_heads + group / cut.tokens;
+  const int end = min((part + 1) * cut.q_heads, a.heads_q);
+  if (tok >= n) return;
+  const uint16_t* from = static_cast<const uint16_t*>(a.q) + (s.row0 + tok) * a.q_stride + 8 * sub;
+  uint16_t* to = static_cast<uint16_t*>(a.q_out) + (s.row0 + tok) * a.heads_q * D + 8 * sub;
+  u32x4 w[kAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (h0 + u * step < end) w[u] = *reinterpret_cast<const u32x4*>(from + (int64_t)(h0 + u * step) * D);
+  };
+  load(h);
+  const Rotation<float, D> rotate(a, sub, (int64_t)s.first_pos + tok);
+  for (; h < end; h += kAhead * step) {
+    float x[kAhead][8];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) unpack(w[u], x[u]);
+    load(h + kAhead * step);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (h + u * step >= end) continue;
+      if (D == 128 && a.turn_in) turn(x[u], sub);
+      rotate(a, x[u]);
+      if (D == 128 && a.turn_out) turn(x[u], sub);
+      *reinterpret_cast<u32x4*>(to + (int64_t)(h + u * step) * D) =
+          u32x4{bf16_pair(x[u][0], x[u][1]), bf16_pair(x[u][2], x[u][3]), bf16_pair(x[u][4], x[u][5]),
+                bf16_pair(x[u][6], x[u][7])};
+    }
+  }
+}
+
+// Keys, and with few tokens values (heads heads_kv .. 2 heads_kv - 1).
+template <int D, int C, bool FEW>
+__device__ __forceinline__ void run_keys(const tb_paged_rotary_args& a, const Cut& cut, int64_t b, const PagedSeq& s, int n,
+                                         int tile, int part) {
+  typedef typename Made<C>::F F;
+  constexpr int kLanes = D / 8;
+  const tb_paged_cache& c = a.cache;
+  const int group = threadIdx.x / kLanes, sub = threadIdx.x % kLanes;
+  const int tok = tile * cut.tokens + group % cut.tokens, step = kThreads / kLanes / cut.tokens;
+  int h = part * cut.kv_heads + group / cut.tokens;
+  const int end = min((part + 1) * cut.kv_heads, FEW ? 2 * c.heads_kv : c.heads_kv);
+  if (tok >= n || h >= end) return;
+  const int pos = s.first_pos + tok;
+  const Place at = place_of(c, b, s, pos);
+  const uint16_t* k = static_cast<const uint16_t*>(a.k) + (s.row0 + tok) * a.k_stride + 8 * sub;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (s.row0 + tok) * a.v_stride + 8 * sub;
+  auto load = [&](int h) {
+    return *reinterpret_cast<const u32x4*>(!FEW || h < c.heads_kv ? k + (int64_t)h * D : v + (int64_t)(h - c.heads_kv) * D);
+  };
+  u32x4 w = load(h);
+  const Rotation<F, D> rotate(a, sub, (int64_t)pos);
+  for (; h < end; h += step) {
+    F x[8];
+    unpack(w, x);
+    if (h + step < end) w = load(h + step);
+    const bool value = FEW && h >= c.heads_kv;
+    const int head = value ? h - c.heads_kv : h;
+    if (D == 128 && (value ? a.turn_v : a.turn_in)) turn(x, sub);
+    if (!value) {
+      rotate(a, x);
+      if (D == 128 && a.turn_out) turn(x, sub);
+    }
+    const double inverse = C == TB_FP8 ? 1.0 / (double)head_scale(value ? c.v_scale : c.k_scale, head) : 1.0;
+    const Codes<C, D> codes(x, inverse);
+    if (value) store_value<C, D>(c, at, head, sub, codes);
+    else store_key<C, D>(c, at, head, sub, codes);
+  }
+}
+
+// Values of 64 positions of a head: a group has 4 positions, whose codes it
+// turns by words into LDS; from there each row's run of positions is written in
+// 16-byte pieces where all of a piece is new.
+template <int D, int C>
+__device__ __forceinline__ void run_values(const tb_paged_rotary_args& a, int64_t b, const PagedSeq& s, int n, int vt,
+                                           int head) {
+  typedef typename Made<C>::F F;
+  typedef typename Made<C>::Elem Elem;
+  constexpr int kLanes = D / 8, kRows = C == TB_INT4 ? D / 2 : D, kMine = kRows / kLanes;  // rows of a lane
+  constexpr int kPiece = 16 / sizeof(Elem), kPieces = kTile / kPiece;
+  constexpr int kWords = kTile * sizeof(Elem) / 4 + 4;  // of a row in LDS
+  constexpr int kPer = 4 / sizeof(Elem);                // positions of a word
+  __shared__ __align__(16) uint32_t tile[kRows * kWords];
+  auto place = [](int row, int piece) { return row * kWords + 4 * (piece ^ ((row / kMine) >> 1 & (kPieces - 1))); };
+
+  const tb_paged_cache& c = a.cache;
+  const int begin = s.first_pos > 0 ? s.first_pos : 0;
+  const int64_t top = (int64_t)s.first_pos + n;
+  const int end = top < s.keys ? (int)(top < 0 ? 0 : top) : s.keys;
+  const int64_t tile0 = ((int64_t)(begin / kTile) + vt) * kTile;
+  if (tile0 >= end) return;
+  const int lo = begin > tile0 ? begin - (int)tile0 : 0;
+  const int hi = end - tile0 < kTile ? (int)(end - tile0) : kTile;
+
+  const int group = threadIdx.x / kLanes, sub = threadIdx.x % kLanes, x0 = 4 * group;
+  if (x0 < kTile && x0 + 4 > lo && x0 < hi) {
+    const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)head * D + 8 * sub;
+    u32x4 w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] = u32x4{0u, 0u, 0u, 0u};
+      if (x0 + e >= lo && x0 + e < hi)
+        w[e] = *reinterpret_cast<const u32x4*>(v + (s.row0 + (tile0 + x0 + e - s.first_pos)) * a.v_stride);
+    }
+    const Place at = place_of(c, b, s, (int)tile0 + x0);  // all four are in its page
+    const double inverse = C == TB_FP8 ? 1.0 / (double)head_scale(c.v_scale, head) : 1.0;
+    uint32_t codes[4][C == TB_BF16 ? 4 : C == TB_FP8 ? 2 : 1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      F x[8];
+      unpack(w[e], x);
+      if (D == 128 && a.turn_v) turn(x, sub);
+      const Codes<C, D> made(x, inverse);
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(made.w) / 4); ++i) codes[e][i] = made.w[i];
+      if (C == TB_INT4 && sub == e && at.page >= 0 && x0 + e >= lo && x0 + e < hi)
+        store_scale(c, Place{at.page, at.slot + e}, head, made.scale);
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+      for (int h = 0; h < 4 / kPer; ++h) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          word |= (codes[kPer * h + e][i / kPer] >> (32 / kPer * (i % kPer)) & (kPer == 4 ? 0xffu : 0xffffu)) << (32 / kPer * e);
+        tile[place(sub * kMine + i, x0 / kPiece) + x0 % kPiece / kPer + h] = word;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = threadIdx.x; i < kRows * kPieces; i += kThreads) {
+    const int row = i / kPieces, piece = i % kPieces, p0 = piece * kPiece;
+    if (p0 + kPiece <= lo || p0 >= hi) continue;
+    const int first = p0 > lo ? p0 : lo;  // a piece lies in one page
+    const Place at = place_of(c, b, s, (int)tile0 + first);
+    if (at.page < 0) continue;
+    Elem* to = static_cast<Elem*>(const_cast<void*>(c.v_cache)) +
+               (((int64_t)at.page * c.heads_kv + head) * kRows + row) * c.page + (at.slot & ~(kPiece - 1));
+    const uint32_t* from = tile + place(row, piece);
+    if (p0 >= lo && p0 + kPiece <= hi) {
+      *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(from);
+    } else {
+      for (int e = 0; e < kPiece; ++e)
+        if (p0 + e >= lo && p0 + e < hi) to[e] = reinterpret_cast<const Elem*>(from)[e];
+    }
+  }
+}
+
+template <int D, int C, bool FEW>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(tb_paged_rotary_args a, Cut cut) {
+  const tb_paged_cache& c = a.cache;
+  const int64_t b = blockIdx.z;
+  const PagedSeq s = paged_seq(c.cu_q, c.kv_len, b, c.total_q, c.table_width * c.page);
+  const int n = s.n < c.max_q ? s.n : (int)c.max_q;
+  const int x = blockIdx.x;
+  int y = blockIdx.y;
+  if ((int64_t)x * (FEW ? 1 : kTokens) >= n + (FEW ? 0 : 2 * kTile)) return;  // values reach into one more tile
+  if (y < cut.q_groups) {
+    run_queries<D>(a, cut, s, n, x, y);
+    return;
+  }
+  y -= cut.q_groups;
+  if (FEW || y < cut.kv_groups) {
+    run_keys<D, C, FEW>(a, cut, b, s, n, x, y);
+    return;
+  }
+  if constexpr (!FEW) {
+    const int head = kRatio * (y - cut.kv_groups) + x % kRatio;
+    if (head < c.heads_kv) run_values<D, C>(a, b, s, n, x / kRatio, head);
+  }
+}
+
+int at_least(int64_t want, int most) { return want < 1 ? 1 : want > most ? most : (int)want; }
+
+template <int D, int C>
+hipError_t launch(const tb_paged_rotary_args& a, hipStream_t stream) {
+  const tb_paged_cache& c = a.cache;
+  constexpr int kGroups = kThreads / (D / 8);
+  Cut cut{};
+  if (c.max_q <= kFew) {
+    cut.tokens = 1;
+    cut.q_heads = cut.kv_heads = kGroups;
+    cut.q_groups = a.q ? (a.heads_q + kGroups - 1) / kGroups : 0;
+    cut.kv_groups = (2 * c.heads_kv + kGroups - 1) / kGroups;
+    const dim3 grid((unsigned)c.max_q, (unsigned)(cut.q_groups + cut.kv_groups), (unsigned)c.B);
+    hipLaunchKernelGGL((rotary_kernel<D, C, true>), grid, dim3(kThreads), 0, stream, a, cut);
+    return hipGetLastError();
+  }
+  cut.tokens = kTokens;
+  // A chunk that does not start on a tile reaches into one more.  Heads are
+  // shared out until there are four workgroups for each of 256 CUs, but at
+  // least four to one, which finds its angles for them.
+  const int64_t tiles = (c.max_q + kTile - 1) / kTile + 1, rows = tiles * kRatio * c.B;
+  const int parts = at_least((1024 + rows - 1) / rows, (a.heads_q + 3) / 4);
+  cut.q_heads = a.q ? (a.heads_q + parts - 1) / parts : 1;
+  cut.q_groups = a.q ? (a.heads_q + cut.q_heads - 1) / cut.q_heads : 0;
+  cut.kv_heads = 8;
+  cut.kv_groups = (c.heads_kv + 7) / 8;
+  const dim3 grid((unsigned)(tiles * kRatio), (unsigned)(cut.q_groups + cut.kv_groups + (c.heads_kv + kRatio - 1) / kRatio),
+                  (unsigned)c.B);
+  hipLaunchKernelGGL((rotary_kernel<D, C, false>), grid, dim3(kThreads), 0, stream, a, cut);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_paged_rotary(const tb_paged_rotary_args& a, hipStream_t stream) {
+  const bool wide = a.cache.head_dim == 128;
+  if (a.cache.cache_dtype == TB_INT4) return wide ? launch<128, TB_INT4>(a, stream) : launch<64, TB_INT4>(a, stream);
+  if (a.cache.cache_dtype == TB_FP8) return wide ? launch<128, TB_FP8>(a, stream) : launch<64, TB_FP8>(a, stream);
+  return wide ? launch<128, TB_BF16>(a, stream) : launch<64, TB_BF16>(a, stream);
+}
+
+}  // namespace tb

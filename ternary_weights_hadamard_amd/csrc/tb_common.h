@@ -69,6 +69,15 @@ __device__ __forceinline__ float xor_lane(float v) {
   return __int_as_float(r);
 }
 
+// The same in 64 bits.
+template <int MASK>
+__device__ __forceinline__ double xor_lane(double v) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __float_as_uint(xor_lane<MASK>(__uint_as_float((uint32_t)w)));
+  const uint32_t hi = __float_as_uint(xor_lane<MASK>(__uint_as_float((uint32_t)(w >> 32))));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Keep the sources `a` and `b` of an instruction that produced `d` in vector
 // registers until after it: the asm reads all three, so it cannot be placed
 // before the instruction, and the sources stay live across it (their

@@ -50,6 +50,14 @@ constexpr int64_t kVerifySlice = 4096;
 hipError_t launch_verify_draft(const tb_verify_draft_args& a, hipStream_t stream);
 hipError_t launch_paged_append(const tb_paged_cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                                int64_t v_stride, hipStream_t stream);
+hipError_t launch_paged_rotary(const tb_paged_rotary_args& a, hipStream_t stream);
+hipError_t launch_paged_read(const tb_paged_cache& c, void* k_out, void* v_out, int out_dtype, hipStream_t stream);
+// vocabularies up to this take one launch and no workspace
+constexpr int64_t kProbsWhole = 1 << 15;
+// entries of one workgroup in larger ones, and what it leaves for a row
+constexpr int64_t kProbsSlice = 4096;
+constexpr size_t kProbsSliceBytes = 16;
+hipError_t launch_token_probs(const tb_token_probs_args& a, hipStream_t stream);
 // bytes of the workspace that positions are split with (0: none is used)
 size_t attn_part_bytes(const tb_paged_attention_args& a);
 hipError_t launch_paged_attention(const tb_paged_attention_args& a, bool split, hipStream_t stream);

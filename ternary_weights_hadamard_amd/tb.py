@@ -23,13 +23,15 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtb.so")
 
-TB_F32, TB_BF16, TB_ACT8, TB_FP8 = 0, 1, 2, 3
+TB_F32, TB_BF16, TB_ACT8, TB_FP8, TB_INT4 = 0, 1, 2, 3, 4
 TB_FMT_DENSE, TB_FMT_24, TB_FMT_DENSE_MINERR, TB_FMT_DENSE_RESID = 0, 1, 2, 3
 TB_EFLAG_NONFINITE, TB_EFLAG_SCALE_OVF = 1, 2
 TB_GEMV_MAX_BATCH = 16
 TB_MAX_SEGMENTS = 8
 TB_NORM_MAX_C = 32768
 TB_MAX_DRAFT = 64
+TB_MAX_BIAS = 2047
+TB_ROPE_PLAIN, TB_ROPE_LINEAR, TB_ROPE_NTK, TB_ROPE_YARN = 0, 1, 2, 3
 TB_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _lib = None
@@ -82,6 +84,22 @@ class PagedAttentionArgs(ctypes.Structure):
                 ("heads_q", _int), ("out_dtype", _int), ("scale", ctypes.c_float), ("reserved", _int)]
 
 
+class PagedRotaryArgs(ctypes.Structure):
+    _fields_ = [("cache", PagedCache), ("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("inv_freq", _vp),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("heads_q", _int), ("rotary_dim", _int),
+                ("neighbours", _int), ("turn_in", _int), ("turn_out", _int), ("turn_v", _int), ("factor", ctypes.c_float),
+                ("reserved", _int)]
+
+
+class TokenProbsArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("p", _vp), ("params", _vp), ("drafts", _vp), ("cu_draft", _vp), ("history", _vp),
+                ("cu_history", _vp), ("prompt_len", _vp), ("bias_ids", _vp), ("bias_values", _vp), ("cu_bias", _vp),
+                ("mask", _vp), ("mask_row", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("B", _i64),
+                ("total", _i64), ("vocab", _i64), ("logits_stride", _i64), ("p_stride", _i64), ("total_history", _i64),
+                ("total_bias", _i64), ("n_masks", _i64), ("mask_stride", _i64), ("max_draft", _int),
+                ("logits_dtype", _int), ("p_dtype", _int), ("reserved", _int)]
+
+
 class VerifyDraftArgs(ctypes.Structure):
     _fields_ = [("p", _vp), ("q", _vp), ("drafts", _vp), ("u", _vp), ("u_next", _vp), ("cu_draft", _vp),
                 ("accepted", _vp), ("tokens", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
@@ -114,6 +132,12 @@ SIGNATURES = {
     "tb_paged_append": (_int, [ctypes.POINTER(PagedCache), _vp, _i64, _vp, _i64, _vp]),
     "tb_paged_attention_workspace": (ctypes.c_size_t, [ctypes.POINTER(PagedAttentionArgs)]),
     "tb_paged_attention": (_int, [ctypes.POINTER(PagedAttentionArgs), _vp]),
+    "tb_paged_append_rotary": (_int, [ctypes.POINTER(PagedRotaryArgs), _vp]),
+    "tb_rotary_frequencies": (_int, [_int, ctypes.c_double, _int, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                     ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_float)]),
+    "tb_paged_read": (_int, [ctypes.POINTER(PagedCache), _vp, _vp, _int, _vp]),
+    "tb_token_probs_workspace": (ctypes.c_size_t, [ctypes.POINTER(TokenProbsArgs)]),
+    "tb_token_probs": (_int, [ctypes.POINTER(TokenProbsArgs), _vp]),
     "tb_verify_draft_workspace": (ctypes.c_size_t, [_i64, _i64]),
     "tb_verify_draft": (_int, [ctypes.POINTER(VerifyDraftArgs), _vp]),
 }
@@ -598,8 +622,10 @@ def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max
         kind = TB_BF16
     elif k_cache.dtype == torch.float8_e4m3fn:
         kind = TB_FP8
+    elif k_cache.dtype == torch.uint8:
+        kind, d = TB_INT4, 2 * d
     else:
-        raise TypeError(f"{where}: the cache must be bfloat16 or float8_e4m3fn (got {k_cache.dtype})")
+        raise TypeError(f"{where}: the cache must be bfloat16, float8_e4m3fn or uint8 (two 4-bit codes; got {k_cache.dtype})")
     b = kv_len.shape[0]
     if not (cu_q.dtype == kv_len.dtype == block_table.dtype == torch.int32):
         raise TypeError(f"{where}: block_table, cu_q and kv_len must be int32")
@@ -607,9 +633,15 @@ def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max
         raise ValueError(f"{where}: kv_len must be [B], cu_q [B + 1], block_table [B, entries]")
     if not block_table.is_cuda or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError(f"{where}: a sequence's block_table entries must be contiguous on the device")
-    for sc in (k_scale, v_scale):
-        if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):
-            raise ValueError(f"{where}: k_scale and v_scale must be float32 [{heads}], of an 8-bit cache")
+    if kind == TB_INT4:
+        for sc, shape in ((k_scale, (pages, heads, page, 2)), (v_scale, (pages, heads, 2, page))):
+            if sc is None or sc.dtype != torch.float16 or sc.shape != shape:
+                raise ValueError(f"{where}: a 4-bit cache needs k_scale float16 [{pages}, {heads}, {page}, 2] and v_scale "
+                                 f"[{pages}, {heads}, 2, {page}]")
+    else:
+        for sc in (k_scale, v_scale):
+            if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):
+                raise ValueError(f"{where}: k_scale and v_scale must be float32 [{heads}], of an 8-bit cache")
     _same_device(tokens, k_cache, v_cache, block_table, cu_q, kv_len, k_scale, v_scale)
     width = block_table.shape[1]
     stride = block_table.stride(0) if b > 1 else width
@@ -623,8 +655,10 @@ def tb_paged_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_
     a fused projection allowed) into the pages of their positions: sequence b's
     tokens are rows cu_q[b]..cu_q[b + 1] - 1 and its last positions below
     kv_len[b].  k_cache [pages, heads, page, d], v_cache [pages, heads, d, page],
-    bf16 or float8_e4m3fn (codes of x / scale[head]); max_q is at least every
-    sequence's new tokens."""
+    bf16 or float8_e4m3fn (codes of x / scale[head]), or 4 bits: uint8 k_cache
+    [pages, heads, page, d / 2], v_cache [pages, heads, d / 2, page], float16 scales
+    and offsets k_scale [pages, heads, page, 2], v_scale [pages, heads, 2, page].
+    max_q is at least every sequence's new tokens."""
     cache = _paged_cache("tb_paged_append", k, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
     _same_device(k, v)
     ks = _token_rows(k, cache.heads_kv, cache.head_dim, "tb_paged_append: k")
@@ -632,6 +666,89 @@ def tb_paged_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_
     if not (v.shape[0] == k.shape[0]):
         raise ValueError("tb_paged_append: k and v differ in tokens")
     _check(lib().tb_paged_append(cache, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream)), "tb_paged_append")
+
+
+def tb_paged_append_rotary(q, k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, inv_freq, factor=1.0,
+                           neighbours=False, turn_in=False, turn_out=False, turn_v=False, k_scale=None, v_scale=None,
+                           q_out=None, stream=None):
+    """Rotate the new tokens' queries and keys by their positions, and write keys
+    and values into the cache as tb_paged_append does, in one launch.  Returns the
+    queries (bf16 [tokens, heads, d], q_out if given; None without q).
+    inv_freq: float32 [rotary_dim / 2] radians a position (tb_rotary_frequencies),
+    or None for no positions; the first rotary_dim channels of a head turn in
+    pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if neighbours; factor
+    multiplies cosine and sine.  turn_in, turn_out (q and k, before and after) and
+    turn_v apply the 128-point Hadamard transform to a head (d = 128 only)."""
+    where = "tb_paged_append_rotary"
+    cache = _paged_cache(where, k, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
+    ks = _token_rows(k, cache.heads_kv, cache.head_dim, where + ": k")
+    vs = _token_rows(v, cache.heads_kv, cache.head_dim, where + ": v")
+    if not (v.shape[0] == k.shape[0]):
+        raise ValueError(f"{where}: k and v differ in tokens")
+    rotary = 0
+    if inv_freq is not None:
+        _dev(inv_freq)
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+            raise ValueError(f"{where}: inv_freq must be float32 [rotary_dim / 2]")
+        rotary = 2 * inv_freq.shape[0]
+    heads = qs = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError(f"{where}: no q_out without q")
+    else:
+        heads = q.shape[1] if q.dim() == 3 else 0
+        qs = _token_rows(q, heads, cache.head_dim, where + ": q")
+        if not (q.shape[0] == k.shape[0]):
+            raise ValueError(f"{where}: q and k differ in tokens")
+        if q_out is None:
+            q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        _dev(q_out)
+        if not (q_out.dtype == torch.bfloat16 and q_out.shape == q.shape):
+            raise ValueError(f"{where}: q_out must be bfloat16 {tuple(q.shape)}")
+    _same_device(k, v, q, q_out, inv_freq)
+    args = PagedRotaryArgs(cache, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), _addr(inv_freq), qs, ks, vs, heads,
+                           rotary, int(neighbours), int(turn_in), int(turn_out), int(turn_v), factor, 0)
+    _check(lib().tb_paged_append_rotary(args, _stream(stream)), where)
+    return q_out
+
+
+def tb_rotary_frequencies(rotary_dim, base=10000.0, scaling=TB_ROPE_PLAIN, scale=1.0, trained=0.0, fast=32.0, slow=1.0):
+    """(inv_freq, factor) for tb_paged_append_rotary: float32 [rotary_dim / 2] on
+    the host, and the factor of cosine and sine.  scaling TB_ROPE_LINEAR, _NTK or
+    _YARN stretches positions `scale` times (include/tb.h); `trained` is the length
+    that a model was trained for (TB_ROPE_YARN)."""
+    rotary_dim = int(rotary_dim)
+    out = (ctypes.c_float * max(rotary_dim // 2, 1))()
+    factor = ctypes.c_float()
+    _check(lib().tb_rotary_frequencies(rotary_dim, base, int(scaling), scale, trained, fast, slow, out,
+                                       ctypes.byref(factor)), "tb_rotary_frequencies")
+    return torch.tensor(list(out), dtype=torch.float32), factor.value
+
+
+def tb_paged_read(k_cache, v_cache, block_table, cu_q, kv_len, total, max_q, k_scale=None, v_scale=None, k=None, v=None,
+                  out_dtype=torch.bfloat16, stream=None):
+    """The cache's values: rows cu_q[b]..cu_q[b + 1] - 1 of (k, v) [total, heads, d]
+    are what sequence b's last positions hold (cu_q counts positions: kv_len of
+    them for whole sequences; max_q is at least every count).  k and v are made
+    when not given; rows whose position does not exist are left as they are."""
+    where = "tb_paged_read"
+    total = int(total)
+    cache = _paged_cache(where, k_cache, k_cache, v_cache, block_table, cu_q, kv_len, int(max_q), k_scale, v_scale)
+    cache.total_q = total
+    shape = (total, cache.heads_kv, cache.head_dim)
+    for t in (k, v):
+        if t is not None:
+            _dev(t)
+            out_dtype = t.dtype
+            if not (t.shape == shape):
+                raise ValueError(f"{where}: k and v must be {list(shape)}")
+    made = [t if t is not None else _empty(shape, out_dtype, k_cache.device, stream) for t in (k, v)]
+    if not (made[0].dtype == made[1].dtype):
+        raise ValueError(f"{where}: k and v differ in dtype")
+    _same_device(k_cache, *made)
+    _check(lib().tb_paged_read(cache, made[0].data_ptr(), made[1].data_ptr(), _float_dt(made[0], where + ": k and v"),
+                               _stream(stream)), where)
+    return made[0], made[1]
 
 
 def _attention_args(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale, window, k_scale, v_scale,
@@ -754,3 +871,88 @@ def tb_verify_draft(p, q, drafts, u, u_next, cu_draft, max_draft, accepted=None,
                            ps, qs, max_draft, _float_dt(p, where + ": p"), TB_F32 if q is None else _float_dt(q, where + ": q"), 0)
     _check(L.tb_verify_draft(args, _stream(stream)), where)
     return accepted, tokens
+
+
+def _token_list(where, what, ids, cu, b):
+    if not (ids.dtype == torch.int32 and ids.dim() == 1):
+        raise ValueError(f"{where}: {what} must be int32, one after another")
+    if cu is None or not (cu.dtype == torch.int32 and cu.shape == (b + 1,)):
+        raise ValueError(f"{where}: {what} needs its offsets, int32 [{b + 1}]")
+
+
+def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, history=None, cu_history=None,
+                   prompt_len=None, bias=None, mask=None, mask_row=None, p=None, out_dtype=torch.float32, workspace=None,
+                   stream=None):
+    """Probabilities of tokens from logits [rows, vocab] (fp32 or bf16): bias,
+    penalties of repeated tokens, mask, temperature and softmax, in this order
+    (include/tb.h).  params float32 [B, 4]: temperature (0: the largest logit gets
+    1), repeats, presence, frequency of each sequence.  Sequence b has a row for
+    each of its drafts and one more, as tb_verify_draft has them (drafts int32
+    [total], cu_draft int32 [B + 1]; None: one row for each sequence).
+    history int32, cu_history [B + 1]: its tokens so far, the first prompt_len[b]
+    of them its prompt's.  bias: (ids int32, values float32, offsets int32 [B + 1]).
+    mask int32 [masks, words], a bit for each allowed token, and mask_row int32
+    [rows] (-1: none; None: mask r for row r).  Returns p [rows, vocab]; rows of
+    no sequence are left as they are."""
+    where = "tb_token_probs"
+    _dev(params, drafts, cu_draft, history, cu_history, prompt_len, mask_row, workspace)
+    max_draft = int(max_draft)
+    if not (params.dtype == torch.float32 and params.dim() == 2 and params.shape[1] == 4):
+        raise ValueError(f"{where}: params must be float32 [B, 4]")
+    b = params.shape[0]
+    ls = _prob_rows(logits, where + ": logits")
+    rows, vocab = logits.shape
+    total = 0
+    if drafts is not None:
+        _token_list(where, "drafts", drafts, cu_draft, b)
+        total = drafts.shape[0]
+    if not (rows == total + b):
+        raise ValueError(f"{where}: logits must have {total + b} rows (drafts + sequences)")
+    n_history = n_bias = n_masks = words = 0
+    if history is not None:
+        _token_list(where, "history", history, cu_history, b)
+        n_history = history.shape[0]
+        if prompt_len is not None and not (prompt_len.dtype == torch.int32 and prompt_len.shape == (b,)):
+            raise ValueError(f"{where}: prompt_len must be int32 [{b}]")
+    ids = values = cu_bias = None
+    if bias is not None:
+        ids, values, cu_bias = bias
+        _dev(ids, values, cu_bias)
+        _token_list(where, "bias", ids, cu_bias, b)
+        n_bias = ids.shape[0]
+        if not (values.dtype == torch.float32 and values.shape == ids.shape):
+            raise ValueError(f"{where}: the biases must be float32 [{n_bias}]")
+    if mask is not None:
+        need = (vocab + 31) // 32
+        if not (mask.is_cuda and mask.dtype == torch.int32 and mask.dim() == 2 and mask.shape[1] >= need
+                and (mask.shape[1] == 1 or mask.stride(1) == 1)):
+            raise ValueError(f"{where}: mask must be int32 [masks, {need}] on the device, a mask contiguous")
+        n_masks = mask.shape[0]
+        words = mask.stride(0) if n_masks > 1 else mask.shape[1]
+        if mask_row is None:
+            if not (n_masks == rows):
+                raise ValueError(f"{where}: {rows} masks are needed without mask_row")
+        elif not (mask_row.dtype == torch.int32 and mask_row.shape == (rows,)):
+            raise ValueError(f"{where}: mask_row must be int32 [{rows}]")
+    elif mask_row is not None:
+        raise ValueError(f"{where}: mask_row needs mask")
+    if p is None:
+        p = _empty((rows, vocab), out_dtype, logits.device, stream)
+    ps = _prob_rows(p, where + ": p")
+    if not (p.shape == (rows, vocab)):
+        raise ValueError(f"{where}: p must be [{rows}, {vocab}]")
+    args = TokenProbsArgs(logits.data_ptr(), p.data_ptr(), params.data_ptr(), _addr(drafts), _addr(cu_draft),
+                          _addr(history), _addr(cu_history), _addr(prompt_len), _addr(ids), _addr(values), _addr(cu_bias),
+                          _addr(mask), _addr(mask_row), None, 0, b, total, vocab, ls, ps, n_history, n_bias, n_masks, words,
+                          max_draft, _float_dt(logits, where + ": logits"), _float_dt(p, where + ": p"), 0)
+    L = lib()
+    if workspace is None:
+        nbytes = L.tb_token_probs_workspace(args)
+        if nbytes:
+            workspace = _empty(nbytes, torch.uint8, logits.device, stream)
+    _same_device(logits, params, drafts, cu_draft, history, cu_history, prompt_len, ids, values, cu_bias, mask, mask_row, p,
+                 workspace)
+    if workspace is not None:
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(L.tb_token_probs(args, _stream(stream)), where)
+    return p
