@@ -25,21 +25,6 @@ __device__ __forceinline__ float weight_reference(float m) {
   return ROOM > 0 && fabsf(m) < 0x1p20f ? m - (float)ROOM : m;
 }
 
-// x in the lane's row of 16 lanes, combined with the other rows': v[lane ^ 16] and v[lane ^ 32]
-__device__ __forceinline__ float max_over_rows(float v) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-
-__device__ __forceinline__ float sum_over_rows(float v) {
-  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // 8 e4m3 bytes widened to bf16 / fp16: both hold every e4m3 value exactly
 __device__ __forceinline__ bf16x8 fp8_to_bf16(const u32x2& w) {
   bf16x8 r;

@@ -78,6 +78,21 @@ __device__ __forceinline__ double xor_lane(double v) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// x in the lane's row of 16 lanes, combined with the other rows': v[lane ^ 16] and v[lane ^ 32]
+__device__ __forceinline__ float max_over_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ __forceinline__ float sum_over_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // Keep the sources `a` and `b` of an instruction that produced `d` in vector
 // registers until after it: the asm reads all three, so it cannot be placed
 // before the instruction, and the sources stay live across it (their

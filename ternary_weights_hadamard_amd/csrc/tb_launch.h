@@ -55,7 +55,7 @@ hipError_t launch_paged_read(const tb_paged_cache& c, void* k_out, void* v_out, 
 // vocabularies up to this take one launch and no workspace
 constexpr int64_t kProbsWhole = 1 << 15;
 // entries of one workgroup in larger ones, and what it leaves for a row
-constexpr int64_t kProbsSlice = 4096;
+constexpr int64_t kProbsSlice = 8192;
 constexpr size_t kProbsSliceBytes = 16;
 hipError_t launch_token_probs(const tb_token_probs_args& a, hipStream_t stream);
 // bytes of the workspace that positions are split with (0: none is used)

@@ -4,13 +4,15 @@
 // What changes a logit is known by its token: for a run of the vocabulary, LDS
 // holds a word for each entry (its bias, how often it was generated, whether the
 // prompt has it), made from the sequence's lists by integer atomics, so that
-// results do not depend on their order.  The lists are read once for all rows of
-// a sequence that a workgroup has: from one row to the next a draft is added.
+// results do not depend on their order.
 //
-// Up to kProbsWhole entries a workgroup has a row in registers: one launch, each
-// logit read once.  Larger vocabularies have a workgroup for a slice: the first
-// launch leaves each slice's maximum, sum and first maximum, the second reads the
-// logits again (from the caches, where they fit) and writes.
+// A workgroup has a row, or a slice of one, in registers.  Up to kProbsWhole
+// entries it is a row: one launch, each logit read once.  Larger vocabularies
+// have a workgroup for each slice: the first launch leaves each slice's maximum,
+// sum and first maximum, the second reads the logits again (from the caches,
+// where they fit) and writes.
+#include <type_traits>
+
 #include "tb_common.h"
 #include "tb_launch.h"
 
@@ -18,15 +20,18 @@ namespace tb {
 
 namespace {
 
-constexpr int kThreads = 256;   // of a slice
+constexpr int kRowThreads = 1024, kSliceThreads = 512;
 constexpr uint32_t kCount = (1u << 20) - 1, kTold = 1u << 31;
 constexpr int kBiasShift = 20;
+constexpr uint32_t kBias = 0x7ffu << kBiasShift;
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(TB_MAX_BIAS < (1 << 11) && kProbsSlice == 16 * kThreads, "a word's fields; four loads of four a thread");
+constexpr float kNone = -__builtin_inff();
+static_assert(TB_MAX_BIAS < (1 << 11), "a word's fields");
 
-// A sequence: its rows, its lists and its parameters.
+// A row's sequence: its rows, its lists and its parameters.
 struct Seq {
-  int64_t row0;            // of its first row
+  bool live;               // it has the row
+  int j;                   // drafts before it
   int64_t draft0;
   int drafts;
   int64_t told, made, end;  // its history: the prompt from `told`, generated from `made`
@@ -34,144 +39,243 @@ struct Seq {
   int biases;
   float sharp;             // log2(e) / temperature; 0: the largest is taken
   float repeats, presence, frequency;
+  float inverse;           // of repeats
+  bool plain;              // which is a number near 1
 };
+
+__device__ __forceinline__ int64_t clamped(int64_t x, int64_t total) { return min(max(x, (int64_t)0), total); }
+
+// The sequence that has row `row`: the last one that starts at it or before.
+// Whole waves look at every n-th of them, 64 at a time.
+__device__ __forceinline__ int sequence_of(const tb_token_probs_args& a, int64_t row) {
+  if (!a.cu_draft) return (int)row;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = (int)a.B;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, b = lo + lane * step;
+    const bool starts = lane * step < n && clamped(a.cu_draft[b], a.total) + b <= row;
+    const int past = __builtin_popcountll(__ballot(starts)), k = past > 0 ? past - 1 : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// What a lane has loaded of sequence first + lane: of up to 63 sequences each
+// lane has one before it is known which is the row's, so that the chain from
+// the row to its lists is one load long.  A list that is not there is empty; its
+// offsets are loaded from what is there, so that no load stands behind a branch.
+struct Offsets {
+  int first;
+  int32_t draft, history, bias, prompt;
+  float params[4];
+};
+template <bool LISTS>
+__device__ __forceinline__ Offsets load_offsets(const tb_token_probs_args& a, int64_t row) {
+  Offsets o;
+  o.first = a.B > 63 ? sequence_of(a, row) : 0;
+  const int lane = threadIdx.x & 63, end = min(o.first + lane, (int)a.B), b = min(end, (int)a.B - 1);
+  const int32_t* none = reinterpret_cast<const int32_t*>(a.params);
+  o.draft = *(a.cu_draft ? a.cu_draft + end : none);
+  o.history = o.bias = o.prompt = 0;
+  o.params[1] = o.params[2] = o.params[3] = 0.f;
+  if constexpr (LISTS) {
+    o.history = *(a.history ? a.cu_history + end : none);
+    o.bias = *(a.bias_ids ? a.cu_bias + end : none);
+    o.prompt = *(a.history && a.prompt_len ? a.prompt_len + b : none);
+    const f32x4 p = *reinterpret_cast<const f32x4*>(a.params + 4 * (int64_t)b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o.params[e] = p[e];
+  } else {
+    o.params[0] = a.params[4 * (int64_t)b];
+  }
+  return o;
+}
 
 struct Range {
   int64_t lo, hi;
 };
-__device__ __forceinline__ Range range_of(const int32_t* cu, int64_t b, int64_t total) {
+// Sequence k's part of a list of `total`, from what lanes have loaded.
+__device__ __forceinline__ Range range_of(const void* list, int32_t cu, int k, int64_t total) {
+  if (!list) total = 0;
   Range r;
-  r.lo = min(max((int64_t)cu[b], (int64_t)0), total);
-  r.hi = min(max((int64_t)cu[b + 1], r.lo), total);
+  r.lo = clamped(__builtin_amdgcn_readlane(cu, k), total);
+  r.hi = max(clamped(__builtin_amdgcn_readlane(cu, k + 1), total), r.lo);
   return r;
 }
+__device__ __forceinline__ float of_lane(float v, int k) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), k));
+}
 
-__device__ __forceinline__ Seq sequence(const tb_token_probs_args& a, int64_t b) {
-  Seq s{};
-  if (a.cu_draft) {
-    const Range d = range_of(a.cu_draft, b, a.total);
-    s.draft0 = d.lo;
-    s.drafts = (int)min(d.hi - d.lo, (int64_t)a.max_draft);
+__device__ __forceinline__ Seq sequence(const tb_token_probs_args& a, const Offsets& o, int64_t row) {
+  int k = 0;
+  if (a.B <= 63) {
+    const int lane = threadIdx.x & 63;
+    const bool starts = lane < (int)a.B && clamped(o.draft, a.total) + lane <= row;
+    const int past = __builtin_popcountll(__ballot(starts));
+    k = !a.cu_draft ? (int)row : past > 0 ? past - 1 : 0;
   }
-  s.row0 = s.draft0 + b;
-  if (a.history) {
-    const Range h = range_of(a.cu_history, b, a.total_history);
-    const int64_t prompt = a.prompt_len ? min(max((int64_t)a.prompt_len[b], (int64_t)0), h.hi - h.lo) : 0;
-    s.told = h.lo;
-    s.made = h.lo + prompt;
-    s.end = h.hi;
-  }
-  if (a.bias_ids) {
-    const Range r = range_of(a.cu_bias, b, a.total_bias);
-    s.bias = r.lo;
-    s.biases = (int)min(r.hi - r.lo, (int64_t)TB_MAX_BIAS);
-  }
-  const f32x4 p = *reinterpret_cast<const f32x4*>(a.params + 4 * b);
-  s.sharp = p[0] > 0.f ? fminf(fmaxf(kLog2e / p[0], 1.4e-45f), 3e38f) : 0.f;  // no 0 * inf
-  s.repeats = p[1];
-  s.presence = p[2];
-  s.frequency = p[3];
+  k = __builtin_amdgcn_readfirstlane(k);
+  const Range d = range_of(a.cu_draft, o.draft, k, a.total);
+  const Range h = range_of(a.history, o.history, k, a.total_history);
+  const Range r = range_of(a.bias_ids, o.bias, k, a.total_bias);
+  const int64_t length = a.history && a.prompt_len ? __builtin_amdgcn_readlane(o.prompt, k) : 0;
+  const float temperature = of_lane(o.params[0], k);
+  Seq s;
+  s.draft0 = d.lo;
+  s.drafts = (int)min(d.hi - d.lo, (int64_t)a.max_draft);
+  const int64_t j = row - (o.first + k) - d.lo;
+  s.live = j >= 0 && j <= s.drafts;
+  s.j = (int)clamped(j, s.drafts);
+  s.told = h.lo;
+  s.made = h.lo + clamped(length, h.hi - h.lo);
+  s.end = h.hi;
+  s.bias = r.lo;
+  s.biases = (int)min(r.hi - r.lo, (int64_t)TB_MAX_BIAS);
+  s.sharp = temperature > 0.f ? fminf(fmaxf(kLog2e / temperature, 1.4e-45f), 3e38f) : 0.f;  // no 0 * inf
+  s.repeats = of_lane(o.params[1], k);
+  s.inverse = 1.f / s.repeats;
+  s.plain = s.repeats > 0x1p-20f && s.repeats < 0x1p20f;
+  s.presence = of_lane(o.params[2], k);
+  s.frequency = of_lane(o.params[3], k);
   return s;
 }
 
-__device__ __forceinline__ void add_draft(const tb_token_probs_args& a, const Seq& s, int j, uint32_t* words, int64_t begin,
-                                          int64_t end) {
-  const int64_t id = a.drafts[s.draft0 + j];
-  if (id >= begin && id < end) atomicAdd(words + (id - begin), 1u);
-}
-
-// The words of entries begin .. end - 1 for a row behind `j` drafts; `count` of
-// them are cleared (a multiple of 4 * THREADS).  Barriers before, between and behind.
-template <int THREADS>
-__device__ __forceinline__ void make_words(const tb_token_probs_args& a, const Seq& s, int j, uint32_t* words, int count,
-                                           int64_t begin, int64_t end) {
-  const int tid = threadIdx.x;
-  for (int i = 4 * tid; i < count; i += 4 * THREADS) *reinterpret_cast<u32x4*>(words + i) = u32x4{0u, 0u, 0u, 0u};
-  __syncthreads();
-  if (s.biases > 0) {
-    for (int i = tid; i < s.biases; i += THREADS) {
-      const int64_t id = a.bias_ids[s.bias + i];
-      if (id >= begin && id < end) atomicMax(words + (id - begin), (uint32_t)(i + 1) << kBiasShift);
-    }
-    __syncthreads();  // the words are only biases yet: the last one of an id is the largest
-  }
-  // no more than the count has room for, with all drafts
-  const int64_t counted = max(s.made, s.end - ((1 << 20) - TB_MAX_DRAFT));
-#pragma unroll 4
-  for (int64_t i = s.told + tid; i < s.end; i += THREADS) {
-    const int64_t id = a.history[i];
-    if (id < begin || id >= end) continue;
-    if (i < s.made) atomicOr(words + (id - begin), kTold);
-    else if (i >= counted) atomicAdd(words + (id - begin), 1u);
-  }
-  if (tid < j) add_draft(a, s, tid, words, begin, end);
-  __syncthreads();
-}
-
 __device__ __forceinline__ float adjusted(const tb_token_probs_args& a, const Seq& s, float x, uint32_t word) {
-  const uint32_t bias = word >> kBiasShift & 0x7ffu, count = word & kCount;
+  const uint32_t bias = (word & kBias) >> kBiasShift, count = word & kCount;
   if (bias) x += a.bias_values[s.bias + bias - 1];
-  if (word & (kTold | kCount)) x = x > 0.f ? x / s.repeats : x * s.repeats;
+  // a quotient by the reciprocal, corrected by its remainder: as the division
+  // rounds it, where nothing in it leaves fp32's range
+  const float q = x * s.inverse;
+  const float less = s.plain ? __builtin_fmaf(__builtin_fmaf(-q, s.repeats, x), s.inverse, q) : x / s.repeats;
+  if (word & (kTold | kCount)) x = x > 0.f ? less : x * s.repeats;
   if (count) x -= s.frequency * (float)count + s.presence;
   return x;
 }
 
+// The words of the row's `length` entries from `begin` on, in LDS that has been
+// cleared.  Barriers before and behind.
+template <int kThreads>
+__device__ __forceinline__ void make_words(const tb_token_probs_args& a, const Seq& s, uint32_t* words, int64_t begin,
+                                           int length) {
+  typedef int32_t __attribute__((ext_vector_type(4), aligned(4))) Four;
+  const int tid = threadIdx.x;
+  auto load = [&](int64_t i) {
+    Four t = {-1, -1, -1, -1};
+    if (i + 4 <= s.end) {
+      t = *reinterpret_cast<const Four*>(a.history + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (i + e < s.end) t[e] = a.history[i + e];
+    }
+    return t;
+  };
+  // what comes first of the lists is on its way while the words are cleared
+  const int64_t i0 = s.told + 4 * tid;
+  const Four first = load(i0);
+  int32_t draft = -1, biased = -1;
+  if (tid < s.j) draft = a.drafts[s.draft0 + tid];
+  if (tid < s.biases) biased = a.bias_ids[s.bias + tid];
+  __syncthreads();
+  // no more than the count has room for, with all drafts
+  const int64_t counted = max(s.made, s.end - ((1 << 20) - TB_MAX_DRAFT));
+  // where an id is in the run: a negative id is far past it
+  auto place = [&](int32_t id) { return (uint32_t)id - (uint32_t)begin; };
+  auto note = [&](int32_t id, int64_t i) {
+    const uint32_t k = place(id);
+    if (k >= (uint32_t)length || id < 0) return;
+    if (i < s.made) atomicOr(words + k, kTold);
+    else if (i >= counted) atomicAdd(words + k, 1u);
+  };
+  Four now = first;
+  for (int64_t i = i0; i < s.end; i += 4 * kThreads) {
+    const Four next = load(i + 4 * kThreads);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) note(now[e], i + e);
+    now = next;
+  }
+  note(draft, INT64_MAX);
+  // of an id's biases the last one: the largest index, put beside the rest of the
+  // word by an exchange that ends when nobody was in between
+  for (int k = tid; k < s.biases; k += kThreads) {
+    const int32_t id = k == tid ? biased : a.bias_ids[s.bias + k];
+    if (id < 0 || place(id) >= (uint32_t)length) continue;
+    uint32_t* w = words + place(id);
+    const uint32_t mine = (uint32_t)(k + 1) << kBiasShift;
+    for (uint32_t old = *w; (old & kBias) < mine;) {
+      const uint32_t was = atomicCAS(w, old, (old & ~kBias) | mine);
+      if (was == old) break;
+      old = was;
+    }
+  }
+  __syncthreads();
+}
+
+// Four entries from element `at` of a row (or slice) on, the first n < 4 of them
+// where it ends.  A row starts at any element, so these are aligned to elements only.
 template <int DTYPE>
-__device__ __forceinline__ f32x4 load4(const void* p, int64_t i, int n) {
-  f32x4 v = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+__device__ __forceinline__ f32x4 load4(const void* row, int at, int n) {
+  f32x4 v = {kNone, kNone, kNone, kNone};
   if constexpr (DTYPE == TB_BF16) {
     typedef uint16_t __attribute__((ext_vector_type(4), aligned(2))) u16x4;
-    const uint16_t* from = static_cast<const uint16_t*>(p) + i;
+    const uint16_t* from = static_cast<const uint16_t*>(row);
     if (n >= 4) {
-      const u16x4 w = *reinterpret_cast<const u16x4*>(from);
+      const u16x4 w = *reinterpret_cast<const u16x4*>(from + at);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = bf16_to_f32(w[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) v[e] = bf16_to_f32(from[e]);
+        if (e < n) v[e] = bf16_to_f32(from[at + e]);
     }
   } else {
     typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4u;
-    const float* from = static_cast<const float*>(p) + i;
+    const float* from = static_cast<const float*>(row);
     if (n >= 4) {
-      const f32x4u w = *reinterpret_cast<const f32x4u*>(from);
+      const f32x4u w = *reinterpret_cast<const f32x4u*>(from + at);
       v = f32x4{w[0], w[1], w[2], w[3]};
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) v[e] = from[e];
+        if (e < n) v[e] = from[at + e];
     }
   }
   return v;
 }
 
 template <int DTYPE>
-__device__ __forceinline__ void store4(void* p, int64_t i, int n, const f32x4& v) {
+__device__ __forceinline__ void store4(void* row, int at, int n, const f32x4& v) {
   if constexpr (DTYPE == TB_BF16) {
     typedef uint16_t __attribute__((ext_vector_type(4), aligned(2))) u16x4;
-    uint16_t* to = static_cast<uint16_t*>(p) + i;
+    uint16_t* to = static_cast<uint16_t*>(row);
     u16x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint16_t)f32_to_bf16_rne(v[e]);
     if (n >= 4) {
-      *reinterpret_cast<u16x4*>(to) = w;
+      *reinterpret_cast<u16x4*>(to + at) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) to[e] = w[e];
+        if (e < n) to[at + e] = w[e];
     }
   } else {
     typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4u;
-    float* to = static_cast<float*>(p) + i;
+    float* to = static_cast<float*>(row);
     if (n >= 4) {
-      *reinterpret_cast<f32x4u*>(to) = f32x4u{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4u*>(to + at) = f32x4u{v[0], v[1], v[2], v[3]};
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < n) to[e] = v[e];
+        if (e < n) to[at + e] = v[e];
     }
   }
+}
+
+template <int DTYPE, typename P>
+__device__ __forceinline__ P* element(P* p, int64_t i) {
+  typedef typename std::conditional<std::is_const<P>::value, const char, char>::type Byte;
+  return reinterpret_cast<Byte*>(p) + i * (DTYPE == TB_BF16 ? 2 : 4);
 }
 
 // The row's mask, or NULL.
@@ -181,37 +285,47 @@ __device__ __forceinline__ const uint32_t* mask_of(const tb_token_probs_args& a,
   return m >= 0 && m < a.n_masks ? a.mask + m * a.mask_stride : nullptr;
 }
 
-// A thread's entries of a row: 4 at v0 + CHUNK * c for each c, as loaded, and
-// what the formula makes of them; past the end of the row -inf.
+// A thread's entries of a run of `length` entries: 4 at 4 * tid + CHUNK * c for
+// each c, as loaded, and what the formula makes of them; past the end -inf.
 template <int CHUNKS, int CHUNK, int LD>
 struct Mine {
   f32x4 x[CHUNKS];
-  uint32_t allowed[CHUNKS];  // from bit 0 on
-  __device__ __forceinline__ void load(const tb_token_probs_args& a, int64_t row, int64_t v0) {
-    const uint32_t* mask = mask_of(a, row);
+  bool masked;
+  uint32_t allowed[CHUNKS];  // if so: from bit 0 on
+  // `run` the logits, `mask` the words (or NULL) of the run's first entry
+  __device__ __forceinline__ void load(const void* run, const uint32_t* mask, int at, int length) {
+    masked = mask != nullptr;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const int64_t v = v0 + CHUNK * c, n = a.vocab - v;
-      x[c] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+      const int v = at + CHUNK * c, n = length - v;
       allowed[c] = 0xfu;
-      if (n <= 0) continue;
-      x[c] = load4<LD>(a.logits, row * a.logits_stride + v, (int)min(n, (int64_t)4));
-      if (mask) allowed[c] = mask[v >> 5] >> (v & 31);  // v is a multiple of 4
+      if (CHUNK * (c + 1) <= length) {  // of all threads
+        x[c] = load4<LD>(run, v, 4);
+      } else {
+        x[c] = f32x4{kNone, kNone, kNone, kNone};
+        if (n > 0) x[c] = load4<LD>(run, v, n);
+      }
+      if (masked && n > 0) allowed[c] = mask[v >> 5] >> (v & 31);  // v is a multiple of 4
     }
   }
   // `words` of the thread's first entry
   template <bool WORDS>
   __device__ __forceinline__ void adjust(const tb_token_probs_args& a, const Seq& s, const uint32_t* words) {
+    if constexpr (WORDS) {
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if constexpr (WORDS) w = *reinterpret_cast<const u32x4*>(words + CHUNK * c);
+      for (int c = 0; c < CHUNKS; ++c) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(words + CHUNK * c);
+        if (!(w[0] | w[1] | w[2] | w[3])) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (WORDS && w[e]) x[c][e] = adjusted(a, s, x[c][e], w[e]);
-        if (!((allowed[c] >> e) & 1u)) x[c][e] = -__builtin_inff();
+        for (int e = 0; e < 4; ++e) x[c][e] = adjusted(a, s, x[c][e], w[e]);
       }
     }
+    if (!masked) return;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!((allowed[c] >> e) & 1u)) x[c][e] = -__builtin_inff();
   }
   __device__ __forceinline__ float top() const {
     float m = -__builtin_inff();
@@ -222,13 +336,13 @@ struct Mine {
     return m;
   }
   // the first entry that is `m`
-  __device__ __forceinline__ int first(int64_t v0, float m) const {
+  __device__ __forceinline__ int first(int v0, float m) const {
     int at = INT32_MAX;
 #pragma unroll
     for (int c = CHUNKS - 1; c >= 0; --c)
 #pragma unroll
       for (int e = 3; e >= 0; --e)
-        if (x[c][e] == m) at = (int)(v0 + CHUNK * c + e);
+        if (x[c][e] == m) at = v0 + CHUNK * c + e;
     return m == -__builtin_inff() ? INT32_MAX : at;
   }
   // turned into weights relative to m (not -inf), and their sum
@@ -242,29 +356,40 @@ struct Mine {
     }
     return sum;
   }
+  // p of the run; hot >= 0: 1 there and 0 elsewhere, past the run if it is not in it
   template <int PD>
-  __device__ __forceinline__ void write(const tb_token_probs_args& a, int64_t row, int64_t v0, float f, int hot) const {
+  __device__ __forceinline__ void write(void* run, int at, int length, float f, int hot) {
+    if (hot >= 0) {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[c][e] = at + CHUNK * c + e == hot ? 1.f : 0.f;
+    } else {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) x[c] *= f;
+    }
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
-      const int64_t v = v0 + CHUNK * c, n = a.vocab - v;
-      if (n <= 0) continue;
-      f32x4 p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = hot >= 0 ? (v + e == hot ? 1.f : 0.f) : x[c][e] * f;
-      store4<PD>(a.p, row * a.p_stride + v, (int)min(n, (int64_t)4), p);
+      const int v = at + CHUNK * c, n = length - v;
+      if (CHUNK * (c + 1) <= length) store4<PD>(run, v, 4, x[c]);
+      else if (n > 0) store4<PD>(run, v, n, x[c]);
     }
   }
 };
 
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  v = fmaxf(v, xor_lane<1>(v));
+  v = fmaxf(v, xor_lane<2>(v));
+  v = fmaxf(v, xor_lane<4>(v));
+  v = fmaxf(v, xor_lane<8>(v));
+  return max_over_rows(v);
 }
 __device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+  v += xor_lane<1>(v);
+  v += xor_lane<2>(v);
+  v += xor_lane<4>(v);
+  v += xor_lane<8>(v);
+  return sum_over_rows(v);
 }
 __device__ __forceinline__ int wave_min(int v) {
 #pragma unroll
@@ -272,47 +397,16 @@ __device__ __forceinline__ int wave_min(int v) {
   return v;
 }
 
-// Over the WAVES waves of the workgroup, in a fixed order; a barrier.  Between
-// two calls with the same array there has to be another.
-template <int WAVES, typename T, typename J>
+// Over the waves of the workgroup, in a fixed order; a barrier.  Between two
+// calls with the same array there has to be another.
+template <int kWaves, typename T, typename J>
 __device__ __forceinline__ T over_waves(T v, T* of_wave, J join) {
   of_wave[threadIdx.x >> 6] = v;
   __syncthreads();
   v = of_wave[0];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) v = join(v, of_wave[w]);
+  for (int w = 1; w < kWaves; ++w) v = join(v, of_wave[w]);
   return v;
-}
-
-constexpr float kNone = -__builtin_inff();
-
-// One workgroup a row, of CHUNKS * 4096 entries at most.
-template <int LD, int PD, int CHUNKS, bool WORDS>
-__global__ void __launch_bounds__(1024) whole_kernel(tb_token_probs_args a) {
-  constexpr int kWaves = 16, kChunk = 4096;
-  __shared__ __align__(16) uint32_t words[WORDS ? CHUNKS * kChunk : 4];
-  __shared__ float tops[kWaves], sums[kWaves];
-  __shared__ int firsts[kWaves];
-  const int64_t b = blockIdx.y;
-  const int j = blockIdx.x;
-  const Seq s = sequence(a, b);
-  if (j > s.drafts) return;
-  const int64_t row = s.row0 + j, v0 = 4 * (int)threadIdx.x;
-  Mine<CHUNKS, kChunk, LD> mine;
-  mine.load(a, row, v0);
-  if constexpr (WORDS) make_words<1024>(a, s, j, words, CHUNKS * kChunk, 0, a.vocab);
-  mine.template adjust<WORDS>(a, s, words + v0);
-  const float m = over_waves<kWaves>(wave_max(mine.top()), tops, [](float x, float y) { return fmaxf(x, y); });
-  int hot = -1;
-  float f = 0.f;
-  if (s.sharp > 0.f) {
-    const float sum = mine.weigh(m == kNone ? 0.f : m, s.sharp);
-    const float total = over_waves<kWaves>(wave_add(sum), sums, [](float x, float y) { return x + y; });
-    f = total == 0.f ? 0.f : 1.f / total;
-  } else {
-    hot = over_waves<kWaves>(wave_min(mine.first(v0, m)), firsts, [](int x, int y) { return min(x, y); });
-  }
-  mine.template write<PD>(a, row, v0, f, hot);
 }
 
 // What a slice leaves for its row.
@@ -322,89 +416,97 @@ struct Slice {
   int reserved;
 };
 
-// Rows part * per .. of a sequence, over one slice of the vocabulary.
-template <int LD, int PD, bool WORDS, bool WRITE>
-__global__ void __launch_bounds__(kThreads) slice_kernel(tb_token_probs_args a, Slice* slices, int per) {
-  constexpr int kWaves = kThreads / 64, kChunk = 4 * kThreads, kChunks = kProbsSlice / kChunk;
-  __shared__ __align__(16) uint32_t words[WORDS ? kProbsSlice : 4];
+// The same of a whole row from its slices, by every wave for itself.
+__device__ __forceinline__ Slice join_slices(const Slice* of, int count, float sharp) {
+  Slice all{kNone, 0.f, INT32_MAX, 0};
+  for (int i = threadIdx.x & 63; i < count; i += 64) {
+    const Slice x = of[i];
+    const float m = fmaxf(all.top, x.top), base = m == kNone ? 0.f : m;
+    all.sum = all.sum * __builtin_amdgcn_exp2f((all.top - base) * sharp) + x.sum * __builtin_amdgcn_exp2f((x.top - base) * sharp);
+    if (x.top > all.top) all.first = x.first;  // a lane's slices come in order
+    all.top = m;
+  }
+  Slice r{wave_max(all.top), 0.f, INT32_MAX, 0};
+  if (sharp > 0.f) r.sum = wave_add(all.sum * __builtin_amdgcn_exp2f((all.top - (r.top == kNone ? 0.f : r.top)) * sharp));
+  else r.first = wave_min(all.top == r.top ? all.first : INT32_MAX);
+  return r;
+}
+
+enum Part { kAll, kStatistics, kWrite };
+
+// A row (kAll), or a slice of one: `length` entries, CHUNKS * 4 * kThreads at most.
+template <int LD, int PD, int CHUNKS, bool WORDS, Part PART, int kThreads = PART == kAll ? kRowThreads : kSliceThreads>
+__global__ void __launch_bounds__(kThreads, PART == kAll ? 4 : 8) probs_kernel(tb_token_probs_args a, Slice* slices, int length) {
+  constexpr int kWaves = kThreads / 64, kChunk = 4 * kThreads;  // entries between a thread's loads of four
+  __shared__ __align__(16) uint32_t words[WORDS ? CHUNKS * kChunk : 4];
   __shared__ float tops[kWaves], sums[kWaves];
   __shared__ int firsts[kWaves];
-  const int64_t b = blockIdx.y, begin = (int64_t)blockIdx.x * kProbsSlice, v0 = begin + 4 * (int)threadIdx.x;
-  const Seq s = sequence(a, b);
-  int j = blockIdx.z * per;
-  const int last = min(j + per - 1, s.drafts);
-  if (j > last) return;
-  Mine<kChunks, kChunk, LD> mine;
-  mine.load(a, s.row0 + j, v0);
-  const int64_t end = min(begin + kProbsSlice, a.vocab);
-  if constexpr (WORDS) make_words<kThreads>(a, s, j, words, kProbsSlice, begin, end);
-  for (;; ++j) {
-    const int64_t row = s.row0 + j;
-    mine.template adjust<WORDS>(a, s, words + (v0 - begin));
-    Slice* of_row = slices + row * gridDim.x;
-    if constexpr (WRITE) {
-      // all slices of the row, by every wave for itself
-      Slice all{kNone, 0.f, INT32_MAX, 0};
-      for (int64_t i = threadIdx.x & 63; i < gridDim.x; i += 64) {
-        const Slice x = of_row[i];
-        const float m = fmaxf(all.top, x.top), base = m == kNone ? 0.f : m;
-        all.sum = all.sum * __builtin_amdgcn_exp2f((all.top - base) * s.sharp) +
-                  x.sum * __builtin_amdgcn_exp2f((x.top - base) * s.sharp);
-        if (x.top > all.top) all.first = x.first;  // slices come in order
-        all.top = m;
-      }
-      const float m = wave_max(all.top), base = m == kNone ? 0.f : m;
-      if (s.sharp > 0.f) {
-        const float total = wave_add(all.sum * __builtin_amdgcn_exp2f((all.top - base) * s.sharp));
-        mine.weigh(base, s.sharp);
-        mine.template write<PD>(a, row, v0, total == 0.f ? 0.f : 1.f / total, -1);
-      } else {
-        const int hot = wave_min(all.top == m ? all.first : INT32_MAX);
-        mine.template write<PD>(a, row, v0, 0.f, hot);
-      }
+  const int tid = threadIdx.x;
+  const int64_t begin = (int64_t)blockIdx.x * length;
+  length = (int)min((int64_t)length, a.vocab - begin);
+  const int64_t row = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (row >= a.total + a.B) return;
+  // What needs no more than the row goes out first.  A row of no sequence is
+  // found out behind it, and goes through the rest unwritten: with a branch here
+  // the compiler would put the loads behind it.
+  const Offsets offsets = load_offsets<WORDS>(a, row);
+  Mine<CHUNKS, kChunk, LD> mine;
+  const void* run = element<LD>(a.logits, row * a.logits_stride + begin);
+  const uint32_t* mask = mask_of(a, row);
+  mine.load(run, mask ? mask + (begin >> 5) : nullptr, 4 * tid, length);
+  if constexpr (WORDS) {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) *reinterpret_cast<u32x4*>(words + 4 * tid + kChunk * c) = u32x4{0u, 0u, 0u, 0u};
+  }
+  const Seq s = sequence(a, offsets, row);
+  if constexpr (WORDS) make_words<kThreads>(a, s, words, begin, length);
+  Slice of_row;
+  if constexpr (PART == kWrite) of_row = join_slices(slices + row * gridDim.x, gridDim.x, s.sharp);
+  mine.template adjust<WORDS>(a, s, words + 4 * tid);
+  if constexpr (PART == kWrite) {
+    if (s.sharp > 0.f) mine.weigh(of_row.top == kNone ? 0.f : of_row.top, s.sharp);
+  } else {
+    of_row = Slice{over_waves<kWaves>(wave_max(mine.top()), tops, [](float x, float y) { return fmaxf(x, y); }), 0.f, INT32_MAX, 0};
+    if (s.sharp > 0.f) {
+      const float sum = mine.weigh(of_row.top == kNone ? 0.f : of_row.top, s.sharp);
+      of_row.sum = over_waves<kWaves>(wave_add(sum), sums, [](float x, float y) { return x + y; });
     } else {
-      const float m = over_waves<kWaves>(wave_max(mine.top()), tops, [](float x, float y) { return fmaxf(x, y); });
-      Slice out{m, 0.f, INT32_MAX, 0};
-      if (s.sharp > 0.f) {
-        const float sum = mine.weigh(m == kNone ? 0.f : m, s.sharp);
-        out.sum = over_waves<kWaves>(wave_add(sum), sums, [](float x, float y) { return x + y; });
-      } else {
-        out.first = over_waves<kWaves>(wave_min(mine.first(v0, m)), firsts, [](int x, int y) { return min(x, y); });
-      }
-      if (threadIdx.x == 0) of_row[blockIdx.x] = out;
+      of_row.first = over_waves<kWaves>(wave_min(mine.first((int)begin + 4 * tid, of_row.top)), firsts, [](int x, int y) { return min(x, y); });
     }
-    if (j == last) return;
-    mine.load(a, row + 1, v0);
-    if constexpr (WORDS) {
-      __syncthreads();
-      if (threadIdx.x == 0) add_draft(a, s, j, words, begin, end);
-      __syncthreads();
-    }
+  }
+  if constexpr (PART == kStatistics) {
+    if (tid == 0) slices[row * gridDim.x + blockIdx.x] = of_row;
+  } else if (s.live) {
+    const int hot = s.sharp > 0.f ? -1 : of_row.first >= begin ? (int)min(of_row.first - begin, (int64_t)INT32_MAX) : INT32_MAX;
+    mine.template write<PD>(element<PD>(a.p, row * a.p_stride + begin), 4 * tid, length,
+                            of_row.sum == 0.f ? 0.f : 1.f / of_row.sum, hot);
   }
 }
 
 template <int LD, int PD, bool WORDS>
 hipError_t launch(const tb_token_probs_args& a, hipStream_t stream) {
+  Slice* of = static_cast<Slice*>(a.workspace);
+  const int64_t rows = a.total + a.B;
+  // rows in two dimensions, of which each has fewer than 2^16
+  const unsigned y = rows < 32768 ? (unsigned)rows : 32768u, z = (unsigned)((rows + y - 1) / y);
   if (a.vocab <= kProbsWhole) {
-    const dim3 grid((unsigned)a.max_draft + 1, (unsigned)a.B), block(1024);
-    if (a.vocab <= 4096) hipLaunchKernelGGL((whole_kernel<LD, PD, 1, WORDS>), grid, block, 0, stream, a);
-    else if (a.vocab <= 8192) hipLaunchKernelGGL((whole_kernel<LD, PD, 2, WORDS>), grid, block, 0, stream, a);
-    else if (a.vocab <= 16384) hipLaunchKernelGGL((whole_kernel<LD, PD, 4, WORDS>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((whole_kernel<LD, PD, 8, WORDS>), grid, block, 0, stream, a);
+    const dim3 grid(1, y, z), block(kRowThreads);
+    const int n = (int)a.vocab;
+    if (n <= 4096) hipLaunchKernelGGL((probs_kernel<LD, PD, 1, WORDS, kAll>), grid, block, 0, stream, a, of, n);
+    else if (n <= 8192) hipLaunchKernelGGL((probs_kernel<LD, PD, 2, WORDS, kAll>), grid, block, 0, stream, a, of, n);
+    else if (n <= 16384) hipLaunchKernelGGL((probs_kernel<LD, PD, 4, WORDS, kAll>), grid, block, 0, stream, a, of, n);
+    else hipLaunchKernelGGL((probs_kernel<LD, PD, 8, WORDS, kAll>), grid, block, 0, stream, a, of, n);
     return hipGetLastError();
   }
-  // Rows of a sequence share a workgroup, so that its lists are read once for
-  // them, but not so many that fewer than four workgroups are left for a CU.
-  const int64_t slices = (a.vocab + kProbsSlice - 1) / kProbsSlice, rows = a.max_draft + 1;
-  int64_t parts = (1024 + slices * a.B - 1) / (slices * a.B);
-  if (parts > rows) parts = rows;
-  const int per = (int)((rows + parts - 1) / parts);
-  const dim3 grid((unsigned)slices, (unsigned)a.B, (unsigned)((rows + per - 1) / per)), block(kThreads);
-  Slice* of = static_cast<Slice*>(a.workspace);
-  hipLaunchKernelGGL((slice_kernel<LD, PD, WORDS, false>), grid, block, 0, stream, a, of, per);
+  // slices of one length, in whole words of a mask
+  constexpr int kChunks = kProbsSlice / (4 * kSliceThreads);
+  const int64_t slices = (a.vocab + kProbsSlice - 1) / kProbsSlice;
+  const int length = (int)(((a.vocab + slices - 1) / slices + 31) / 32 * 32);
+  const dim3 grid((unsigned)slices, y, z), block(kSliceThreads);
+  hipLaunchKernelGGL((probs_kernel<LD, PD, kChunks, WORDS, kStatistics>), grid, block, 0, stream, a, of, length);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((slice_kernel<LD, PD, WORDS, true>), grid, block, 0, stream, a, of, per);
+  hipLaunchKernelGGL((probs_kernel<LD, PD, kChunks, WORDS, kWrite>), grid, block, 0, stream, a, of, length);
   return hipGetLastError();
 }
 
