@@ -37,29 +37,37 @@ __device__ __forceinline__ float channel(const u32x4& w, int d) {
 
 // The scale and offset of a position's channels in 4 bits (include/tb.h,
 // TB_INT4), and its codes: a group of LANES = D / 8 consecutive lanes holds a
-// position, 8 channels a lane.  In 64 bits: the scale rounds a quotient of 24
-// or more bits to 11, and a code a quotient by it, so that with 32 bits some of
-// 65536 rows get another scale, and with it other values in every channel.
+// position, 8 channels a lane, in 64 bits, or in 32 if they are exact there.
+// Scale and offset are found in 64: they round what has 24 bits or more to 11,
+// and by 32 some rows of 65536 would get another scale, and with it other values
+// in every channel.  A code is found in 32 bits: its quotient, at most 80, is
+// off by less than 2^-16, so that only one that near to the middle between two codes
+// has to be looked at in 64.
 struct Codes4 {
   uint32_t word;   // byte i: channels i (low) and i + 4 of the lane's eight
   uint32_t scale;  // fp16 bits: scale, and offset above it
 };
 constexpr double kLimit4 = 4096.0;
 
-template <int LANES>
-__device__ __forceinline__ Codes4 codes4(double (&x)[8]) {
+__device__ __forceinline__ float least(float a, float b) { return __builtin_fminf(a, b); }
+__device__ __forceinline__ float most(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double least(double a, double b) { return __builtin_fmin(a, b); }
+__device__ __forceinline__ double most(double a, double b) { return __builtin_fmax(a, b); }
+
+template <int LANES, typename F>
+__device__ __forceinline__ Codes4 codes4(F (&x)[8]) {
   bool nan = false;
-  double lo = kLimit4, hi = -kLimit4;
+  F lo = (F)kLimit4, hi = (F)-kLimit4;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     nan = nan || x[e] != x[e];
-    x[e] = x[e] > kLimit4 ? kLimit4 : x[e] < -kLimit4 ? -kLimit4 : x[e];
-    lo = x[e] < lo ? x[e] : lo;
-    hi = x[e] > hi ? x[e] : hi;
+    x[e] = most(least(x[e], (F)kLimit4), (F)-kLimit4);
+    lo = least(lo, x[e]);
+    hi = most(hi, x[e]);
   }
-  auto join = [&](double l, double h) {
-    lo = l < lo ? l : lo;
-    hi = h > hi ? h : hi;
+  auto join = [&](F l, F h) {
+    lo = least(lo, l);
+    hi = most(hi, h);
   };
   join(xor_lane<1>(lo), xor_lane<1>(hi));
   join(xor_lane<2>(lo), xor_lane<2>(hi));
@@ -69,25 +77,26 @@ __device__ __forceinline__ Codes4 codes4(double (&x)[8]) {
   const uint64_t group = ((uint64_t)1 << LANES) - 1;
   Codes4 r{0u, 0x7e007e00u};
   if ((__ballot(nan) >> (lane & ~(LANES - 1)) & group) != 0) return r;
-  const _Float16 sh = (_Float16)((hi - lo) / 15.0);
+  const _Float16 sh = (_Float16)(((double)hi - (double)lo) / 15.0);
   const double s = (double)sh;
-  const _Float16 oh = (_Float16)(lo - 64.0 * s);
-  const double o = (double)oh, inverse = 1.0 / s;
+  const _Float16 oh = (_Float16)((double)lo - 64.0 * s);
   r.scale = (uint32_t)__builtin_bit_cast(uint16_t, sh) | (uint32_t)__builtin_bit_cast(uint16_t, oh) << 16;
   if (!(s > 0.0)) return r;
+  const float inverse = 1.f / (float)sh, away = -(float)oh * inverse;
+  float n[8], far = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const double t = x[e] - o;
-    double n = __builtin_rint(t * inverse);
-    // the product is a step of 2^-53 off at most: what it may get wrong is a
-    // quotient next to, or at, the middle between two codes
-    const double twice = 2.0 * __builtin_fma(-n, s, t);
-    const bool odd = ((int)n & 1) != 0;
-    if (twice > s || (twice == s && odd)) n += 1.0;
-    else if (twice < -s || (twice == -s && odd)) n -= 1.0;
-    const int code = (int)n - 64;
-    r.word |= (uint32_t)(code < 0 ? 0 : code > 15 ? 15 : code) << (8 * (e & 3) + (e & 4));
+    const float q = __builtin_fmaf((float)x[e], inverse, away);
+    n[e] = __builtin_rintf(q);
+    far = __builtin_fmaxf(far, fabsf(q - n[e]));
   }
+  if (far > 0.5f - 0x1p-12f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n[e] = (float)__builtin_rint(((double)x[e] - (double)oh) / s);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    r.word |= (uint32_t)(int)__builtin_amdgcn_fmed3f(n[e] - 64.f, 0.f, 15.f) << (8 * (e & 3) + (e & 4));
   return r;
 }
 

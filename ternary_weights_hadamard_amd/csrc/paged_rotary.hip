@@ -25,6 +25,7 @@ constexpr int kTile = 64;      // positions of a workgroup of values
 constexpr int kTokens = 16;    // tokens of a workgroup of queries or keys, for chunks
 constexpr int kFew = 16;       // tokens a sequence up to which each group has one head
 constexpr int kRatio = kTile / kTokens;
+constexpr int kKeyHeads = 4;   // heads of a workgroup of keys, for chunks
 
 // cosine and sine of x
 struct Angle {
@@ -65,9 +66,6 @@ __device__ __forceinline__ Angle angle_of(double position, float f) {
   return a;
 }
 
-__device__ __forceinline__ float fused(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
-__device__ __forceinline__ double fused(double a, double b, double c) { return __builtin_fma(a, b, c); }
-
 // A lane's eight channels, rotated by a position: x -> x c + (its partner) s.
 template <typename F, int D>
 struct Rotation {
@@ -85,9 +83,10 @@ struct Rotation {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const Angle x = angle_of((double)position, a.inv_freq[(d0 + e) / 2]);
-        c[e] = c[e + 1] = (F)(x.c * (double)a.factor);
-        s[e + 1] = (F)(x.s * (double)a.factor);
-        s[e] = -s[e + 1];
+        const F cosine = (F)(x.c * (double)a.factor), sine = (F)(x.s * (double)a.factor);
+        c[e] = c[e + 1] = cosine;
+        s[e] = -sine;
+        s[e + 1] = sine;
       }
     } else {
 #pragma unroll
@@ -117,20 +116,16 @@ struct Rotation {
 };
 
 template <typename F>
-__device__ __forceinline__ void turn(F (&x)[8], int sub) {
-  fwht128_lanes(x, sub);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= (F)0x1.6a09e667f3bcdp-4;
-}
-
-template <typename F>
 __device__ __forceinline__ void unpack(const u32x4& w, F (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = (F)channel(w, e);
 }
 
+// nearest bf16 (ties to even), by the conversion that does two in one operation
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return f32_to_bf16_rne(a) | f32_to_bf16_rne(b) << 16;
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  const bf16x2 r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
 }
 
 // What a cache's codes are made from, and how: 8 channels a lane.
@@ -162,15 +157,17 @@ template <int C, int D>
 struct Codes {
   uint32_t w[C == TB_BF16 ? 4 : C == TB_FP8 ? 2 : 1];
   uint32_t scale;
-  __device__ __forceinline__ Codes(typename Made<C>::F (&x)[8], double inverse) {
+  template <typename F>
+  __device__ __forceinline__ Codes(F (&x)[8], double inverse) {
     if constexpr (C == TB_BF16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) w[i] = bf16_pair((float)x[2 * i], (float)x[2 * i + 1]);
     } else if constexpr (C == TB_FP8) {
+      float y[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        w[i] = fp8_pair((float)(x[4 * i] * inverse), (float)(x[4 * i + 1] * inverse)) |
-               fp8_pair((float)(x[4 * i + 2] * inverse), (float)(x[4 * i + 3] * inverse)) << 16;
+      for (int e = 0; e < 8; ++e) y[e] = (float)((double)x[e] * inverse);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = fp8_pair(y[4 * i], y[4 * i + 1]) | fp8_pair(y[4 * i + 2], y[4 * i + 3]) << 16;
     } else {
       const Codes4 r = codes4<D / 8>(x);
       w[0] = r.word;
@@ -178,6 +175,21 @@ struct Codes {
     }
   }
 };
+
+// A value's codes from 8 channels as they were loaded: in 32 bits they are exact
+// as long as they are not turned.
+template <int C, int D>
+__device__ __forceinline__ Codes<C, D> value_codes(const u32x4& w, bool turned, int sub, double inverse) {
+  if (D == 128 && turned) {
+    typename Made<C>::F x[8];
+    unpack(w, x);
+    fwht128_normal(x, sub);
+    return Codes<C, D>(x, inverse);
+  }
+  float x[8];
+  unpack(w, x);
+  return Codes<C, D>(x, inverse);
+}
 
 // one head's page of K: bytes, and the words of its scales
 template <int C, int D>
@@ -251,12 +263,162 @@ __device__ __forceinline__ void run_queries(const tb_paged_rotary_args& a, const
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (h + u * step >= end) continue;
-      if (D == 128 && a.turn_in) turn(x[u], sub);
+      if (D == 128 && a.turn_in) fwht128_normal(x[u], sub);
       rotate(a, x[u]);
-      if (D == 128 && a.turn_out) turn(x[u], sub);
+      if (D == 128 && a.turn_out) fwht128_normal(x[u], sub);
       *reinterpret_cast<u32x4*>(to + (int64_t)(h + u * step) * D) =
           u32x4{bf16_pair(x[u][0], x[u][1]), bf16_pair(x[u][2], x[u][3]), bf16_pair(x[u][4], x[u][5]),
                 bf16_pair(x[u][6], x[u][7])};
+    }
+  }
+}
+
+// Queries of chunks in the transform's basis, by matrix products.
+//
+// H = H4 x H32 (channel = 32 T + k): a wave has one head of 16 tokens as the
+// columns of H32 X (v_mfma 16x16x32; the entries of H are +-1 and those of X
+// bf16, so products are exact), and the four-point transform over T is eight additions
+// in a lane.  The rows of H32 are in the order that gives a lane the channels 32
+// T + 8 q + 0..7 of its token, as it loads and stores them and as the next
+// product takes them.  What is turned after the rotation goes in as the sum of
+// three bf16, which is fp32.  By butterflies between lanes, 24 additions and 32
+// exchanges a lane for 8 channels, the two transforms of the queries alone kept the vector
+// unit busy for longer than the bytes take.
+enum Pairs { kHalves128, kHalves64, kNeighbours };  // rotary_dim 128, 64; any
+
+__device__ __forceinline__ f32x4 mfma16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+template <Pairs PAIRS>
+__device__ __forceinline__ void run_queries_turned(const tb_paged_rotary_args& a, const Cut& cut, const PagedSeq& s, int n,
+                                                   int tile, int part) {
+  constexpr int D = 128;
+  if (tile * kTokens >= n) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q4 = lane >> 4;
+  const bool live = tile * kTokens + i16 < n;
+  const int tok = live ? tile * kTokens + i16 : n - 1;
+  int h = part * cut.q_heads + wave;
+  const int end = min((part + 1) * cut.q_heads, a.heads_q);
+  const uint16_t* from = static_cast<const uint16_t*>(a.q) + (s.row0 + tok) * a.q_stride + 8 * q4;
+  uint16_t* to = static_cast<uint16_t*>(a.q_out) + (s.row0 + tok) * a.heads_q * D + 8 * q4;
+  u32x4 w[4];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const u32x4*>(from + (int64_t)h * D + 32 * t);
+  };
+  if (h < end) load(h);
+
+  // H32 of the lane's row 8 (i16 / 4) + i16 % 4, and of the row 4 further, at columns 8 q4 + e
+  bf16x8 rows[2];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool odd = (__builtin_popcount((i16 & 3) & (e & 3)) + __builtin_popcount((i16 >> 2) & q4)) & 1;
+    rows[0][e] = (__bf16)(odd ? -1.f : 1.f);
+    rows[1][e] = (__bf16)(odd != (e >= 4) ? -1.f : 1.f);
+  }
+
+  // both transforms' factors go into cosine and sine (and the channels without them)
+  const float scale = (a.turn_in ? 0.08838834764831845f : 1.f) * (a.turn_out ? 0.08838834764831845f : 1.f);
+  constexpr int kAngles = PAIRS == kHalves64 ? 8 : 16;
+  float c[kAngles], sn[kAngles];
+  bool rotated[4];  // neighbours: the lane's channels of T
+#pragma unroll
+  for (int t = 0; t < 4; ++t) rotated[t] = 32 * t + 8 * q4 < a.rotary_dim;
+#pragma unroll
+  for (int i = 0; i < kAngles; ++i) {
+    const int at = PAIRS == kNeighbours ? 16 * (i >> 2) + 4 * q4 + (i & 3) : 32 * (i >> 3) + 8 * q4 + (i & 7);
+    c[i] = scale;
+    sn[i] = 0.f;
+    if (PAIRS != kNeighbours || rotated[i >> 2]) {
+      const Angle x = angle_of((double)((int64_t)s.first_pos + tok), a.inv_freq[at]);
+      c[i] = (float)(x.c * (double)a.factor) * scale;
+      sn[i] = (float)(x.s * (double)a.factor) * scale;
+    }
+  }
+
+  // the sum over T: P[T'] over the signs of T & T'
+  auto join = [](const f32x4 (&p)[4][2], float (&x)[4][8]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f32x4 a0 = p[0][u] + p[1][u], a1 = p[0][u] - p[1][u], b0 = p[2][u] + p[3][u], b1 = p[2][u] - p[3][u];
+      const f32x4 y[4] = {a0 + b0, a1 + b1, a0 - b0, a1 - b1};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[t][4 * u + e] = y[t][e];
+    }
+  };
+
+  for (; h < end; h += kThreads / 64) {
+    float x[4][8];
+    if (a.turn_in) {
+      f32x4 p[4][2];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p[t][u] = mfma16(rows[u], __builtin_bit_cast(bf16x8, w[t]), f32x4{0.f, 0.f, 0.f, 0.f});
+      join(p, x);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) unpack(w[t], x[t]);
+    }
+    if (h + kThreads / 64 < end) load(h + kThreads / 64);
+
+    if constexpr (PAIRS == kNeighbours) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          // 0 as a sine would make an infinity of its neighbour a NaN
+          const float ca = c[4 * t + e / 2], sa = sn[4 * t + e / 2], x0 = x[t][e], x1 = x[t][e + 1];
+          x[t][e] = rotated[t] ? fused(x0, ca, -(x1 * sa)) : x0 * ca;
+          x[t][e + 1] = rotated[t] ? fused(x1, ca, x0 * sa) : x1 * ca;
+        }
+    } else {
+      constexpr int kApart = PAIRS == kHalves128 ? 2 : 1;
+#pragma unroll
+      for (int t = 0; t < kApart; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float ca = c[8 * t + e], sa = sn[8 * t + e], x0 = x[t][e], x1 = x[t + kApart][e];
+          x[t][e] = fused(x0, ca, -(x1 * sa));
+          x[t + kApart][e] = fused(x1, ca, x0 * sa);
+        }
+#pragma unroll
+      for (int t = 2 * kApart; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[t][e] *= scale;
+    }
+
+    if (a.turn_out) {
+      f32x4 p[4][2];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        bf16x8 part[3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float r = x[t][e];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            part[i][e] = (__bf16)r;
+            r -= (float)part[i][e];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          p[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 2; i >= 0; --i) p[t][u] = mfma16(rows[u], part[i], p[t][u]);
+        }
+      }
+      join(p, x);
+    }
+    if (live) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<u32x4*>(to + (int64_t)h * D + 32 * t) =
+            u32x4{bf16_pair(x[t][0], x[t][1]), bf16_pair(x[t][2], x[t][3]), bf16_pair(x[t][4], x[t][5]), bf16_pair(x[t][6], x[t][7])};
     }
   }
 }
@@ -283,20 +445,21 @@ __device__ __forceinline__ void run_keys(const tb_paged_rotary_args& a, const Cu
   u32x4 w = load(h);
   const Rotation<F, D> rotate(a, sub, (int64_t)pos);
   for (; h < end; h += step) {
-    F x[8];
-    unpack(w, x);
+    const u32x4 now = w;
     if (h + step < end) w = load(h + step);
     const bool value = FEW && h >= c.heads_kv;
     const int head = value ? h - c.heads_kv : h;
-    if (D == 128 && (value ? a.turn_v : a.turn_in)) turn(x, sub);
-    if (!value) {
-      rotate(a, x);
-      if (D == 128 && a.turn_out) turn(x, sub);
-    }
     const double inverse = C == TB_FP8 ? 1.0 / (double)head_scale(value ? c.v_scale : c.k_scale, head) : 1.0;
-    const Codes<C, D> codes(x, inverse);
-    if (value) store_value<C, D>(c, at, head, sub, codes);
-    else store_key<C, D>(c, at, head, sub, codes);
+    if (value) {
+      store_value<C, D>(c, at, head, sub, value_codes<C, D>(now, a.turn_v, sub, inverse));
+      continue;
+    }
+    F x[8];
+    unpack(now, x);
+    if (D == 128 && a.turn_in) fwht128_normal(x, sub);
+    rotate(a, x);
+    if (D == 128 && a.turn_out) fwht128_normal(x, sub);
+    store_key<C, D>(c, at, head, sub, Codes<C, D>(x, inverse));
   }
 }
 
@@ -306,7 +469,6 @@ __device__ __forceinline__ void run_keys(const tb_paged_rotary_args& a, const Cu
 template <int D, int C>
 __device__ __forceinline__ void run_values(const tb_paged_rotary_args& a, int64_t b, const PagedSeq& s, int n, int vt,
                                            int head) {
-  typedef typename Made<C>::F F;
   typedef typename Made<C>::Elem Elem;
   constexpr int kLanes = D / 8, kRows = C == TB_INT4 ? D / 2 : D, kMine = kRows / kLanes;  // rows of a lane
   constexpr int kPiece = 16 / sizeof(Elem), kPieces = kTile / kPiece;
@@ -339,10 +501,7 @@ __device__ __forceinline__ void run_values(const tb_paged_rotary_args& a, int64_
     uint32_t codes[4][C == TB_BF16 ? 4 : C == TB_FP8 ? 2 : 1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      F x[8];
-      unpack(w[e], x);
-      if (D == 128 && a.turn_v) turn(x, sub);
-      const Codes<C, D> made(x, inverse);
+      const Codes<C, D> made = value_codes<C, D>(w[e], a.turn_v, sub, inverse);
 #pragma unroll
       for (int i = 0; i < (int)(sizeof(made.w) / 4); ++i) codes[e][i] = made.w[i];
       if (C == TB_INT4 && sub == e && at.page >= 0 && x0 + e >= lo && x0 + e < hi)
@@ -388,19 +547,27 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(tb_paged_rotary_args a
   const int x = blockIdx.x;
   int y = blockIdx.y;
   if ((int64_t)x * (FEW ? 1 : kTokens) >= n + (FEW ? 0 : 2 * kTile)) return;  // values reach into one more tile
-  if (y < cut.q_groups) {
-    run_queries<D>(a, cut, s, n, x, y);
-    return;
-  }
-  y -= cut.q_groups;
-  if (FEW || y < cut.kv_groups) {
-    run_keys<D, C, FEW>(a, cut, b, s, n, x, y);
-    return;
-  }
+  // the longest first
+  if (y < cut.kv_groups) return run_keys<D, C, FEW>(a, cut, b, s, n, x, y);
+  y -= cut.kv_groups;
   if constexpr (!FEW) {
-    const int head = kRatio * (y - cut.kv_groups) + x % kRatio;
-    if (head < c.heads_kv) run_values<D, C>(a, b, s, n, x / kRatio, head);
+    const int groups = (c.heads_kv + kRatio - 1) / kRatio;
+    if (y < groups) {
+      const int head = kRatio * y + x % kRatio;
+      if (head < c.heads_kv) run_values<D, C>(a, b, s, n, x / kRatio, head);
+      return;
+    }
+    y -= groups;
   }
+  if constexpr (D == 128 && !FEW) {
+    // pairs that are in one lane there; others go between lanes
+    if (a.turn_in || a.turn_out) {
+      if (a.neighbours || a.rotary_dim == 0) return run_queries_turned<kNeighbours>(a, cut, s, n, x, y);
+      if (a.rotary_dim == 128) return run_queries_turned<kHalves128>(a, cut, s, n, x, y);
+      if (a.rotary_dim == 64) return run_queries_turned<kHalves64>(a, cut, s, n, x, y);
+    }
+  }
+  run_queries<D>(a, cut, s, n, x, y);
 }
 
 int at_least(int64_t want, int most) { return want < 1 ? 1 : want > most ? most : (int)want; }
@@ -427,8 +594,8 @@ hipError_t launch(const tb_paged_rotary_args& a, hipStream_t stream) {
   const int parts = at_least((1024 + rows - 1) / rows, (a.heads_q + 3) / 4);
   cut.q_heads = a.q ? (a.heads_q + parts - 1) / parts : 1;
   cut.q_groups = a.q ? (a.heads_q + cut.q_heads - 1) / cut.q_heads : 0;
-  cut.kv_heads = 8;
-  cut.kv_groups = (c.heads_kv + 7) / 8;
+  cut.kv_heads = kKeyHeads;
+  cut.kv_groups = (c.heads_kv + kKeyHeads - 1) / kKeyHeads;
   const dim3 grid((unsigned)(tiles * kRatio), (unsigned)(cut.q_groups + cut.kv_groups + (c.heads_kv + kRatio - 1) / kRatio),
                   (unsigned)c.B);
   hipLaunchKernelGGL((rotary_kernel<D, C, false>), grid, dim3(kThreads), 0, stream, a, cut);
