@@ -412,10 +412,19 @@ __device__ __forceinline__ bool attn_rows_part(const tb_paged_attention_args& a,
           low_w[e] = (__bf16)(p - (float)w[e]);
         }
       }
+      if (INT4 && dropped) {  // apart, so that the products that are not rare stand in one run
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          V8 v = value_of(x, dt, nb);
+          take_nonfinite(v);
+          o[dt] = mfma16(v, w, o[dt]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        continue;
+      }
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        V8 v = value_of(x, dt, nb);
-        if (INT4 && dropped) take_nonfinite(v);
+        const V8 v = value_of(x, dt, nb);
         o[dt] = mfma16(v, w, o[dt]);
         if constexpr (C == TB_BF16) o[dt] = mfma16(v, low_w, o[dt]);
       }

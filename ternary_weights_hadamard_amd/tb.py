@@ -508,6 +508,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new(like, shape, dtype, stream):
+    """_empty on the device of a tensor, which is found faster from the tensor."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, like.device, stream)
+
+
 def _float_dt(t, what):
     d = _FLOATS.get(t.dtype)
     if d is None:
@@ -604,50 +611,64 @@ def tb_block_norm(y, resid=None, w_post=None, w_pre=None, gate=None, rows_per_ga
 def _token_rows(t, heads, d, where):
     """Elements between tokens of a [tokens, heads, d] tensor whose tokens are
     contiguous inside (a slice of a fused projection's output)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{where} must be bfloat16 [tokens, {heads}, {d}] (got {t.dtype} {tuple(t.shape)})")
-    if not t.is_cuda or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{where} must be bfloat16 [tokens, {heads}, {d}] (got {t.dtype} {tuple(shape)})")
+    if t.get_device() < 0 or stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{where}: a token's heads must be contiguous on the device")
-    return t.stride(0) if t.shape[0] > 1 else heads * d  # of one token it says nothing
+    return stride[0] if shape[0] > 1 else heads * d  # of one token it says nothing
+
+
+def _buffers(first, *ts):
+    """All contiguous, and on the device of `first` (the checks of _dev and
+    _same_device in two looks at a tensor)."""
+    index = first.get_device()
+    for t in ts:
+        if t is not None and (index < 0 or t.get_device() != index or not t.is_contiguous()):
+            _dev(t)
+            _same_device(first, t)
+            raise ValueError("buffers must be contiguous device tensors")
 
 
 def _paged_cache(where, tokens, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_scale, v_scale):
-    _dev(k_cache, v_cache, cu_q, kv_len, k_scale, v_scale)
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.dtype != v_cache.dtype:
+    _buffers(tokens, k_cache, v_cache, cu_q, kv_len, k_scale, v_scale)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.dtype != dtype:
         raise ValueError(f"{where}: k_cache must be [pages, heads, page, d], v_cache [pages, heads, d, page], one dtype")
-    pages, heads, page, d = k_cache.shape
+    pages, heads, page, d = shape
     if v_cache.shape != (pages, heads, d, page):
         raise ValueError(f"{where}: v_cache must be [{pages}, {heads}, {d}, {page}] (got {tuple(v_cache.shape)})")
-    if k_cache.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         kind = TB_BF16
-    elif k_cache.dtype == torch.float8_e4m3fn:
+    elif dtype == torch.float8_e4m3fn:
         kind = TB_FP8
-    elif k_cache.dtype == torch.uint8:
+    elif dtype == torch.uint8:
         kind, d = TB_INT4, 2 * d
     else:
-        raise TypeError(f"{where}: the cache must be bfloat16, float8_e4m3fn or uint8 (two 4-bit codes; got {k_cache.dtype})")
-    b = kv_len.shape[0]
+        raise TypeError(f"{where}: the cache must be bfloat16, float8_e4m3fn or uint8 (two 4-bit codes; got {dtype})")
     if not (cu_q.dtype == kv_len.dtype == block_table.dtype == torch.int32):
         raise TypeError(f"{where}: block_table, cu_q and kv_len must be int32")
-    if kv_len.dim() != 1 or cu_q.shape != (b + 1,) or block_table.dim() != 2 or block_table.shape[0] != b:
+    lens, table = kv_len.shape, block_table.shape
+    if len(lens) != 1 or cu_q.shape != (lens[0] + 1,) or len(table) != 2 or table[0] != lens[0]:
         raise ValueError(f"{where}: kv_len must be [B], cu_q [B + 1], block_table [B, entries]")
-    if not block_table.is_cuda or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    b, width = table
+    stride = block_table.stride()
+    if width > 1 and stride[1] != 1:
         raise ValueError(f"{where}: a sequence's block_table entries must be contiguous on the device")
     if kind == TB_INT4:
-        for sc, shape in ((k_scale, (pages, heads, page, 2)), (v_scale, (pages, heads, 2, page))):
-            if sc is None or sc.dtype != torch.float16 or sc.shape != shape:
+        for sc, of in ((k_scale, (pages, heads, page, 2)), (v_scale, (pages, heads, 2, page))):
+            if sc is None or sc.dtype != torch.float16 or sc.shape != of:
                 raise ValueError(f"{where}: a 4-bit cache needs k_scale float16 [{pages}, {heads}, {page}, 2] and v_scale "
                                  f"[{pages}, {heads}, 2, {page}]")
     else:
         for sc in (k_scale, v_scale):
             if sc is not None and (sc.dtype != torch.float32 or sc.shape != (heads,) or kind != TB_FP8):
                 raise ValueError(f"{where}: k_scale and v_scale must be float32 [{heads}], of an 8-bit cache")
-    _same_device(tokens, k_cache, v_cache, block_table, cu_q, kv_len, k_scale, v_scale)
-    width = block_table.shape[1]
-    stride = block_table.stride(0) if b > 1 else width
+    if block_table.get_device() != tokens.get_device():
+        _same_device(tokens, block_table)
     return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
-                      cu_q.data_ptr(), kv_len.data_ptr(), pages, stride, width, b, tokens.shape[0], max_q, kind, page,
-                      heads, d)
+                      cu_q.data_ptr(), kv_len.data_ptr(), pages, stride[0] if b > 1 else width, width, b, tokens.shape[0],
+                      max_q, kind, page, heads, d)
 
 
 def tb_paged_append(k, v, k_cache, v_cache, block_table, cu_q, kv_len, max_q, k_scale=None, v_scale=None, stream=None):
@@ -687,7 +708,7 @@ def tb_paged_append_rotary(q, k, v, k_cache, v_cache, block_table, cu_q, kv_len,
         raise ValueError(f"{where}: k and v differ in tokens")
     rotary = 0
     if inv_freq is not None:
-        _dev(inv_freq)
+        _buffers(k, inv_freq)
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
             raise ValueError(f"{where}: inv_freq must be float32 [rotary_dim / 2]")
         rotary = 2 * inv_freq.shape[0]
@@ -701,11 +722,12 @@ def tb_paged_append_rotary(q, k, v, k_cache, v_cache, block_table, cu_q, kv_len,
         if not (q.shape[0] == k.shape[0]):
             raise ValueError(f"{where}: q and k differ in tokens")
         if q_out is None:
-            q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
-        _dev(q_out)
-        if not (q_out.dtype == torch.bfloat16 and q_out.shape == q.shape):
-            raise ValueError(f"{where}: q_out must be bfloat16 {tuple(q.shape)}")
-    _same_device(k, v, q, q_out, inv_freq)
+            q_out = _new(q, q.shape, torch.bfloat16, stream)
+        else:
+            _buffers(k, q_out)
+            if not (q_out.dtype == torch.bfloat16 and q_out.shape == q.shape):
+                raise ValueError(f"{where}: q_out must be bfloat16 {tuple(q.shape)}")
+    _same_device(k, v, q)
     args = PagedRotaryArgs(cache, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), _addr(inv_freq), qs, ks, vs, heads,
                            rotary, int(neighbours), int(turn_in), int(turn_out), int(turn_v), factor, 0)
     _check(lib().tb_paged_append_rotary(args, _stream(stream)), where)
@@ -742,7 +764,7 @@ def tb_paged_read(k_cache, v_cache, block_table, cu_q, kv_len, total, max_q, k_s
             out_dtype = t.dtype
             if not (t.shape == shape):
                 raise ValueError(f"{where}: k and v must be {list(shape)}")
-    made = [t if t is not None else _empty(shape, out_dtype, k_cache.device, stream) for t in (k, v)]
+    made = [t if t is not None else _new(k_cache, shape, out_dtype, stream) for t in (k, v)]
     if not (made[0].dtype == made[1].dtype):
         raise ValueError(f"{where}: k and v differ in dtype")
     _same_device(k_cache, *made)
@@ -789,7 +811,7 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
         if not (out.shape == q.shape):
             raise ValueError(f"tb_paged_attention: out must be {tuple(q.shape)}")
     else:
-        out = _empty(q.shape, out_dtype, q.device, stream)
+        out = _new(q, q.shape, out_dtype, stream)
         out_dt = _float_dt(out, "tb_paged_attention: out")
     args = _attention_args(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale, window, k_scale,
                            v_scale, out_dt)
@@ -798,12 +820,12 @@ def tb_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, ma
         if not (lse.dtype == torch.float32 and lse.shape == q.shape[:2]):
             raise ValueError(f"tb_paged_attention: lse must be float32 {tuple(q.shape[:2])}")
     elif with_lse:
-        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
+        lse = _new(q, q.shape[:2], torch.float32, stream)
     L = lib()
     if workspace is None:
         nbytes = L.tb_paged_attention_workspace(args)
         if nbytes:
-            workspace = _empty(nbytes, torch.uint8, q.device, stream)
+            workspace = _new(q, nbytes, torch.uint8, stream)
     else:
         _dev(workspace)
     _same_device(q, out, lse, workspace)
@@ -895,7 +917,7 @@ def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, hist
     [rows] (-1: none; None: mask r for row r).  Returns p [rows, vocab]; rows of
     no sequence are left as they are."""
     where = "tb_token_probs"
-    _dev(params, drafts, cu_draft, history, cu_history, prompt_len, mask_row, workspace)
+    _buffers(logits, params, drafts, cu_draft, history, cu_history, prompt_len, mask_row, workspace)
     max_draft = int(max_draft)
     if not (params.dtype == torch.float32 and params.dim() == 2 and params.shape[1] == 4):
         raise ValueError(f"{where}: params must be float32 [B, 4]")
@@ -917,7 +939,7 @@ def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, hist
     ids = values = cu_bias = None
     if bias is not None:
         ids, values, cu_bias = bias
-        _dev(ids, values, cu_bias)
+        _buffers(logits, ids, values, cu_bias)
         _token_list(where, "bias", ids, cu_bias, b)
         n_bias = ids.shape[0]
         if not (values.dtype == torch.float32 and values.shape == ids.shape):
@@ -937,7 +959,7 @@ def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, hist
     elif mask_row is not None:
         raise ValueError(f"{where}: mask_row needs mask")
     if p is None:
-        p = _empty((rows, vocab), out_dtype, logits.device, stream)
+        p = _new(logits, (rows, vocab), out_dtype, stream)
     ps = _prob_rows(p, where + ": p")
     if not (p.shape == (rows, vocab)):
         raise ValueError(f"{where}: p must be [{rows}, {vocab}]")
@@ -949,9 +971,8 @@ def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, hist
     if workspace is None:
         nbytes = L.tb_token_probs_workspace(args)
         if nbytes:
-            workspace = _empty(nbytes, torch.uint8, logits.device, stream)
-    _same_device(logits, params, drafts, cu_draft, history, cu_history, prompt_len, ids, values, cu_bias, mask, mask_row, p,
-                 workspace)
+            workspace = _new(logits, nbytes, torch.uint8, stream)
+    _same_device(logits, mask, p)
     if workspace is not None:
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(L.tb_token_probs(args, _stream(stream)), where)
