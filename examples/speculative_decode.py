@@ -8,17 +8,22 @@ rotated basis, and the operators between them stay in it:
   tb_block_norm       residual, norm and both rotations between two products
   tb_ternary_gemm     queries, keys and values of 128-wide heads stay rotated:
                       scores do not change, and the output projection takes
-                      rotated inputs (rotary positions, which this decoder does
-                      not have, would need queries and keys rotated back first)
+                      rotated inputs
   tb_paged_append     the new keys and values into the pages of the cache
+  tb_paged_append_rotary  (--rotary) the same with positions: queries and keys are
+                      rotated back for them, and into the products' basis again,
+                      where a cache of few bits loses least
   tb_paged_attention  the new tokens over their sequence's pages
+  tb_token_probs      the target's probabilities: penalties of tokens that a
+                      sequence has had, tokens that are not allowed, temperature
   tb_verify_draft     which drafts are kept, and the token drawn after them
 
 The drafter is the model without its layers: it draws from what the last
 token's embedding alone gives.  A draft that is not kept leaves its key and
 value in the cache; the next step's tokens are written over them.
 
-  python examples/speculative_decode.py [--steps 32] [--max-draft 4] [--cache bf16|fp8]
+  python examples/speculative_decode.py [--steps 32] [--max-draft 4] [--cache bf16|fp8|int4] [--rotary 10000]
+                                        [--repeats 1.1] [--presence 0.5] [--frequency 0.2]
 """
 
 import argparse
@@ -47,6 +52,11 @@ class Config:
     cache: str = "bf16"
     temperature: float = 0.5
     sure: float = 0.05  # the drafter stops where its likeliest token has less
+    rotary: float = 0.0  # base of the rotary positions' frequencies; 0: no positions
+    repeats: float = 1.0  # penalties, of tokens in the sequence, and of its
+    presence: float = 0.0  # generated ones: once, and
+    frequency: float = 0.0  # for each time
+    banned: tuple = ()  # tokens that are never drawn
 
 
 class Decoder:
@@ -69,15 +79,29 @@ class Decoder:
 
         # Pages are handed out in any order; a sequence keeps a table of its own.
         each = -(-max_tokens // c.page)
-        kind = torch.bfloat16 if c.cache == "bf16" else torch.float8_e4m3fn
+        kind = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int4": torch.uint8}[c.cache]
+        wide = HEAD_DIM // 2 if c.cache == "int4" else HEAD_DIM  # two 4-bit codes a byte
         self.max_tokens, pages = each * c.page, batch * each
+        scale8 = None if c.cache != "fp8" else torch.full((c.heads_kv,), 1.0 / 32, device=device)
         for layer in self.layers:
-            layer["k"] = torch.zeros((pages, c.heads_kv, c.page, HEAD_DIM), device=device).to(kind)
-            layer["v"] = torch.zeros((pages, c.heads_kv, HEAD_DIM, c.page), device=device).to(kind)
+            layer["k"] = torch.zeros((pages, c.heads_kv, c.page, wide), device=device).to(kind)
+            layer["v"] = torch.zeros((pages, c.heads_kv, wide, c.page), device=device).to(kind)
+            layer["scales"] = dict(k_scale=scale8, v_scale=scale8)
+            if c.cache == "int4":  # a scale and an offset for each position and head
+                half = lambda *shape: torch.zeros(shape, dtype=torch.float16, device=device)  # noqa: E731
+                layer["scales"] = dict(k_scale=half(pages, c.heads_kv, c.page, 2), v_scale=half(pages, c.heads_kv, 2, c.page))
         order = torch.randperm(pages, generator=gen, device=device)
         self.table = order.view(batch, each).to(torch.int32)
-        self.scale8 = None if c.cache == "bf16" else torch.full((c.heads_kv,), 1.0 / 32, device=device)
+        self.freq = tb.tb_rotary_frequencies(HEAD_DIM, c.rotary)[0].to(device) if c.rotary else None
+        self.params = torch.tensor([[c.temperature, c.repeats, c.presence, c.frequency]] * batch, device=device)
+        self.mask = None
+        if c.banned:
+            allowed = torch.ones(-(-c.vocab // 32) * 32, dtype=torch.int64)
+            allowed[list(c.banned)] = 0
+            words = (allowed.view(-1, 32) << torch.arange(32)).sum(1)
+            self.mask = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)[None].to(device)
         self.tokens = [[] for _ in range(batch)]
+        self.prompt = [0] * batch
         self.random = torch.Generator(device=device).manual_seed(seed + 1)
 
     def _ints(self, values):
@@ -95,14 +119,17 @@ class Decoder:
             raise ValueError(f"a sequence of {max(ends)} tokens: there is room for {self.max_tokens}")
         max_q = max(len(n) for n in new)
         where = (self.table, self._ints(cu), self._ints(ends))
-        scales = dict(k_scale=self.scale8, v_scale=self.scale8)
         h = self.embedding[torch.tensor([t for n in new for t in n], device=self.device)]
         _, z = tb.tb_block_norm(None, h, w_pre=self.layers[0]["norm"], rotate_out=True)
         for i, w in enumerate(self.layers):
             qkv = tb.tb_ternary_gemm(z, *w["qkv"]).view(-1, c.heads + 2 * c.heads_kv, HEAD_DIM)
             q, k, v = qkv.split([c.heads, c.heads_kv, c.heads_kv], dim=1)
-            tb.tb_paged_append(k, v, w["k"], w["v"], *where, max_q, **scales)
-            o = tb.tb_paged_attention(q, w["k"], w["v"], *where, max_q, max(ends), **scales)
+            if self.freq is None:
+                tb.tb_paged_append(k, v, w["k"], w["v"], *where, max_q, **w["scales"])
+            else:
+                q = tb.tb_paged_append_rotary(q, k, v, w["k"], w["v"], *where, max_q, self.freq, turn_in=True, turn_out=True,
+                                              **w["scales"])
+            o = tb.tb_paged_attention(q, w["k"], w["v"], *where, max_q, max(ends), **w["scales"])
             y = tb.tb_ternary_gemm(o.view(-1, c.heads * HEAD_DIM), *w["out"], out_dtype=torch.float32)
             _, z = tb.tb_block_norm(y, h, w_pre=w["norm2"], rotate_in=True, rotate_out=True, h=h)
             up, gate = tb.tb_ternary_gemm_rotated(z, *w["up"]), tb.tb_ternary_gemm_rotated(z, *w["gate"])
@@ -120,14 +147,22 @@ class Decoder:
     def probabilities(self, logits):
         return torch.softmax(logits / self.config.temperature, dim=-1)
 
-    def _verify(self, p, q, drafts, max_draft):
+    def _offsets(self, lists):
         cu = [0]
-        for d in drafts:
-            cu.append(cu[-1] + len(d))
+        for x in lists:
+            cu.append(cu[-1] + len(x))
+        return cu
+
+    def _verify(self, logits, q, drafts, max_draft, so_far):
+        """`so_far`: the sequences' tokens before their drafts."""
+        cu = self._offsets(drafts)
+        ids, offsets = self._ints([t for d in drafts for t in d]), self._ints(cu)
+        mask = {} if self.mask is None else dict(mask=self.mask, mask_row=self._ints([0] * logits.shape[0]))
+        p = tb.tb_token_probs(logits, self.params, ids, offsets, max_draft, history=self._ints([t for s in so_far for t in s]),
+                              cu_history=self._ints(self._offsets(so_far)), prompt_len=self._ints(self.prompt), **mask)
         u = torch.rand(cu[-1], generator=self.random, device=self.device)
         u_next = torch.rand(len(drafts), generator=self.random, device=self.device)
-        return tb.tb_verify_draft(p, q, self._ints([t for d in drafts for t in d]), u, u_next, self._ints(cu),
-                                  max_draft)
+        return tb.tb_verify_draft(p, q, ids, u, u_next, offsets, max_draft)
 
     def prefill(self, prompts):
         """Start the batch: the prompts' keys and values, and a first token of
@@ -135,7 +170,8 @@ class Decoder:
         logits = self.forward(prompts)
         ends = torch.tensor([len(p) for p in prompts], device=self.device).cumsum(0) - 1
         logits = logits[ends]
-        _, drawn = self._verify(self.probabilities(logits), None, [[] for _ in prompts], 0)
+        self.prompt = [len(p) for p in prompts]
+        _, drawn = self._verify(logits, None, [[] for _ in prompts], 0, prompts)
         self.tokens = [list(p) + t for p, t in zip(prompts, drawn.tolist())]
         return logits
 
@@ -167,7 +203,7 @@ class Decoder:
         drafts, q = self.draft(max_draft)
         new = [t[-1:] + d for t, d in zip(self.tokens, drafts)]
         logits = self.forward(new)
-        kept, out = self._verify(self.probabilities(logits), q, drafts, max_draft)
+        kept, out = self._verify(logits, q, drafts, max_draft, self.tokens)
         first = torch.tensor([0] + [len(n) for n in new[:-1]], device=self.device).cumsum(0)
         for t, n, row in zip(self.tokens, kept.tolist(), out.tolist()):
             t += row[:n + 1]
@@ -186,9 +222,14 @@ def main():
     ap.add_argument("--prompt", type=int, default=200, help="longest prompt")
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--max-draft", type=int, default=4)
-    ap.add_argument("--cache", choices=["bf16", "fp8"], default="bf16")
+    ap.add_argument("--cache", choices=["bf16", "fp8", "int4"], default="bf16")
+    ap.add_argument("--rotary", type=float, default=0.0, help="base of the positions' frequencies (0: no positions)")
+    ap.add_argument("--repeats", type=float, default=1.0)
+    ap.add_argument("--presence", type=float, default=0.0)
+    ap.add_argument("--frequency", type=float, default=0.0)
     args = ap.parse_args()
-    config = Config(cache=args.cache)
+    config = Config(cache=args.cache, rotary=args.rotary, repeats=args.repeats, presence=args.presence,
+                    frequency=args.frequency)
     decoder = Decoder(config, args.batch, args.prompt + 1 + args.steps * (args.max_draft + 1))
     prompts = prompts_of(args.batch, args.prompt, config.vocab)
     decoder.prefill(prompts)
