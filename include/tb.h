@@ -879,7 +879,7 @@ TB_API tb_status tb_verify_draft(const tb_verify_draft_args* args, void* stream)
  *   history  int32 [total_history], or NULL (none): tokens cu_history[b] ..
  *           cu_history[b + 1] - 1 are sequence b's; the first prompt_len[b] of
  *           them (int32 [B]; NULL: 0) are its prompt's, which count as
- *           repeated, not as generated.  At most 2^20 - 64 generated tokens of
+ *           repeated, not as generated.  At most 2^20 - 65 generated tokens of
  *           a sequence are counted, the last ones
  *   bias_ids int32, bias_values fp32 [total_bias], cu_bias int32 [B + 1], or
  *           all NULL (bias 0): sequence b's biased tokens; of an id that is

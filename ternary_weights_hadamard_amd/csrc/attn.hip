@@ -174,7 +174,10 @@ AttnPlan plan_of(const tb_paged_attention_args& a) {
   p.rows_line.slot_rows = kRowsTile;
   p.chunk_line.least = 4;
   p.chunk_line.slot_rows = kChunkTile;
-  if (has_rows(a, p) && keys > p.rows_line.least * rows_positions(c.cache_dtype)) p.rows_line.pieces = kPieces;
+  // 4 bits: up to 16 tiles one after another take no longer than pieces and their
+  // join (one sequence of 1000, 40 heads: 12.3 us against 14.3; of 1500: 15.4 against 14.6).
+  const int64_t uncut = c.cache_dtype == TB_INT4 ? 16 : p.rows_line.least;
+  if (has_rows(a, p) && keys > uncut * rows_positions(c.cache_dtype)) p.rows_line.pieces = kPieces;
   // Chunks whose items fill the GPU are not cut: one after another, the row
   // tiles of a head find its keys and values in L2, while pieces of a line are
   // all elsewhere (4 x 2048 tokens over 8192, 40 heads, an earlier form of the

@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(tb_paged_cache c, void* 
 
 hipError_t launch_paged_read(const tb_paged_cache& c, void* k_out, void* v_out, int out_dtype, hipStream_t stream) {
   // positions that do not start on a tile reach into one more
-  const dim3 grid((unsigned)((c.max_q + kTile - 1) / kTile + 1), (unsigned)c.heads_kv, (unsigned)c.B), block(kThreads);
+  const int64_t most = c.max_q < c.total_q ? c.max_q : c.total_q;
+  const dim3 grid((unsigned)((most + kTile - 1) / kTile + 1), (unsigned)c.heads_kv, (unsigned)c.B), block(kThreads);
   const bool wide = c.head_dim == 128;
   switch (c.cache_dtype) {
     case TB_BF16:

@@ -576,13 +576,14 @@ template <int D, int C>
 hipError_t launch(const tb_paged_rotary_args& a, hipStream_t stream) {
   const tb_paged_cache& c = a.cache;
   constexpr int kGroups = kThreads / (D / 8);
+  const int64_t most = c.max_q < c.total_q ? c.max_q : c.total_q;  // tokens of a sequence
   Cut cut{};
-  if (c.max_q <= kFew) {
+  if (most <= kFew) {
     cut.tokens = 1;
     cut.q_heads = cut.kv_heads = kGroups;
     cut.q_groups = a.q ? (a.heads_q + kGroups - 1) / kGroups : 0;
     cut.kv_groups = (2 * c.heads_kv + kGroups - 1) / kGroups;
-    const dim3 grid((unsigned)c.max_q, (unsigned)(cut.q_groups + cut.kv_groups), (unsigned)c.B);
+    const dim3 grid((unsigned)most, (unsigned)(cut.q_groups + cut.kv_groups), (unsigned)c.B);
     hipLaunchKernelGGL((rotary_kernel<D, C, true>), grid, dim3(kThreads), 0, stream, a, cut);
     return hipGetLastError();
   }
@@ -590,7 +591,7 @@ hipError_t launch(const tb_paged_rotary_args& a, hipStream_t stream) {
   // A chunk that does not start on a tile reaches into one more.  Heads are
   // shared out until there are four workgroups for each of 256 CUs, but at
   // least four to one, which finds its angles for them.
-  const int64_t tiles = (c.max_q + kTile - 1) / kTile + 1, rows = tiles * kRatio * c.B;
+  const int64_t tiles = (most + kTile - 1) / kTile + 1, rows = tiles * kRatio * c.B;
   const int parts = at_least((1024 + rows - 1) / rows, (a.heads_q + 3) / 4);
   cut.q_heads = a.q ? (a.heads_q + parts - 1) / parts : 1;
   cut.q_groups = a.q ? (a.heads_q + cut.q_heads - 1) / cut.q_heads : 0;

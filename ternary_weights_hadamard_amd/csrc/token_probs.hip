@@ -179,7 +179,7 @@ __device__ __forceinline__ void make_words(const tb_token_probs_args& a, const S
   if (tid < s.biases) biased = a.bias_ids[s.bias + tid];
   __syncthreads();
   // no more than the count has room for, with all drafts
-  const int64_t counted = max(s.made, s.end - ((1 << 20) - TB_MAX_DRAFT));
+  const int64_t counted = max(s.made, s.end - ((int64_t)kCount - TB_MAX_DRAFT));
   // where an id is in the run: a negative id is far past it
   auto place = [&](int32_t id) { return (uint32_t)id - (uint32_t)begin; };
   auto note = [&](int32_t id, int64_t i) {

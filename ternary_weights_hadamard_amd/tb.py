@@ -190,6 +190,16 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_on(t, stream, where):
+    """The stream of a call whose tensors are on t's device, which has to be the
+    current one (kernels are launched on that)."""
+    index = t.get_device()
+    now = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    if index != now or (stream is not None and stream.device_index != index):
+        raise ValueError(f"{where}: the tensors are on device {index}, which must be the current one ({now}) and the stream's")
+    return _stream(stream)
+
+
 def _dt(t):
     if t.dtype == torch.float32:
         return TB_F32
@@ -730,7 +740,7 @@ def tb_paged_append_rotary(q, k, v, k_cache, v_cache, block_table, cu_q, kv_len,
     _same_device(k, v, q)
     args = PagedRotaryArgs(cache, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), _addr(inv_freq), qs, ks, vs, heads,
                            rotary, int(neighbours), int(turn_in), int(turn_out), int(turn_v), factor, 0)
-    _check(lib().tb_paged_append_rotary(args, _stream(stream)), where)
+    _check(lib().tb_paged_append_rotary(args, _stream_on(k, stream, where)), where)
     return q_out
 
 
@@ -769,7 +779,7 @@ def tb_paged_read(k_cache, v_cache, block_table, cu_q, kv_len, total, max_q, k_s
         raise ValueError(f"{where}: k and v differ in dtype")
     _same_device(k_cache, *made)
     _check(lib().tb_paged_read(cache, made[0].data_ptr(), made[1].data_ptr(), _float_dt(made[0], where + ": k and v"),
-                               _stream(stream)), where)
+                               _stream_on(k_cache, stream, where)), where)
     return made[0], made[1]
 
 
@@ -975,5 +985,5 @@ def tb_token_probs(logits, params, drafts=None, cu_draft=None, max_draft=0, hist
     _same_device(logits, mask, p)
     if workspace is not None:
         args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(L.tb_token_probs(args, _stream(stream)), where)
+    _check(L.tb_token_probs(args, _stream_on(logits, stream, where)), where)
     return p

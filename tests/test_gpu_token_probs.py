@@ -271,7 +271,7 @@ def test_long_history():
     n = (1 << 20) + 500
     c = Case([1], 64, history=0, bias=0, masks=False)
     c.params[:] = [1.0, 1.3, 0.1, 1e-6]
-    early, most = 7, (1 << 20) - 64
+    early, most = 7, (1 << 20) - 65
     history = torch.full((n + 1,), 3, dtype=torch.int32, device=DEV)
     history[0] = early                                      # the prompt
     history[1:101] = 9                                      # generated, but too long ago
@@ -279,6 +279,12 @@ def test_long_history():
                           cu_history=ints([0, n + 1]), prompt_len=ints([1]))
     c.drafts, c.history, c.prompt = np.array([9]), [[early] + [3] * most], [1]
     c.check(p, "long")
+    # the most that a count can come to: all of them and 64 drafts the same
+    c = Case([64], 64, history=0, bias=0, masks=False)
+    c.bias = [[(3, 2.5), (9, 1.5)]]
+    c.params[:] = [1.0, 1.3, 0.1, 1e-6]
+    c.drafts, c.history, c.prompt = np.full(64, 3), [[early] + [3] * most], [1]
+    c.check(c.run(history=history, cu_history=ints([0, n + 1]), prompt_len=ints([1])), "largest count")
 
 
 def test_feeds_the_verification():
