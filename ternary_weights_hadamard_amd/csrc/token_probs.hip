@@ -244,6 +244,9 @@ __device__ __forceinline__ f32x4 load4(const void* row, int at, int n) {
   return v;
 }
 
+// The same of p, past the caches: of it little is read again (a verification reads
+// a row of each sequence), and the logits stay in them for the second launch (72
+// rows over 131073 in bf16 under masks: 24.5 -> 22.4 us).
 template <int DTYPE>
 __device__ __forceinline__ void store4(void* row, int at, int n, const f32x4& v) {
   if constexpr (DTYPE == TB_BF16) {
@@ -253,7 +256,7 @@ __device__ __forceinline__ void store4(void* row, int at, int n, const f32x4& v)
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint16_t)f32_to_bf16_rne(v[e]);
     if (n >= 4) {
-      *reinterpret_cast<u16x4*>(to + at) = w;
+      __builtin_nontemporal_store(w, reinterpret_cast<u16x4*>(to + at));
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
@@ -263,7 +266,7 @@ __device__ __forceinline__ void store4(void* row, int at, int n, const f32x4& v)
     typedef float __attribute__((ext_vector_type(4), aligned(4))) f32x4u;
     float* to = static_cast<float*>(row);
     if (n >= 4) {
-      *reinterpret_cast<f32x4u*>(to + at) = f32x4u{v[0], v[1], v[2], v[3]};
+      __builtin_nontemporal_store(f32x4u{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4u*>(to + at));
     } else {
 #pragma unroll
       for (int e = 0; e < 3; ++e)
