@@ -735,7 +735,8 @@ TB_API tb_status tb_paged_attention(const tb_paged_attention_args* args, void* s
  * Angles are formed and reduced in 64 bits.  Queries, and the keys of a bf16
  * cache, are computed in fp32, with cosine and sine correct to fp32's step at
  * 1; keys and values of the other caches in 64 bits, so that their codes are
- * those of the formula but for ties that 64 bits do not tell.  A token at a
+ * those of the formula but for ties that 64 bits do not tell (TB_FP8: that the
+ * quotient, rounded to fp32 on the way, does not tell).  A token at a
  * negative position is rotated by it all the same (its key has no place).
  */
 typedef struct {

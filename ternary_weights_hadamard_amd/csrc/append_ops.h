@@ -40,9 +40,10 @@ __device__ __forceinline__ float channel(const u32x4& w, int d) {
 // position, 8 channels a lane, in 64 bits, or in 32 if they are exact there.
 // Scale and offset are found in 64: they round what has 24 bits or more to 11,
 // and by 32 some rows of 65536 would get another scale, and with it other values
-// in every channel.  A code is found in 32 bits: its quotient, at most 80, is
-// off by less than 2^-16, so that only one that near to the middle between two codes
-// has to be looked at in 64.
+// in every channel.  A code is found in 32 bits, as x / scale + away with away =
+// -offset / scale: of a quotient that is at most 80, less than 2^-12 is lost, and of
+// away and of x / scale, which far from 0 are large and cancel, 2^-24 each.  Only
+// one that may be that near to the middle between two codes is looked at in 64.
 struct Codes4 {
   uint32_t word;   // byte i: channels i (low) and i + 4 of the lane's eight
   uint32_t scale;  // fp16 bits: scale, and offset above it
@@ -90,7 +91,7 @@ __device__ __forceinline__ Codes4 codes4(F (&x)[8]) {
     n[e] = __builtin_rintf(q);
     far = __builtin_fmaxf(far, fabsf(q - n[e]));
   }
-  if (far > 0.5f - 0x1p-12f) {
+  if (far > 0.5f - __builtin_fmaf(fabsf(away), 0x1p-22f, 0x1p-12f)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) n[e] = (float)__builtin_rint(((double)x[e] - (double)oh) / s);
   }

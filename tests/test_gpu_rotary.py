@@ -155,6 +155,20 @@ def test_far_positions(cache):
     r.check(r.run())
 
 
+@pytest.mark.parametrize("lens", [[(70, 70), (200, 300)], [(16, 90), (9, 70), (3, 3), (16, 16), (16, 40)]])
+def test_codes_far_from_zero(lens):
+    """One channel far above the others becomes, turned, the same large number in
+    every channel with a little on it: up to thousands of steps from 0."""
+    say(f"far from zero {lens}")
+    r = Rotary(lens, 2, 8, 128, 64, "int4", 0, turn=(False, True, True), seed=11)
+    for t in (r.c.new_k, r.c.new_v):
+        t.mul_(0.25)
+        n = t.shape[0] * t.shape[1]
+        t[..., 0] = torch.linspace(100.0, 45000.0, n, device=DEV).view(t.shape[:2]).to(torch.bfloat16)
+        t[::2, :, 0].neg_()
+    r.check(r.run())
+
+
 def test_without_queries_and_in_place():
     say("rotary without queries")
     for lens in ([(3, 30)], [(40, 60)]):
