@@ -11,6 +11,15 @@
 //   values    64 positions of one head, turned in LDS: pages hold [d][position]
 // With few tokens a sequence (at most kFew) a group has one head, and values are
 // stored as they come, a code at a time: no turn through LDS, no barrier.
+//
+// What bounds it.  A step: launch and dependent loads (1 token of 40 + 8 heads
+// 3.8 us; 16 of 40 + 8 into 4 bits 6.6 us).  A chunk into bf16 or e4m3: HBM (4 x up to
+// 2048 tokens of 40 + 8 heads, 106 MB in 23.9 us, 4.4 TB/s; a plain copy moves
+// 5.2).  A chunk into 4 bits with transforms (40 + 8 heads, 103 MB in 41 us): the
+// vector unit, whose 64-bit operations find the scales and offsets of K and V;
+// the queries' transforms are matrix products there (run_queries_turned: 60 -> 48
+// us together with codes found in 32 bits) and keys, the longest, come first with
+// 4 heads a workgroup (48 -> 41; 2 and 8 heads were slower).
 #include "append_ops.h"
 #include "fwht_lanes.h"
 #include "paged.h"
