@@ -38,31 +38,33 @@ __device__ __forceinline__ float channel(const u32x4& w, int d) {
 // The scale and offset of a position's channels in 4 bits (include/tb.h,
 // TB_INT4), and its codes: a group of LANES = D / 8 consecutive lanes holds a
 // position, 8 channels a lane, in 64 bits, or in 32 if they are exact there.
-// Scale and offset are found in 64: they round what has 24 bits or more to 11,
-// and by 32 some rows of 65536 would get another scale, and with it other values
-// in every channel.  A code is found in 32 bits, as x / scale + away with away =
-// -offset / scale: of a quotient that is at most 80, less than 2^-12 is lost, and of
-// away and of x / scale, which far from 0 are large and cancel, 2^-24 each.  Only
-// one that may be that near to the middle between two codes is looked at in 64.
+// All of it is found in 32 bits first.  Scale and offset round what has 24 bits
+// or more to 11: by 32 alone some rows of 65536 would get another scale, and with
+// it other values in every channel.  But rounding and clamping are monotone: where
+// both ends of the interval of what 32 bits may have lost give the same fp16, 64
+// give it too; where they do not, 64 decide.  A code is found as x / scale + away
+// with away = -offset / scale: of a quotient that is at most 80, less than 2^-15 is
+// lost, and of away and of x / scale, which far from 0 are large and cancel, 2^-24
+// each.  Only one that may be that near to the middle between two codes is
+// looked at in 64.
 struct Codes4 {
   uint32_t word;   // byte i: channels i (low) and i + 4 of the lane's eight
   uint32_t scale;  // fp16 bits: scale, and offset above it
 };
-constexpr double kLimit4 = 4096.0;
+constexpr float kLimit4 = 4096.f;
 
 __device__ __forceinline__ float least(float a, float b) { return __builtin_fminf(a, b); }
 __device__ __forceinline__ float most(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double least(double a, double b) { return __builtin_fmin(a, b); }
 __device__ __forceinline__ double most(double a, double b) { return __builtin_fmax(a, b); }
 
+// The least and the largest channel of the group, first limited.
 template <int LANES, typename F>
-__device__ __forceinline__ Codes4 codes4(F (&x)[8]) {
-  bool nan = false;
-  F lo = (F)kLimit4, hi = (F)-kLimit4;
+__device__ __forceinline__ void ends4(const F (&x)[8], F& lo, F& hi) {
+  lo = (F)kLimit4;
+  hi = -(F)kLimit4;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    nan = nan || x[e] != x[e];
-    x[e] = most(least(x[e], (F)kLimit4), (F)-kLimit4);
     lo = least(lo, x[e]);
     hi = most(hi, x[e]);
   }
@@ -74,26 +76,57 @@ __device__ __forceinline__ Codes4 codes4(F (&x)[8]) {
   join(xor_lane<2>(lo), xor_lane<2>(hi));
   join(xor_lane<4>(lo), xor_lane<4>(hi));
   if constexpr (LANES == 16) join(xor_lane<8>(lo), xor_lane<8>(hi));
+  lo = most(lo, -(F)kLimit4);
+  hi = least(hi, (F)kLimit4);
+}
+
+template <int LANES, typename F>
+__device__ __forceinline__ Codes4 codes4(const F (&x)[8]) {
+  bool nan = false;
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = (float)x[e];
+    nan = nan || y[e] != y[e];
+  }
+  float lo, hi;
+  ends4<LANES>(y, lo, hi);
+  // 2^-21 is several times what the operations here lose, 2^-24 of the larger end
+  // what x did on its way to 32 bits
+  const float narrow = sizeof(F) == 4 ? 0.f : most(fabsf(lo), fabsf(hi)) * 0x1p-24f;
+  const float step = (hi - lo) * (1.f / 15.f), step_off = __builtin_fmaf(step, 0x1p-21f, narrow * 0.14f);
+  _Float16 sh = (_Float16)(step - step_off);
+  const float low = __builtin_fmaf(-64.f, (float)sh, lo), low_off = __builtin_fmaf(fabsf(low), 0x1p-21f, narrow);
+  _Float16 oh = (_Float16)(low - low_off);
+  const bool sure = !nan && sh > (_Float16)0.f && sh == (_Float16)(step + step_off) && oh == (_Float16)(low + low_off) &&
+                    oh != (_Float16)0.f;
   const int lane = threadIdx.x & 63;
   const uint64_t group = ((uint64_t)1 << LANES) - 1;
-  Codes4 r{0u, 0x7e007e00u};
-  if ((__ballot(nan) >> (lane & ~(LANES - 1)) & group) != 0) return r;
-  const _Float16 sh = (_Float16)(((double)hi - (double)lo) / 15.0);
-  const double s = (double)sh;
-  const _Float16 oh = (_Float16)((double)lo - 64.0 * s);
+  if ((__ballot(!sure) >> (lane & ~(LANES - 1)) & group) != 0) {
+    if ((__ballot(nan) >> (lane & ~(LANES - 1)) & group) != 0) return Codes4{0u, 0x7e007e00u};
+    F l, h;
+    ends4<LANES>(x, l, h);
+    sh = (_Float16)(((double)h - (double)l) / 15.0);
+    oh = (_Float16)((double)l - 64.0 * (double)sh);
+  }
+  Codes4 r;
+  r.word = 0u;
   r.scale = (uint32_t)__builtin_bit_cast(uint16_t, sh) | (uint32_t)__builtin_bit_cast(uint16_t, oh) << 16;
-  if (!(s > 0.0)) return r;
+  if (!(sh > (_Float16)0.f)) return r;
   const float inverse = 1.f / (float)sh, away = -(float)oh * inverse;
   float n[8], far = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float q = __builtin_fmaf((float)x[e], inverse, away);
+    const float q = __builtin_fmaf(most(least(y[e], kLimit4), -kLimit4), inverse, away);
     n[e] = __builtin_rintf(q);
     far = __builtin_fmaxf(far, fabsf(q - n[e]));
   }
-  if (far > 0.5f - __builtin_fmaf(fabsf(away), 0x1p-22f, 0x1p-12f)) {
+  if (far > 0.5f - __builtin_fmaf(fabsf(away), 0x1p-22f, 0x1p-15f)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) n[e] = (float)__builtin_rint(((double)x[e] - (double)oh) / s);
+    for (int e = 0; e < 8; ++e) {
+      const double limited = most(least((double)x[e], (double)kLimit4), -(double)kLimit4);
+      n[e] = (float)__builtin_rint((limited - (double)oh) / (double)sh);
+    }
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)

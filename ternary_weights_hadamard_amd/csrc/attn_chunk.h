@@ -26,7 +26,7 @@
 // 540 us, in pages of 16 602 us.  2 x 777 tokens over 6000 in a window of 1000,
 // 16 heads of 64 in e4m3: 35.3 us.  4-bit codes are widened to fp16 on their way
 // into LDS: a quarter of the vector operations, and not between the products,
-// where no registers are left for it (11 spilled, 613 us): 584 us, 821 TFLOP/s; in
+// where no registers are left for it (11 spilled, 613 us): 584 to 602 us, 795 to 821 TFLOP/s; in
 // the window 38.1 us.
 #pragma once
 

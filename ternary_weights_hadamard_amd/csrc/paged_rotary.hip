@@ -16,10 +16,14 @@
 // 3.8 us; 16 of 40 + 8 into 4 bits 6.6 us).  A chunk into bf16 or e4m3: HBM (4 x up to
 // 2048 tokens of 40 + 8 heads, 106 MB in 23.9 us, 4.4 TB/s; a plain copy moves
 // 5.2).  A chunk into 4 bits with transforms (40 + 8 heads, 103 MB in 41 us): the
-// vector unit, whose 64-bit operations find the scales and offsets of K and V;
-// the queries' transforms are matrix products there (run_queries_turned: 60 -> 48
-// us together with codes found in 32 bits) and keys, the longest, come first with
-// 4 heads a workgroup (48 -> 41; 2 and 8 heads were slower).
+// vector unit, for the transforms of the queries (40 heads and 8 in bf16: 36 us with
+// them, 26 without) and the 64-bit ones of K and V (alone 24 us, in bf16 18).  The
+// queries' are matrix products there (run_queries_turned: 60 -> 48 us together
+// with codes found in 32 bits), keys, the longest, come first with 4 heads a
+// workgroup (48 -> 42; 2 and 8 heads were slower), and scales and offsets are found
+// in 32 bits where 64 would not change them (42.1 -> 40.9; K and V alone 27.5 -> 24.4).
+// With the transforms of K and V in 32 bits too, and again in 64 where a code may
+// depend on it, the angles of the rare path took registers: 54 to 58 us.
 #include "append_ops.h"
 #include "fwht_lanes.h"
 #include "paged.h"

@@ -169,6 +169,14 @@ def test_codes_far_from_zero(lens):
     r.check(r.run())
 
 
+@pytest.mark.parametrize("turn", [(True, True, True), (False, False, False)])
+def test_codes_of_many_rows(turn):
+    """Enough rows that some scales and offsets lie next to where fp16 rounds."""
+    say(f"many rows {turn}")
+    r = Rotary([(600, 700), (500, 500)], 2, 16, 128, 64, "int4", 128, turn=turn, seed=12)
+    r.check(r.run())
+
+
 def test_without_queries_and_in_place():
     say("rotary without queries")
     for lens in ([(3, 30)], [(40, 60)]):
